@@ -15,6 +15,13 @@ API (flash_qla 0.1.2 README, "Usage / High-level API" and "Low-level API"):
     dq, dk, dv, db, dg, dh0 = chunk_gated_delta_rule_bwd(q, k, v, g_cum, beta,
         A, do, dht=None, scale=None, initial_state=None, cu_seqlens=None)
 
+the decoding calls that follow a prefill (``decode.py``):
+
+    o = recurrent_gated_delta_rule(q, k, v, g, beta, state, ...)        # state pool moved in place
+    o = tree_gated_delta_rule(q, k, v, g, beta, parents, state, ...)    # drafted tokens, state kept
+    scores, tokens, parents = beam_search_step(logits, scores, ...)
+    reorder_states(states, parents, ...)
+
 plus the save-for-backward pair that training through ``chunk_gated_delta_rule`` uses (the forward
 keeps its operand images and chunk-entry states; the backward skips its recompute passes):
 
@@ -34,7 +41,8 @@ from . import build as _build
 
 __all__ = ["chunk_gated_delta_rule", "chunk_gated_delta_rule_fwd", "chunk_gated_delta_rule_bwd",
            "chunk_gated_delta_rule_fwd_saved", "chunk_gated_delta_rule_bwd_saved", "SavedForward",
-           "cp_plan", "cp_trigger", "GdnError", "load_library", "library_path", "workspace_bytes", "CHUNK"]
+           "cp_plan", "cp_trigger", "GdnError", "load_library", "library_path", "workspace_bytes", "CHUNK",
+           "recurrent_gated_delta_rule", "tree_gated_delta_rule", "beam_search_step", "reorder_states"]
 
 CHUNK = 64
 GDN_F32, GDN_BF16 = 0, 1
@@ -362,3 +370,7 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None,
     o, ht = _GdnFunction.apply(q, k, v, g, beta, scale, initial_state, bool(output_final_state),
                                cu_seqlens)
     return o, (ht if output_final_state else None)
+
+
+from .decode import (beam_search_step, recurrent_gated_delta_rule, reorder_states,  # noqa: E402
+                     tree_gated_delta_rule)

@@ -273,6 +273,127 @@ int gdn_profile_read(char *names, int name_stride, int *counts, double *ms, int 
 const char *gdn_version(void);
 
 /*
+ * ---- Decoding ----
+ *
+ * Entry points for a model that generates: the state that gdn_fwd left
+ * (final_state) is kept in a pool of slots and moved token by token.  They
+ * need no workspace (but for gdn_beam_search) and read no offsets on the host,
+ * so they can be captured in a CUDA graph.
+ *
+ * What a call cannot check on the host, because the numbers are on the device,
+ * is checked by the kernels and never reaches memory out of range:
+ *   - a state index below 0 marks an idle row: its outputs are 0, no slot is
+ *     read or written;
+ *   - a state index of n_slots or more, a token index of T or more, or a
+ *     parent that is not an earlier node makes the row's outputs from there on
+ *     NaN and leaves its slot as it was.
+ */
+typedef struct {
+    int64_t batch, token, head; /* in elements; the innermost dimension is contiguous */
+} gdn_strides;
+
+typedef struct {
+    int64_t B, T, Hq, Hv, K, V;    /* K, V in {64, 128}; Hv % Hq == 0                       */
+    gdn_strides q, k, v, g, beta;  /* q, k [B,T,Hq,K]; v [B,T,Hv,V]; g, beta [B,T,Hv]       */
+    gdn_dtype io_dtype;            /* dtype of q, k, v, o; g and beta are fp32              */
+    float scale;
+    int64_t n_slots, slot_stride;  /* state: [n_slots] of [Hv,K,V] fp32, slot_stride floats
+                                      apart (a multiple of 4)                               */
+    const int32_t *state_indices;  /* device [n_seqs] or NULL: row n has slot n             */
+    int64_t n_seqs;                /* = B, or number of sequences when varlen               */
+    const int32_t *cu_seqlens;     /* device [n_seqs + 1] or NULL; requires B == 1          */
+    const int32_t *token_indices;  /* device [n_seqs, n_steps] or NULL, see gdn_recurrent   */
+    int64_t n_steps;
+} gdn_decode_problem;
+
+/*
+ * The recurrence itself, token by token:
+ *     S_t = exp(g_t) S_{t-1} + k_t (beta_t (v_t - exp(g_t) S_{t-1}^T k_t))^T,  o_t = scale S_t^T q_t
+ * for every row (sequence) over its T tokens, in fp32.  It reads and writes
+ * each state once; meant for one to about sixteen tokens (above that gdn_fwd
+ * is faster) and right for any number.
+ *   state     [n_slots, Hv, K, V] fp32, updated in place at the row's slot.  The
+ *             slots of one call must differ from each other.
+ *   out_state nullable [n_seqs, Hv, K, V] fp32 contiguous: row n's new state goes
+ *             there instead and `state` is only read (slots may then repeat).
+ *             Must not overlap `state`.
+ *   token_indices: row n runs through its tokens token_indices[n][0], [1], ... up
+ *             to the first negative entry instead of 0 .. T-1: the accepted path
+ *             of a drafted tree, or rows of different lengths.  Not with
+ *             cu_seqlens.
+ *   o         [B, T, Hv, V] contiguous, or [B, n_steps, Hv, V] with token_indices
+ *             (0 past a row's end).  q and o may both be NULL: only the states
+ *             move.  With cu_seqlens, rows of o outside every sequence are not
+ *             written.
+ */
+gdn_status gdn_recurrent(const gdn_decode_problem *p, const void *q, const void *k, const void *v,
+                         const float *g, const float *beta, float *state, float *out_state, void *o,
+                         gdn_stream_t stream);
+
+/*
+ * A tree of drafted tokens over a state: node t of row n is the token that
+ * follows the tokens on the path from the state down to its parent,
+ *     o_t = scale S_t^T q_t,  S_t = (the recurrence's step from S_parent(t)),
+ * and the state itself stays as it was.  parents [B, T] (device, contiguous):
+ * an earlier node of the row, or -1 for a child of the state; below -1 the
+ * node is absent, and with it what hangs under it (o = 0).  T <= GDN_TREE_MAX.
+ * After acceptance, gdn_recurrent with token_indices = the accepted path moves
+ * the state.  cu_seqlens and token_indices must be NULL.
+ */
+#define GDN_TREE_MAX 64
+gdn_status gdn_tree(const gdn_decode_problem *p, const void *q, const void *k, const void *v,
+                    const float *g, const float *beta, const int32_t *parents, const float *state, void *o,
+                    gdn_stream_t stream);
+
+/*
+ * One selection of a beam search.  With lse_w the logarithm of the sum of the
+ * exponentials of beam w's allowed logits, candidate (w, token) has the score
+ *     scores[w] + (logits[w][token] - lse_w),
+ * and a finished beam has itself, with its score, as its only candidate.  The
+ * n best candidates of each of the B searches come out in descending order,
+ * equal ones by the lower w * vocab + token (a finished beam counts as its
+ * token 0).  A logit of -inf, one whose mask byte is 0 (whatever it holds) and
+ * any candidate whose score is not above -inf are never chosen; a beam with a
+ * NaN or +inf among its allowed logits has no candidates.  Where fewer than n
+ * are left the score is -inf, the token -1 and the parent j % W for place j.
+ * The token of a finished beam is -1.
+ */
+typedef struct {
+    int64_t B, W, vocab, n;                 /* 1 <= W, n <= GDN_BEAM_MAX; vocab <= GDN_BEAM_VOCAB_MAX */
+    int64_t logits_batch, logits_beam;      /* strides in elements; the vocabulary is contiguous */
+    int64_t mask_batch, mask_beam;          /* strides in bytes, 0 to share                      */
+    gdn_dtype logits_dtype;
+} gdn_beam_problem;
+#define GDN_BEAM_MAX 64
+#define GDN_BEAM_VOCAB_MAX (1 << 20)
+
+/* Bytes of device workspace (0 on a bad problem), 256-byte aligned. */
+size_t gdn_beam_search_workspace_bytes(const gdn_beam_problem *p);
+/* scores [B, W] fp32, finished [B, W] bytes (nullable), mask bytes (nullable) -> out_scores fp32, out_tokens,
+ * out_parents int32, all [B, n] contiguous. */
+gdn_status gdn_beam_search(const gdn_beam_problem *p, const void *logits, const float *scores,
+                           const uint8_t *finished, const uint8_t *mask, float *out_scores, int32_t *out_tokens,
+                           int32_t *out_parents, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * The beams' states follow a selection, in place: with slot(b, i) =
+ * state_indices[b * W + i] (NULL: b * W + i), for every view at once
+ *     new[slot(b, i)] = old[slot(b, parents[b * W + i])]
+ * Each source is read and each moved slot is written once; nothing is staged.
+ * A view is one tensor of n_slots slots of slot_bytes bytes, slot_stride bytes
+ * apart.  The slots of one call must differ from each other and the views must
+ * not overlap.  A negative parent leaves the slot as it is; one of W or more,
+ * or one whose slot is not in the pool, fills it with 0xFF bytes (NaN).
+ * Views are read on the host during the call.
+ */
+typedef struct {
+    void *data;
+    int64_t slot_stride, slot_bytes;
+} gdn_state_view;
+gdn_status gdn_reorder_states(const gdn_state_view *views, int64_t n_views, int64_t n_slots, int64_t B, int64_t W,
+                              const int32_t *parents, const int32_t *state_indices, gdn_stream_t stream);
+
+/*
  * Test aid for the bounded device-side waits (process-wide; set it only while
  * no other thread calls the library).  Problems planned after this call use
  * wait_ns as the limit of every mbarrier wait of the forward's state-chain
