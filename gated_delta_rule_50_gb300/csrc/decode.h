@@ -24,6 +24,8 @@ struct DecodeArgs {
 cudaError_t launch_recurrent(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st);
 cudaError_t launch_tree(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st);
 
+cudaError_t launch_tree_tc(const DecodeArgs &a, int K, cudaStream_t st);  // bf16 io
+
 struct BeamArgs {
     const void *logits;
     const float *scores;

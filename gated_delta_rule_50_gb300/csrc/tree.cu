@@ -6,6 +6,7 @@
 //     o_t = scale (Gam_t S^T q_t + sum_{i in anc(t)} P_ti d_i),                  P_ti = D_ti (q_t . k_i)
 // which is the recurrence along every path at once: no node needs a state of its own.  D is built by products
 // down the tree (D_ti = e^{g_t} D_parent(t),i), so a gate of -inf stays 0 and nothing is a difference of sums.
+// This file holds the CUDA-core kernel, for fp32 io; tree_tc.cu has the tensor-core kernel for bf16.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -130,6 +131,7 @@ template <int K, typename IO> __global__ void __launch_bounds__(128) k_tree(cons
             y = fmaf(lp.y, di, y);
         }
         y = fmaf(s_lp[t * T + t].y, d, y);
+        if ((bad | absent) >> t & 1) d = 0.f;  // whatever the node holds: nobody sees it
         s_d[t * V + col] = d;  // read by this lane alone
         const float out = (bad >> t & 1) ? __int_as_float(0x7fffffff) : (absent >> t & 1) ? 0.f : a.scale * y;
         o[t * o_tok + col] = from_f<IO>(out);
@@ -148,7 +150,7 @@ template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream
 }  // namespace
 
 cudaError_t launch_tree(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st) {
-    if (io == GDN_BF16) return K == 128 ? launch<128, __nv_bfloat16>(a, st) : launch<64, __nv_bfloat16>(a, st);
+    if (io == GDN_BF16) return launch_tree_tc(a, K, st);
     return K == 128 ? launch<128, float>(a, st) : launch<64, float>(a, st);
 }
 

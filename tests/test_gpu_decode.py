@@ -303,7 +303,7 @@ def tree_reference(x, parents, h0):
         after = {-1: h0[b].double()}
         for t in range(T):
             p = int(parents[b, t])
-            if p not in after:
+            if p not in after:  # absent, or under such a node
                 continue
             S = after[p] * torch.exp(g[b, t])[:, None, None]
             d = beta[b, t][:, None] * (v[b, t] - torch.einsum("hkv,hk->hv", S, k[b, t]))
@@ -352,6 +352,9 @@ def test_tree_shapes(shape, dtype):
         parents = random_parents(B, T, 2)
         parents[:, 5], parents[:, 11], parents[1, 0] = -2, -7, -2
         parents[:, 12], parents[:, 40] = 11, 12
+        for name in ("q", "k", "v", "g", "beta"):  # what an absent node holds reaches nobody
+            x[name][:, [5, 11]] = math.nan
+            x[name][1, 0] = math.inf
     state = x["state"].cuda()
     o = gdn.tree_gated_delta_rule(*args(x), parents.cuda(), state, state_indices=x["idx"].cuda())
     ref = tree_reference(x, parents, x["state"][x["idx"].long()])
