@@ -36,7 +36,7 @@ gdn_status decode_args(const gdn_decode_problem *p, const void *q, const void *k
     const unsigned elem = p->io_dtype == GDN_BF16 ? 2 : 4;
     if (!none && tokens && (!k || !v || !g || !beta)) return GDN_ERR_INVALID_ARG;
     if (!none && p->n_slots > 0 && !state) return GDN_ERR_INVALID_ARG;
-    if (!aligned(q, elem) || !aligned(k, elem) || !aligned(v, elem) || !aligned(o, elem) || !aligned(g, 4) ||
+    if (!aligned(q, elem) || !aligned(k, elem) || !aligned(v, elem) || !aligned(o, 16) || !aligned(g, 4) ||
         !aligned(beta, 4) || !aligned(state, 16) || !aligned(p->state_indices, 4) || !aligned(p->cu_seqlens, 4) ||
         !aligned(p->token_indices, 4))
         return GDN_ERR_INVALID_ARG;

@@ -1,17 +1,21 @@
-// tree_tc.cu -- the drafted-tree operator on the tensor cores (bf16 io).  The mathematics is in tree.cu; here
-// one CTA of 128 threads computes a (row, value head) with thread v = TMEM lane v = value column v:
+// tree_tc.cu -- the drafted-tree operator on the tensor cores (bf16 io).  The mathematics is in tree.cu, here as
 //
-//   G  = [K; Q] K^T                (operands in shared memory)       lane r: row r of K K^T, then of Q K^T
-//   D1 = S^T [K; Q]^T              (S^T from TMEM, hi + lo)          lane v: S^T k_t, then S^T q_t, of column v
-//   d  = (I + L)^-1 R              forward substitution, a column per thread, all of it in registers
-//   D2 = d^T P^T                   (d^T from TMEM, hi + lo)          lane v: sum_i P_ti d_i of column v
-//   o_t = scale (Gam_t D1_q + D2)
+//   o_t = scale (Gam_t S^T q_t + sum_i W_ti R_i),  R_i = beta_i (v_i - Gam_i S^T k_i),  W = P (I + L)^-1
 //
-// q and k are bf16 as given; S, P and d enter as hi + lo bf16 pairs (16 bits; one bf16 rounding of them would
-// cost as much as the rounding of o).  L stays in fp32: the substitution multiplies it by unrounded d.
-// S arrives by one bulk copy (a head's state is contiguous) while q, k and G are made, and goes to TMEM; its
-// place in shared memory then holds L and P.  Two CTAs fit on an SM (100 KB, 256 TMEM columns), so that one's
-// copies run under the other's arithmetic.
+// because W needs no state: it is made while the state is on its way.  One CTA computes a (row, value head):
+//
+//   all warps     rows of k and q into shared memory
+//   group B       G = [K; Q] K^T (lane r: row r of K K^T, then of Q K^T); the products of e^g down the tree; L and
+//                 P; W by blocks of 16 columns from the last on, W_b = (P_b - sum_{c > b} W_c L_cb) (I + L_bb)^-1,
+//                 16 rows per warp on fragments that stay in registers
+//   group A       S^T from its bulk copy to TMEM; D1 = S^T [K; Q]^T (lane v: S^T k_t, then S^T q_t, of column v);
+//                 R^T to TMEM
+//   all warps     D2 = R^T W^T (lane v: sum_i W_ti R_i of column v); o
+//
+// q and k are bf16 as given; S, R, L, P and W enter products as hi + lo bf16 pairs (16 bits; one bf16 rounding of
+// them would cost as much as the rounding of o) and are kept in fp32 between them.
+// S arrives by one bulk copy (a head's state is contiguous); its place in shared memory then holds L, P, W and o.
+// Two CTAs fit on an SM (107 KB, 256 TMEM columns each), so that one's copies run under the other's arithmetic.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -23,264 +27,450 @@ namespace {
 
 using namespace tc;
 
-constexpr int NT = 128;
+constexpr int GROUP = 128, NT = 2 * GROUP;
 constexpr uint32_t kBlock = 16384;  // 128 rows of 64 bf16: one K block of [K; Q]
-constexpr uint32_t kCols = 256;     // TMEM: S^T hi, lo (K columns; later d^T hi, lo and D2) | D1 from column 128
-constexpr uint32_t kD1 = 128, kD2 = 64, kDlo = 32;
+constexpr uint32_t kCols = 256;     // TMEM: S^T hi, lo (K columns), later R^T hi, lo and D2 | G, later D1
+constexpr uint32_t kRlo = 32, kD2 = 64, kD1 = 128;
+enum { BAR_S = 0, BAR_G = 8, BAR_D = 16, BAR_O = 24 };  // mbarriers: the state, G, D1, D2
+enum { NB_STATE = 1, NB_B = 2, NB_FREE = 3, NB_A = 4, NB_OUT = 5 };  // named barriers
 
 template <int K, int TP> struct Map {
-    static constexpr uint32_t LS = TP + 4;  // L begins at 0, its row stride: 16-byte rows, eight neighbours on different banks
-    static constexpr uint32_t PHI = (2 * TP * LS * 4 + 1023) / 1024 * 1024, PLO = PHI + TP * 128;
-    static constexpr uint32_t scratch = PLO + TP * 128, state = K * 128 * 4;
+    // over the state once it is in TMEM: P in fp32, then row by row W (eight rows of hi, then of lo, in the place of
+    // eight of P), then o; L hi and lo; the blocks of L on the diagonal in fp32, by columns; their inverses; v
+    static constexpr uint32_t PW = 0, LHI = TP * 256, LLO = LHI + TP * 128, DIAG = LLO + TP * 128, DS = 20;
+    static constexpr uint32_t INV = DIAG + TP * DS * 4, INV_BLOCK = 16 * 48;  // hi, then lo; rows of 48 bytes
+    static constexpr uint32_t V = INV + TP / 16 * 2 * INV_BLOCK, scratch = V + TP * 256, state = K * 128 * 4;
     static constexpr uint32_t KQ = ((scratch > state ? scratch : state) + 1023) / 1024 * 1024;
-    static constexpr uint32_t VEC = KQ + K / 64 * kBlock;  // a, beta, Gam, parent, what the node is: TP each
+    // the products of e^g from node i to node t >= i: rows t and TP - 1 - t share one (see table_row); the stride
+    // puts eight neighbouring rows on different banks
+    static constexpr uint32_t TABLE = KQ + K / 64 * kBlock, LS = TP + 4;
+    static constexpr uint32_t VEC = TABLE + TP / 2 * LS * 4;  // (a, parent), beta, beta Gam, scale Gam: TP each
     static constexpr uint32_t BAR = VEC + 5 * TP * 4;
-    static constexpr uint32_t bytes = BAR + 32 + 1024;
+    static constexpr uint32_t MISC = BAR + 32;
+    static constexpr uint32_t bytes = MISC + 32 + 1024;
 };
+
+// Where row t of the table begins: the first half of the rows at 0, with entries up to t at most; the others
+// behind those of their partner TP - 1 - t, on a 16-byte boundary.
+template <int TP> __host__ __device__ constexpr int table_row(int t) {
+    return t < TP / 2 ? t * (TP + 4) : (TP - 1 - t) * (TP + 4) + ((TP - 1 - t + 4) & ~3);
+}
 
 __device__ __forceinline__ uint64_t kdesc(uint32_t a) { return sdesc_sw128(a, 16, 1024); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void bar_arrive(uint32_t id, uint32_t threads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// 16 bytes to shared memory, zeros where there is no source row
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copy_piece(uint32_t dst, const __nv_bfloat16 *src, bool in) {  // any alignment
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (in)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (uint32_t)__bfloat16_as_ushort(src[2 * i]) | (uint32_t)__bfloat16_as_ushort(src[2 * i + 1]) << 16;
+    st_shared_v4(dst, w[0], w[1], w[2], w[3]);
+}
+// Fragments of 16 x 16 blocks: C as two 16 x 8 accumulators, A as hi and lo of four registers each.
+struct Frag {
+    uint32_t hi[4], lo[4];
+};
+__device__ __forceinline__ Frag split_frag(const float (&c)[8], bool negate) {  // C of a product -> A of the next
+    Frag f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_pair(c[2 * i], c[2 * i + 1], f.hi[i], f.lo[i]);
+    if (negate)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.hi[i] ^= 0x80008000u, f.lo[i] ^= 0x80008000u;
+    return f;
+}
+__device__ __forceinline__ void mma16816(float *c, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c += a B for a 16 x 16 block B [k][n] of bf16 hi and lo in shared memory; each lane gives the address of its row
+__device__ __forceinline__ void block_product(float (&c)[8], const Frag &a, uint32_t b_hi, uint32_t b_lo) {
+    uint32_t h[4], l[4];
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+                 : "r"(b_hi)
+                 : "memory");
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(l[0]), "=r"(l[1]), "=r"(l[2]), "=r"(l[3])
+                 : "r"(b_lo)
+                 : "memory");
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        mma16816(c + 4 * j, a.hi, h[2 * j], h[2 * j + 1]);
+        mma16816(c + 4 * j, a.lo, h[2 * j], h[2 * j + 1]);
+        mma16816(c + 4 * j, a.hi, l[2 * j], l[2 * j + 1]);
+    }
 }
 
 template <int K, int TP>
 __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec) {
     using M = Map<K, TP>;
-    constexpr int LS = M::LS;
-    constexpr uint32_t ID_G = idesc_bf16(128, TP, 0, 0), ID_S = idesc_bf16(128, 2 * TP, 0, 0);
+    constexpr uint32_t ID_1 = idesc_bf16(128, TP, 0, 0), ID_2 = idesc_bf16(128, 2 * TP, 0, 0);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_align1024(smem_raw);
-    const uint32_t sb = smem_u32(sm);
-    const int t = threadIdx.x, warp = t >> 5, T = a.T, V = a.V;
-    const int n = blockIdx.x / a.Hv, h = blockIdx.x - n * a.Hv, hq = h / a.G;
+    const uint32_t sb = smem_u32(sm), bars = sb + M::BAR;
+    const int t = threadIdx.x, warp = t >> 5, T = a.T, V = a.V, lane_row = t & (GROUP - 1);
+    const int n = blockIdx.x, hq = blockIdx.y, h = hq * a.G + blockIdx.z;
     const float nan = __int_as_float(0x7fffffff);
-    const bool mine = t < V;  // this thread has a value column (the same for a whole warp)
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)n * T * a.Hv + h) * V + t;
+    constexpr int SETUP = 7;  // the warp that sets up, and issues G
+    const bool group_b = t >= GROUP, column = lane_row < V;  // the same for a whole warp
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)n * T * a.Hv + h) * V;
     const int64_t o_tok = (int64_t)a.Hv * V;
 
     const int64_t slot = a.state_indices ? a.state_indices[n] : n;
-    if (slot < 0 || slot >= a.n_slots) {
-        if (mine)
-            for (int i = 0; i < T; ++i) o[i * o_tok] = __float2bfloat16_rn(slot < 0 ? 0.f : nan);
-        return;
-    }
-    float *s_a = reinterpret_cast<float *>(sm + M::VEC), *s_b = s_a + TP, *s_gam = s_b + TP;
-    int *s_par = reinterpret_cast<int *>(s_gam + TP), *s_kind = s_par + TP;  // kind: 0 a node, 1 absent, 2 no such parent
-    uint32_t *misc = reinterpret_cast<uint32_t *>(sm + M::BAR + 16);
+    int2 *s_up = reinterpret_cast<int2 *>(sm + M::VEC);  // e^g (its bits) and the parent
+    float *s_b = reinterpret_cast<float *>(s_up + TP), *s_bg = s_b + TP, *s_sg = s_bg + TP;
+    float *table = reinterpret_cast<float *>(sm + M::TABLE);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(sm + M::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
-    const uint32_t bar_s = sb + M::BAR, bar_m = bar_s + 8;
-    if (t == 0) {
-        mbar_init(bar_s, 1);
-        mbar_init(bar_m, 1);
-        misc[1] = 0;
-        fence_mbar_init();
-        const uint32_t bytes = (uint32_t)(K * V * 4);
-        mbar_arrive_expect_tx(bar_s, bytes);
-        bulk_load(sb, a.state + slot * a.slot_stride + (int64_t)h * K * V, bytes, bar_s);
+    uint32_t *s_absent = misc + 2, *s_bad = misc + 4;  // nodes of each kind, a bit each
+    const bool live = slot >= 0 && slot < a.n_slots;
+    if (warp == SETUP && live) {
+        if (t == 32 * SETUP) {
+            for (int i = 0; i < 4; ++i) mbar_init(bars + 8 * i, 1);
+            for (int i = 1; i < 6; ++i) misc[i] = 0;
+            fence_mbar_init();
+            const uint32_t bytes = (uint32_t)(K * V * 4);
+            mbar_arrive_expect_tx(bars + BAR_S, bytes);
+            bulk_load(sb, a.state + slot * a.slot_stride + (int64_t)h * K * V, bytes, bars + BAR_S);
+        }
+        __syncwarp();
+        tmem_alloc(sb + M::MISC, kCols);
     }
-    if (warp == 0) tmem_alloc(sb + M::BAR + 16, kCols);
-
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + n * a.sq.batch + hq * a.sq.head;
-    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + n * a.sk.batch + hq * a.sk.head;
-    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + n * a.sv.batch + h * a.sv.head + t;
-    for (int e = t; e < 2 * T * (K / 8); e += NT) {  // 16-byte pieces of the rows of k, then of q
-        const int row = e / (K / 8), x = e % (K / 8);
-        const bool is_q = row >= T;
-        const int tok = is_q ? row - T : row;
-        const __nv_bfloat16 *src = is_q ? q + tok * a.sq.token : k + tok * a.sk.token;
-        const uint32_t dst = sw128_addr(sb + M::KQ + (x >> 3) * kBlock, is_q ? TP + tok : tok, x & 7);
+    {  // rows of k and q, 16 bytes per thread, a multiple of eight rows at a time
+        constexpr int PIECES = K / 8, ROWS = NT / PIECES;
+        const int x = t % PIECES, r0 = t / PIECES;
+        const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + n * a.sk.batch + hq * a.sk.head + 8 * x;
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + n * a.sq.batch + hq * a.sq.head + 8 * x;
+        const uint32_t dst = sw128_addr(sb + M::KQ + (x >> 3) * kBlock, r0, x & 7);
         if (vec) {
-            cp_async16(dst, src + 8 * x);
-        } else {
-            uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = (uint32_t)__bfloat16_as_ushort(src[8 * x + 2 * i]) | (uint32_t)__bfloat16_as_ushort(src[8 * x + 2 * i + 1]) << 16;
-            st_shared_v4(dst, w[0], w[1], w[2], w[3]);
+            for (int r = 0; r < TP; r += ROWS) {
+                if (r0 + r >= TP) break;
+                const bool in = r0 + r < T;
+                cp_async16(dst + r * 128, in ? k + (r0 + r) * a.sk.token : k, in);
+                cp_async16(dst + (TP + r) * 128, in ? q + (r0 + r) * a.sq.token : q, in);
+            }
+        } else {
+#pragma unroll 1
+            for (int r = 0; r0 + r < TP; r += ROWS) {
+                copy_piece(dst + r * 128, k + (r0 + r) * a.sk.token, r0 + r < T);
+                copy_piece(dst + (TP + r) * 128, q + (r0 + r) * a.sq.token, r0 + r < T);
+            }
         }
     }
-    if (t < TP) {
-        const bool in = t < T;
-        s_a[t] = in ? expf(a.g[n * a.sg.batch + h * a.sg.head + t * a.sg.token]) : 0.f;
-        s_b[t] = in ? a.beta[n * a.sb.batch + h * a.sb.head + t * a.sb.token] : 0.f;
-        s_par[t] = in ? a.parents[(int64_t)n * T + t] : -2;
+    float ga = 0.f, be = 0.f;
+    int up = -1;
+    if (t < T) {
+        ga = a.g[n * a.sg.batch + h * a.sg.head + t * a.sg.token];
+        be = a.beta[n * a.sb.batch + h * a.sb.head + t * a.sb.token];
+        up = a.parents[(int64_t)n * T + t];
     }
-    __nv_bfloat16 vr[TP];
-#pragma unroll
-    for (int i = 0; i < TP; ++i) vr[i] = mine && i < T ? v[i * a.sv.token] : __float2bfloat16_rn(0.f);
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!live) {
+        if (t < V)
+            for (int i = 0; i < T; ++i) o[i * o_tok + t] = __float2bfloat16_rn(slot < 0 ? 0.f : nan);
+        cp_async_wait();
+        return;
+    }
+    for (int e = t; e < TP / 2 * (int)M::LS / 4; e += NT) reinterpret_cast<float4 *>(table)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < TP) {
+        s_up[t] = make_int2(__float_as_int(expf(ga)), up);
+        s_b[t] = be;
+    }
+    cp_async_wait();
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc[0], lanes = (uint32_t)(32 * warp) << 16;
+    const uint32_t tmem = misc[0], lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     bool ok = true;
-
-    if (t == 0) {
-        for (int kb = 0; kb < K / 64; ++kb)
-            mma_chain<4, 2, 2>(tmem + kD1, kdesc(sb + M::KQ + kb * kBlock), kdesc(sb + M::KQ + kb * kBlock), ID_G, kb);
-        mma_commit(bar_m);
-    }
-    ok = mbar_wait_warp(bar_m, 0, abort_flag) && ok;
-    tc_fence_after();
-    uint32_t gram[TP];  // row t of K K^T, or row t - TP of Q K^T
-#pragma unroll
-    for (int c = 0; c < TP / 16; ++c) {
-        uint32_t r[16];
-        tmem_ld16(tmem + lanes + kD1 + 16 * c, r);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) gram[16 * c + i] = r[i];
-    }
-    ok = mbar_wait_warp(bar_s, 0, abort_flag) && ok;
-    if (mine) {
-        const float *s = reinterpret_cast<const float *>(sm) + t;
-#pragma unroll
-        for (int c = 0; c < K / 32; ++c) {
-            float x[32];
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = s[(32 * c + i) * V];
-            split_pack16(x, hi, lo);
-            tmem_st16x2(tmem + lanes + 16 * c, hi, tmem + lanes + K / 2 + 16 * c, lo);
-        }
-    }
-    tc_fence_before();
-    ok = __syncthreads_and(ok) != 0;
-    if (ok) {
-        tc_fence_after();
-        if (t == 0) {
-            for (int part = 0; part < 2; ++part)
+    if (group_b) {
+        if (warp == SETUP) {
+            if (t == 32 * SETUP) {
                 for (int kb = 0; kb < K / 64; ++kb)
-                    mma_chain_ta<4, 2>(tmem + kD1, tmem + part * (K / 2) + 32 * kb, kdesc(sb + M::KQ + kb * kBlock), ID_S,
-                                       part + kb);
-            mma_commit(bar_m);
+                    mma_chain<4, 2, 2>(tmem + kD1, kdesc(sb + M::KQ + kb * kBlock), kdesc(sb + M::KQ + kb * kBlock), ID_1, kb);
+                mma_commit(bars + BAR_G);
+            }
+            __syncwarp();
         }
-        // Meanwhile L and P, over the state's place: thread t walks from node t (or t - TP) up to the state and
-        // leaves the products of e^g on the way in its row.
-        float *row = reinterpret_cast<float *>(sm) + t * LS;
-        const int node = t < TP ? t : t - TP;
-        if (t < 2 * TP) {
-#pragma unroll
-            for (int i = 0; i < TP / 4; ++i) reinterpret_cast<float4 *>(row)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int row = lane_row, node = row < TP ? row : row - TP;
+        const bool has_row = row < 2 * TP, is_p = row >= TP;
+        float *mine = table + table_row<TP>(has_row ? node : 0);
+        if (row < TP) {  // from the node up to the state, leaving the products of e^g on the way
             float prod = 1.f;
             int p = node, kind = 0;
             while (p >= 0) {
-                row[p] = prod;
-                const int up = s_par[p];
-                if (up >= p || up < -1) {
-                    kind = up < -1 ? 1 : 2;
+                mine[p] = prod;
+                const int2 up = s_up[p];
+                if (up.y >= p || up.y < -1) {
+                    kind = up.y < -1 ? 1 : 2;
                     break;
                 }
-                prod *= s_a[p];
-                p = up;
+                prod *= __int_as_float(up.x);
+                p = up.y;
             }
-            if (t < TP) s_gam[t] = prod, s_kind[t] = kind;
-            const float b = t < TP ? s_b[node] : 1.f;
+            if (kind) {  // nothing of such a node is used, whatever it holds
+                for (int i = 0; i <= node; ++i) mine[i] = 0.f;
+                atomicOr(&(kind == 1 ? s_absent : s_bad)[node >> 5], 1u << (node & 31));
+            }
+            const float b = kind ? 0.f : s_b[node];
+            s_b[node] = b;
+            s_bg[node] = kind ? 0.f : b * prod;
+            s_sg[node] = kind ? 0.f : a.scale * prod;
+        }
+        ok = mbar_wait_warp(bars + BAR_G, 0, abort_flag);
+        tc_fence_after();
+        float x[TP];
+#pragma unroll
+        for (int c = 0; c < TP / 16; ++c) {
+            uint32_t r[16];
+            tmem_ld16(lanes + kD1 + 16 * c, r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[16 * c + i] = __uint_as_float(r[i]);
+        }
+        tc_fence_before();
+        bar_arrive(NB_STATE, NT);
+        named_bar(NB_B, GROUP);  // the products are there
+        const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
+        if (has_row) {
+            const float b = is_p ? 1.f : s_b[node];
+            const int last = is_p ? node : node - 1;  // P has its diagonal, L does not
+#pragma unroll
+            for (int c = 0; c < TP / 4; ++c) {
+                const float4 f = reinterpret_cast<const float4 *>(mine)[c];  // past the node: anything
+                const float d[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[4 * c + i] = 4 * c + i <= last ? b * d[i] * x[4 * c + i] : 0.f;
+                if (dead)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (d[i] == 0.f) x[4 * c + i] = 0.f;
+            }
+        }
+        named_bar(NB_FREE, NT);  // the state's place is free
+        if (has_row && is_p) {
+            float4 *p = reinterpret_cast<float4 *>(sm + M::PW + node * 256);
+#pragma unroll
+            for (int c = 0; c < TP / 4; ++c)
+                p[c ^ (node & 15)] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+        } else if (has_row) {
 #pragma unroll
             for (int c = 0; c < TP / 8; ++c) {
-                float x[8];
-                lds8f(row + 8 * c, x);
+                st_split_chunk(sb + M::LHI, sb + M::LLO, node, c, x + 8 * c);
+                if ((node >> 4) == (c >> 1)) {
+                    float *diag = reinterpret_cast<float *>(sm + M::DIAG) + ((node & ~15) + 8 * (c & 1)) * M::DS + (node & 15);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {  // what is not above the node may hold anything: selected, not multiplied
-                    const float w = __uint_as_float(gram[8 * c + i]);
-                    const bool above = x[i] != 0.f && kind == 0 && (t >= TP || 8 * c + i < node);
-                    x[i] = above ? b * x[i] * w : 0.f;
-                }
-                if (t < TP) {
-                    reinterpret_cast<float4 *>(row)[2 * c] = make_float4(x[0], x[1], x[2], x[3]);
-                    reinterpret_cast<float4 *>(row)[2 * c + 1] = make_float4(x[4], x[5], x[6], x[7]);
-                } else {
-                    st_split_chunk(sb + M::PHI, sb + M::PLO, node, c, x);
+                    for (int i = 0; i < 8; ++i) diag[i * M::DS] = x[8 * c + i];
                 }
             }
         }
-        fence_proxy_async_smem();
-        ok = mbar_wait_warp(bar_m, 1, abort_flag);
-        tc_fence_after();
-        ok = __syncthreads_and(ok) != 0;
-    }
-    float x[TP];
-    if (ok) {
-        if (mine) {
+        named_bar(NB_B, GROUP);
+        if (row >= GROUP - TP) {  // a column of an inverse per thread: a finished y_i at once into all rows below it
+            const int u = row - (GROUP - TP), j0 = u & 15;
+            const float *diag = reinterpret_cast<const float *>(sm + M::DIAG) + (u & ~15) * M::DS;
+            float y[16];
 #pragma unroll
-            for (int c = 0; c < TP / 16; ++c) {
-                uint32_t r[16];
-                tmem_ld16(tmem + lanes + kD1 + 16 * c, r);
+            for (int j = 0; j < 16; ++j) y[j] = j == j0 ? 1.f : 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = 16 * c + i;
-                    x[j] = s_kind[j] ? 0.f : s_b[j] * (__bfloat162float(vr[j]) - s_gam[j] * __uint_as_float(r[i]));
+            for (int i = 0; i < 15; ++i) {
+                float l[16];
+#pragma unroll
+                for (int j = (i + 1) / 4 * 4; j < 16; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(diag + i * M::DS + j);
+                    l[j] = f.x, l[j + 1] = f.y, l[j + 2] = f.z, l[j + 3] = f.w;
+                }
+#pragma unroll
+                for (int j = i + 1; j < 16; ++j) y[j] = fmaf(-l[j], y[i], y[j]);
+            }
+            unsigned char *inv = sm + M::INV + (u >> 4) * 2 * M::INV_BLOCK + 2 * j0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const __nv_bfloat16 hi = __float2bfloat16_rn(y[j]);
+                *reinterpret_cast<__nv_bfloat16 *>(inv + j * 48) = hi;
+                *reinterpret_cast<__nv_bfloat16 *>(inv + M::INV_BLOCK + j * 48) = __float2bfloat16_rn(y[j] - __bfloat162float(hi));
+            }
+        }
+        named_bar(NB_B, GROUP);
+        const int w = warp - 4, lane = t & 31;
+        if (16 * w < TP) {  // rows 16 w .. 16 w + 15 of W: blocks beyond the w-th are 0
+            const int g = lane >> 2, q2 = lane & 3;
+            float c[TP / 16][8];
+#pragma unroll
+            for (int b = 0; b < TP / 16; ++b)
+                if (b <= w)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // (rows g, g + 8) x (columns 2 q2, 2 q2 + 1 of each half)
+                        const int r = 16 * w + g + 8 * (i & 1), col = 16 * b + 8 * (i >> 1) + 2 * q2;
+                        const float2 f = *reinterpret_cast<const float2 *>(sm + M::PW + r * 256 + ((col >> 2) ^ (r & 15)) * 16 +
+                                                                           (col & 2) * 4);
+                        c[b][4 * (i >> 1) + 2 * (i & 1)] = f.x;
+                        c[b][4 * (i >> 1) + 2 * (i & 1) + 1] = f.y;
+                    }
+            __syncwarp();  // W takes the place of P's rows
+            // the row of a 16 x 16 block whose address this lane gives, and the half
+            const int br = (lane & 7) + (lane & 8), bh = lane >> 4;
+#pragma unroll
+            for (int b = TP / 16 - 1; b >= 0; --b) {
+                Frag f;
+                if (b <= w) {
+                    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    const uint32_t inv = sb + M::INV + b * 2 * M::INV_BLOCK + br * 48 + bh * 16;
+                    block_product(y, split_frag(c[b], false), inv, inv + M::INV_BLOCK);
+                    f = split_frag(y, false);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f.hi[i] = f.lo[i] = 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 16 * w + g + 8 * (i & 1);
+                    const uint32_t at = sb + M::PW + (r >> 3) * 2048 + (r & 7) * 128 + (((2 * b + (i >> 1)) ^ (r & 7)) << 4) + 4 * q2;
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(f.hi[i]) : "memory");
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024), "r"(f.lo[i]) : "memory");
+                }
+                if (b <= w) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f.hi[i] ^= 0x80008000u, f.lo[i] ^= 0x80008000u;
+#pragma unroll
+                    for (int e = 0; e < b; ++e)
+                        block_product(c[e], f, sw128_addr(sb + M::LHI, 16 * b + br, 2 * e + bh),
+                                      sw128_addr(sb + M::LLO, 16 * b + br, 2 * e + bh));
                 }
             }
-            // four rows at a time: what the rows before them give, then the triangle between the four
-            const float *L = reinterpret_cast<const float *>(sm);
+            fence_proxy_async_smem();
+        }
+    } else {
+        // v has its place once the state has left it; until then its lines come as far as L2
+        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + n * a.sv.batch + h * a.sv.head;
+        for (int e = t; e < T * V / 64; e += GROUP)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(v + (e >> (V == 128)) * a.sv.token + (V == 128 ? e & 1 : 0) * 64));
+        ok = mbar_wait_warp(bars + BAR_S, 0, abort_flag);
+        if (column) {
+            const float *s = reinterpret_cast<const float *>(sm) + t;
+#pragma unroll 1
+            for (int c = 0; c < K / 32; ++c) {
+                float y[32];
+                uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int j = 0; j < TP; j += 4) {
-                float acc[4] = {x[j], x[j + 1], x[j + 2], x[j + 3]};
-#pragma unroll
-                for (int i = 0; i < j; i += 4)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float4 l = *reinterpret_cast<const float4 *>(L + (j + r) * LS + i);
-                        acc[r] = fmaf(-l.x, x[i], acc[r]);
-                        acc[r] = fmaf(-l.y, x[i + 1], acc[r]);
-                        acc[r] = fmaf(-l.z, x[i + 2], acc[r]);
-                        acc[r] = fmaf(-l.w, x[i + 3], acc[r]);
-                    }
-                const float4 l1 = *reinterpret_cast<const float4 *>(L + (j + 1) * LS + j);
-                const float4 l2 = *reinterpret_cast<const float4 *>(L + (j + 2) * LS + j);
-                const float4 l3 = *reinterpret_cast<const float4 *>(L + (j + 3) * LS + j);
-                acc[1] = fmaf(-l1.x, acc[0], acc[1]);
-                acc[2] = fmaf(-l2.y, acc[1], fmaf(-l2.x, acc[0], acc[2]));
-                acc[3] = fmaf(-l3.z, acc[2], fmaf(-l3.y, acc[1], fmaf(-l3.x, acc[0], acc[3])));
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[j + r] = acc[r];
-            }
-#pragma unroll
-            for (int c = 0; c < TP / 16; ++c) {
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) split_pair(x[16 * c + 2 * i], x[16 * c + 2 * i + 1], hi[i], lo[i]);
-                tmem_st8x2(tmem + lanes + 8 * c, hi, tmem + lanes + kDlo + 8 * c, lo);
+                for (int i = 0; i < 32; ++i) y[i] = s[i * V];
+                s += 32 * V;
+                split_pack16(y, hi, lo);
+                tmem_st16x2(lanes + 16 * c, hi, lanes + K / 2 + 16 * c, lo);
             }
         }
         tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (t == 0) {
-            mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem, kdesc(sb + M::PHI), ID_G, 0);
-            mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem + kDlo, kdesc(sb + M::PHI), ID_G, 1);
-            mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem, kdesc(sb + M::PLO), ID_G, 1);
-            mma_commit(bar_m);
-        }
-        ok = mbar_wait_warp(bar_m, 0, abort_flag);
-        tc_fence_after();
-        if (mine && ok) {
-#pragma unroll
-            for (int c = 0; c < TP / 16; ++c) {
-                uint32_t sq[16], d2[16];
-                tmem_ld16x2(tmem + lanes + kD1 + TP + 16 * c, sq, tmem + lanes + kD2 + 16 * c, d2);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = 16 * c + i;
-                    const float y = a.scale * fmaf(s_gam[j], __uint_as_float(sq[i]), __uint_as_float(d2[i]));
-                    if (j < T) o[j * o_tok] = __float2bfloat16_rn(s_kind[j] == 0 ? y : s_kind[j] == 1 ? 0.f : nan);
-                }
+        bar_arrive(NB_FREE, NT);
+        named_bar(NB_STATE, NT);  // the state is in TMEM, G has been read
+        if (warp == 0) {
+            tc_fence_after();
+            if (t == 0) {
+                for (int part = 0; part < 2; ++part)
+                    for (int kb = 0; kb < K / 64; ++kb)
+                        mma_chain_ta<4, 2>(tmem + kD1, tmem + part * (K / 2) + 32 * kb, kdesc(sb + M::KQ + kb * kBlock), ID_2,
+                                           part + kb);
+                mma_commit(bars + BAR_D);
+            }
+            __syncwarp();
+        } else {
+            const int c = t & (V / 8 - 1);
+            const uint32_t dst = sb + M::V + 16 * c;
+            const int pieces = V == 128 ? 4 : 3, step = (GROUP - 32) >> pieces;
+            if (vec) {
+#pragma unroll 4
+                for (int r = (t - 32) >> pieces; r < T; r += step) cp_async16(dst + 2 * V * r, v + r * a.sv.token + 8 * c, true);
+            } else {
+#pragma unroll 1
+                for (int r = (t - 32) >> pieces; r < T; r += step) copy_piece(dst + 2 * V * r, v + r * a.sv.token + 8 * c, true);
             }
         }
+        cp_async_wait();
+        ok = mbar_wait_warp(bars + BAR_D, 0, abort_flag) && ok;
+        tc_fence_after();
+        named_bar(NB_A, GROUP);  // v is there
+        const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
+        const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sm + M::V) + t;
+        if (column)
+#pragma unroll 1
+            for (int c = 0; c < TP / 16; ++c) {
+                uint32_t ks[16], hi[8], lo[8];
+                float b[16], bg[16], y[16];
+                tmem_ld16(lanes + kD1 + 16 * c, ks);
+                lds16f(s_b + 16 * c, b);
+                lds16f(s_bg + 16 * c, bg);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    y[j] = fmaf(-bg[j], __uint_as_float(ks[j]), b[j] * __bfloat162float(vs[(16 * c + j) * V]));
+                if (16 * c + 16 > T || dead) {  // past the last node v was not written
+                    const uint32_t gone = (s_absent[c >> 1] | s_bad[c >> 1]) >> (16 * (c & 1));
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (gone >> j & 1 || 16 * c + j >= T) y[j] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split_pair(y[2 * i], y[2 * i + 1], hi[i], lo[i]);
+                tmem_st8x2(lanes + 8 * c, hi, lanes + kRlo + 8 * c, lo);
+            }
+    }
+    tc_fence_before();
+    ok = __syncthreads_and(ok) != 0;
+    tc_fence_after();
+    if (ok) {
+        if (t == 0) {
+            const uint64_t hi = sdesc_sw128(sb + M::PW, 16, 2048), lo = sdesc_sw128(sb + M::PW + 1024, 16, 2048);
+            mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem, hi, ID_1, 0);
+            mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem + kRlo, hi, ID_1, 1);
+            mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem, lo, ID_1, 1);
+            mma_commit(bars + BAR_O);
+        }
+        __syncwarp();
+        ok = mbar_wait_warp(bars + BAR_O, 0, abort_flag);
+        tc_fence_after();
+        // o by way of shared memory (the place of W, whose products are done), rows in 16-byte pieces
+        __nv_bfloat16 *s_o = reinterpret_cast<__nv_bfloat16 *>(sm);
+        if (column)
+#pragma unroll 1
+            for (int c = t / GROUP; 16 * c < T; c += 2) {
+                uint32_t sq[16], d2[16];
+                float sg[16];
+                tmem_ld16x2(lanes + kD1 + TP + 16 * c, sq, lanes + kD2 + 16 * c, d2);
+                lds16f(s_sg + 16 * c, sg);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s_o[(16 * c + i) * V + lane_row] =
+                        __float2bfloat16_rn(fmaf(sg[i], __uint_as_float(sq[i]), a.scale * __uint_as_float(d2[i])));
+            }
+        named_bar(NB_OUT, NT);
+        const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
+        if (dead) {
+            for (int i = t / GROUP; i < T && column; i += 2) {
+                if (s_absent[i >> 5] >> (i & 31) & 1) s_o[i * V + lane_row] = __float2bfloat16_rn(0.f);
+                if (s_bad[i >> 5] >> (i & 31) & 1) s_o[i * V + lane_row] = __float2bfloat16_rn(nan);
+            }
+            named_bar(NB_OUT, NT);
+        }
+        const int c = t & (V / 8 - 1), pieces = V == 128 ? 4 : 3;
+        for (int r = t >> pieces; r < T; r += NT >> pieces)
+            *reinterpret_cast<uint4 *>(o + r * o_tok + 8 * c) = *reinterpret_cast<const uint4 *>(s_o + r * V + 8 * c);
     }
     // A wait that ran out (its limit is a second): nothing in flight is left behind, and the row shows it.
     ok = __syncthreads_and(ok) != 0;
     if (!ok) {
-        if (t == 0) mbar_drain(bar_s, 0);
-        if (mine)
-            for (int i = 0; i < T; ++i) o[i * o_tok] = __float2bfloat16_rn(nan);
-        __syncthreads();
+        if (t == 0) mbar_drain(bars + BAR_S, 0);
+        if (t < V)
+            for (int i = 0; i < T; ++i) o[i * o_tok + t] = __float2bfloat16_rn(nan);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == SETUP) {
         tc_fence_after();
         tmem_dealloc(tmem, kCols);
     }
@@ -291,7 +481,7 @@ template <int K, int TP> cudaError_t launch(const DecodeArgs &a, bool vec, cudaS
     static_assert(2 * (bytes + 1024) <= 233472, "two CTAs per SM");
     const cudaError_t e = cudaFuncSetAttribute(k_tree_tc<K, TP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    k_tree_tc<K, TP><<<(unsigned)(a.n_seqs * a.Hv), NT, bytes, st>>>(a, vec);
+    k_tree_tc<K, TP><<<dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)a.G), NT, bytes, st>>>(a, vec);
     return cudaGetLastError();
 }
 
@@ -305,9 +495,11 @@ template <int K> cudaError_t launch_width(const DecodeArgs &a, bool vec, cudaStr
 }  // namespace
 
 cudaError_t launch_tree_tc(const DecodeArgs &a, int K, cudaStream_t st) {
-    // 16-byte copies of the rows of q and k where every row begins on such a boundary
-    const int64_t s = a.sq.batch | a.sq.token | a.sq.head | a.sk.batch | a.sk.token | a.sk.head;
-    const bool vec = !(s & 7) && !((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k)) & 15);
+    // 16-byte copies of the rows of q, k and v where every row begins on such a boundary
+    const int64_t s = a.sq.batch | a.sq.token | a.sq.head | a.sk.batch | a.sk.token | a.sk.head | a.sv.batch | a.sv.token |
+                      a.sv.head;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+    const bool vec = !(s & 7) && !(at & 15);
     return K == 128 ? launch_width<128>(a, vec, st) : launch_width<64>(a, vec, st);
 }
 
