@@ -4,11 +4,15 @@
 // the softmax, and the chunk's n best logits.  A logit and its place make one whole number (a key: ordered
 // bits of the value above, complement of the index below), so all keys differ and "the n best" needs no rule
 // for ties.  The n-th largest of the threads' own maxima bounds the n-th best key from below, and at most n
-// threads hold anything above it; those read their elements again (from the caches) and what is left, at
-// most n times a thread's elements whatever the order of the input, is ranked by counting.
+// threads hold anything above it; a warp reads each of those threads' elements again (from the caches) and what
+// is left, at most n times a thread's elements whatever the order of the input, is ranked by counting.
 // k_beam_pick: a CTA per search joins the chunks' sums into the beams' normalisers, turns the keys into
-// scores and selects in the same way, by the heads of the sorted lists.
+// scores and selects in the same way.  It is launched beside the first kernel and waits for its end on the GPU.
 // No result depends on the order in which threads arrive: places of collected keys do, their ranks do not.
+//
+// The sum is one of 2^(c x - m) with c = log2 e in fp32: one multiply-add and one exp2 per logit, and the same c
+// and m turn the sum back (in 64 bits, once per beam).  m follows the maximum only where that has grown by a
+// factor of 2^kSlack, so that the sums are hardly ever rescaled.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -18,7 +22,10 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPer = 128;  // elements of a chunk per thread, at most
+constexpr int kMaxGot = 8192;  // n times the elements per thread, at most: keys in shared memory
+constexpr int kPickKeys = 8;   // keys per thread that k_beam_pick holds in registers
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 40.f;
 
 __device__ __forceinline__ uint32_t ordered(float x) {  // larger for larger x; +0 and -0 alike
     const uint32_t u = __float_as_uint(x + 0.f);
@@ -34,23 +41,43 @@ __device__ __forceinline__ uint64_t make_key(float x, uint32_t index) {
 __device__ __forceinline__ uint32_t key_index(uint64_t key) { return 0xFFFFFFFFu - (uint32_t)key; }
 __device__ __forceinline__ float key_value(uint64_t key) { return unordered((uint32_t)(key >> 32)); }
 
-__device__ __forceinline__ float exp_of(float x) {  // e^x for x <= 0
+__device__ __forceinline__ float exp2_of(float x) {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-// Joins (m, s) with (m2, s2): sums of e^(x - m).  An empty side has m = -inf, s = 0.
+// A sum of 2^(c x - m) and its m; an empty one is (-inf, 0).  A logit of NaN or +inf leaves s = NaN.
 __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
     const float top = fmaxf(m, m2);
-    s = (m == -INFINITY ? s : s * expf(m - top)) + (m2 == -INFINITY ? s2 : s2 * expf(m2 - top));
+    s = (m == -INFINITY ? s : s * exp2f(m - top)) + (m2 == -INFINITY ? s2 : s2 * exp2f(m2 - top));
+    m = top;
+}
+__device__ __forceinline__ void join_warp(float &m, float &s) {
+    float top = m;
+#pragma unroll
+    for (int step = 16; step; step >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, step));
+    if (m != -INFINITY) s *= exp2f(m - top);
+#pragma unroll
+    for (int step = 16; step; step >>= 1) s += __shfl_xor_sync(~0u, s, step);
     m = top;
 }
 
-// The n-th largest (n <= 256) of the 256 threads' keys, to all threads: each warp sorts its 32, then a key's
-// rank is its place there plus, by bisection, the number of larger ones in the other warps' lists.  Keys that
-// are equal (only 0 can be) take the ranks of their warps.
-__device__ uint64_t nth_largest(uint64_t key, int n, uint64_t *s_sorted, uint64_t *s_answer) {
+// The logarithm of the sum: (m + log2 s) / c, the exponent of s apart so that the rounding is that of the result.
+__device__ __forceinline__ float normaliser(float m, float s) {
+    if (!(s > 0.f)) return s == 0.f ? -INFINITY : s;
+    const int e = (int)(__float_as_uint(s) >> 23) - 127;  // s is at least 1, up to rounding, and no infinity
+    const float f = __uint_as_float((__float_as_uint(s) & 0x007FFFFFu) | 0x3F800000u);
+    return (float)(((double)m + (double)e + (double)log2f(f)) * (1.0 / (double)kLog2e));
+}
+
+struct Nth {  // shared memory of nth_largest
+    uint64_t warp[kThreads / 32], heads[kThreads], answer;
+    int count;
+};
+// The n-th largest of the 256 threads' keys (all different, but for 0) to all threads; 0 if there are fewer.
+// The n-th largest of any one warp bounds it from below: each warp sorts its keys, what reaches the best of the
+// eight bounds is ranked by counting.
+__device__ __forceinline__ uint64_t nth_largest(uint64_t key, int n, Nth &sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t x = key;
 #pragma unroll
@@ -59,137 +86,183 @@ __device__ uint64_t nth_largest(uint64_t key, int n, uint64_t *s_sorted, uint64_
         for (int step = size >> 1; step; step >>= 1) {
             const uint64_t y = __shfl_xor_sync(~0u, x, step);
             const bool larger = ((lane & step) == 0) == ((lane & size) == 0);  // descending
-            x = larger ? (x > y ? x : y) : (x > y ? y : x);
+            x = (x > y) == larger ? x : y;
         }
-    __syncthreads();  // the arrays may still be read from an earlier use
-    s_sorted[threadIdx.x] = x;
+    const uint64_t bound = __shfl_sync(~0u, x, n <= 32 ? n - 1 : 31);
+    if (lane == 0) sh.warp[warp] = n <= 32 ? bound : 0;
+    if (threadIdx.x == 0) sh.answer = 0, sh.count = 0;
     __syncthreads();
-    int rank = lane;
+    uint64_t low = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const uint64_t *list = s_sorted + 32 * w;
-        int at = 0;  // entries of the list that come before x
-#pragma unroll
-        for (int step = 16; step; step >>= 1)
-            if (w < warp ? list[at + step - 1] >= x : list[at + step - 1] > x) at += step;
-        if (at == 31 && (w < warp ? list[31] >= x : list[31] > x)) at = 32;
-        if (w != warp) rank += at;
+    for (int w = 0; w < kThreads / 32; ++w) low = sh.warp[w] > low ? sh.warp[w] : low;
+    if (key && key >= low) sh.heads[atomicAdd(&sh.count, 1)] = key;
+    __syncthreads();
+    const int count = sh.count;
+    if ((int)threadIdx.x < count) {
+        const uint64_t mine = sh.heads[threadIdx.x];
+        int rank = 0;
+        for (int i = 0; i < count; ++i) rank += sh.heads[i] > mine;
+        if (rank == n - 1) sh.answer = mine;
     }
-    if (rank == n - 1) *s_answer = x;
     __syncthreads();
-    return *s_answer;
+    return sh.answer;
 }
 
 template <typename IO> struct Pack;
 template <> struct Pack<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void unpack(uint4 u, float (&x)[8]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    static __device__ __forceinline__ float get(const uint4 &u, int i) {
+        const uint32_t w = i < 2 ? u.x : i < 4 ? u.y : i < 6 ? u.z : u.w;
+        return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+    }
+    static __device__ __forceinline__ float max(const uint4 &u) {  // NaN counts as nothing
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+        const __nv_bfloat162 t = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(t), __high2float(t));
+    }
+    // the words of four elements' mask bytes, a pair each
+    static __device__ __forceinline__ void apply(uint32_t &lo, uint32_t &hi, uint32_t m) {
+        if (!(m & 0x000000FFu)) lo = (lo & 0xFFFF0000u) | 0xFF80u;
+        if (!(m & 0x0000FF00u)) lo = (lo & 0x0000FFFFu) | 0xFF800000u;
+        if (!(m & 0x00FF0000u)) hi = (hi & 0xFFFF0000u) | 0xFF80u;
+        if (!(m & 0xFF000000u)) hi = (hi & 0x0000FFFFu) | 0xFF800000u;
+    }
+    static __device__ __forceinline__ void apply(uint4 &u, const uint8_t *mask) {  // mask: 8 bytes, aligned
+        const uint2 m = *reinterpret_cast<const uint2 *>(mask);
+        apply(u.x, u.y, m.x);
+        apply(u.z, u.w, m.y);
     }
 };
 template <> struct Pack<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void unpack(uint4 u, float (&x)[4]) {
-        x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
+    static constexpr uint32_t kNone = 0xFF800000u;
+    static __device__ __forceinline__ float get(const uint4 &u, int i) {
+        return __uint_as_float(i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w);
+    }
+    static __device__ __forceinline__ float max(const uint4 &u) {
+        return fmaxf(fmaxf(get(u, 0), get(u, 1)), fmaxf(get(u, 2), get(u, 3)));
+    }
+    static __device__ __forceinline__ void apply(uint4 &u, const uint8_t *mask) {
+        const uint32_t m = *reinterpret_cast<const uint32_t *>(mask);
+        if (!(m & 0x000000FFu)) u.x = kNone;
+        if (!(m & 0x0000FF00u)) u.y = kNone;
+        if (!(m & 0x00FF0000u)) u.z = kNone;
+        if (!(m & 0xFF000000u)) u.w = kNone;
     }
 };
 
-// Elements [at, at + N) of a row (at may begin before it); what is outside or masked is -inf.
-template <typename IO>
-__device__ __forceinline__ void load(const IO *row, const uint8_t *mask, bool mask_whole, int at, int vocab, float (&x)[Pack<IO>::N]) {
-    constexpr int N = Pack<IO>::N;
-    if (at >= 0 && at + N <= vocab) {
-        Pack<IO>::unpack(*reinterpret_cast<const uint4 *>(row + at), x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = at + i >= 0 && at + i < vocab ? to_f<IO>(row[at + i]) : -INFINITY;
-    }
-    if (mask) {
-        if (mask_whole && at >= 0 && at + N <= vocab) {
-            uint32_t u[2] = {0, 0};
-            if (N == 8) {
-                const uint2 p = *reinterpret_cast<const uint2 *>(mask + at);
-                u[0] = p.x, u[1] = p.y;
-            } else {
-                u[0] = *reinterpret_cast<const uint32_t *>(mask + at);
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (!(u[i >> 2] >> (8 * (i & 3)) & 0xFF)) x[i] = -INFINITY;
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (at + i >= 0 && at + i < vocab && !mask[at + i]) x[i] = -INFINITY;
-        }
-    }
-}
+// One beam's logits as vectors on 16-byte boundaries: the first may begin before the row, the last end after it
+template <typename IO> struct Row {
+    static constexpr int N = Pack<IO>::N;
+    const IO *x;
+    const uint8_t *mask;
+    bool mask_whole;  // a vector's mask bytes are aligned too
+    int vocab;
 
-template <typename IO> __global__ void __launch_bounds__(kThreads) k_beam_scan(const BeamArgs a) {
-    constexpr int N = Pack<IO>::N;
-    extern __shared__ uint64_t s_got[];  // n * (elements per thread)
-    __shared__ uint64_t s_sorted[kThreads], s_nth;
+    // elements [at, at + N); what is outside or masked is -inf
+    __device__ __forceinline__ uint4 load(int at) const {
+        uint4 u;
+        if (at >= 0 && at + N <= vocab) {
+            u = *reinterpret_cast<const uint4 *>(x + at);
+            if (mask) {
+                if (mask_whole) {
+                    Pack<IO>::apply(u, mask + at);
+                } else {
+                    alignas(8) uint32_t m[2] = {0, 0};
+#pragma unroll
+                    for (int i = 0; i < N; ++i) m[i >> 2] |= (uint32_t)mask[at + i] << (8 * (i & 3));
+                    Pack<IO>::apply(u, reinterpret_cast<const uint8_t *>(m));
+                }
+            }
+        } else {
+            u = edge(at);
+        }
+        return u;
+    }
+    __device__ __noinline__ uint4 edge(int at) const {
+        IO v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = at + i >= 0 && at + i < vocab && (!mask || mask[at + i]) ? x[at + i] : from_f<IO>(-INFINITY);
+        uint4 u;
+        memcpy(&u, v, 16);
+        return u;
+    }
+};
+
+template <typename IO> __global__ void __launch_bounds__(kThreads, 6) k_beam_scan(const BeamArgs a) {
+    constexpr int N = Pack<IO>::N, STEP = kThreads * N;
+    extern __shared__ uint64_t s_got[];  // n times the elements per thread
+    __shared__ Nth sh;
     __shared__ float2 s_stat[kThreads / 32];
-    __shared__ int s_count;
-    const int tid = threadIdx.x, n = a.n;
-    const int64_t unit = blockIdx.x;  // (row, chunk)
-    const int row = (int)(unit / a.n_chunks), chunk = (int)(unit - (int64_t)row * a.n_chunks);
+    __shared__ int s_count, s_list[GDN_BEAM_MAX], s_listed;
+    const int tid = threadIdx.x, lane = tid & 31, n = a.n;
+    const int row = blockIdx.x / a.n_chunks, chunk = blockIdx.x - row * a.n_chunks;
+    asm volatile("griddepcontrol.launch_dependents;");  // the next kernel may take its place; it waits for this one's end
     if (a.finished && a.finished[row]) return;
     const int b = row / a.W, w = row - b * a.W;
-    const IO *x_row = static_cast<const IO *>(a.logits) + b * a.logits_batch + w * a.logits_beam;
-    const uint8_t *mask = a.mask ? a.mask + b * a.mask_batch + w * a.mask_beam : nullptr;
-    // vectors lie on 16-byte boundaries: the first one may begin before the row
-    const int shift = (int)((reinterpret_cast<uintptr_t>(x_row) & 15) / sizeof(IO));
-    const bool mask_whole = mask && ((reinterpret_cast<uintptr_t>(mask) - shift) & (N - 1)) == 0;
-    const int begin = chunk * a.chunk - shift + tid * N, end = min((chunk + 1) * a.chunk - shift, a.vocab);
+    Row<IO> x;
+    x.x = static_cast<const IO *>(a.logits) + b * a.logits_batch + w * a.logits_beam;
+    x.mask = a.mask ? a.mask + b * a.mask_batch + w * a.mask_beam : nullptr;
+    x.vocab = a.vocab;
+    const int shift = (int)((reinterpret_cast<uintptr_t>(x.x) & 15) / sizeof(IO));
+    x.mask_whole = ((reinterpret_cast<uintptr_t>(x.mask) - shift) & (N - 1)) == 0;
+    const int first = chunk * a.chunk - shift, begin = first + tid * N;
+    const int end = min(first + a.chunk, a.vocab);
 
-    float m = -INFINITY, s = 0.f, best = -INFINITY;
+    float best = -INFINITY, m = 0.f, s0 = 0.f, s1 = 0.f;  // m: at most c * best, 0 before there is one
     int best_at = begin;
-#pragma unroll 4
-    for (int at = begin; at < end; at += kThreads * N) {
-        float x[N];
-        load<IO>(x_row, mask, mask_whole, at, a.vocab, x);
-        float top = x[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
-        if (top > best) best = top, best_at = at;
-        if (top > m) {
-            s = m == -INFINITY ? s : s * exp_of(m - top);
-            m = top;
+    auto take = [&](const uint4 &u, int at) {
+        const float top = Pack<IO>::max(u);
+        if (top > best) {
+            if (best == -INFINITY || fmaf(top, kLog2e, -m) > kSlack) {
+                const float f = best == -INFINITY ? 1.f : exp2_of(fmaf(top, -kLog2e, m));
+                s0 *= f, s1 *= f, m = kLog2e * top;
+            }
+            best = top, best_at = at;
         }
-        float add = 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) add += m == -INFINITY ? (x[i] == -INFINITY ? 0.f : x[i]) : exp_of(x[i] - m);
-        s += add;
+        for (int i = 0; i < N; i += 2) {
+            s0 += exp2_of(fmaf(Pack<IO>::get(u, i), kLog2e, -m));
+            s1 += exp2_of(fmaf(Pack<IO>::get(u, i + 1), kLog2e, -m));
+        }
+    };
+    int at = begin;
+    for (; at + 3 * STEP < end; at += 4 * STEP) {
+        uint4 u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = x.load(at + j * STEP);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) take(u[j], at + j * STEP);
     }
+    for (; at < end; at += STEP) take(x.load(at), at);
     uint64_t mine = 0;
     if (best > -INFINITY) {
-        float x[N];
-        load<IO>(x_row, mask, mask_whole, best_at, a.vocab, x);
+        const uint4 u = x.load(best_at);
 #pragma unroll
         for (int i = N - 1; i >= 0; --i)
-            if (x[i] == best) mine = make_key(best, best_at + i);
+            if (Pack<IO>::get(u, i) == best) mine = make_key(best, best_at + i);
     }
-#pragma unroll
-    for (int step = 16; step; step >>= 1) {
-        const float m2 = __shfl_xor_sync(~0u, m, step), s2 = __shfl_xor_sync(~0u, s, step);
-        join(m, s, m2, s2);
+    float ms = best == -INFINITY ? -INFINITY : m, s = s0 + s1;
+    join_warp(ms, s);
+    if (tid == 0) s_count = 0, s_listed = 0;
+    if (lane == 0) s_stat[tid >> 5] = make_float2(ms, s);
+    const uint64_t low = nth_largest(mine, n, sh);
+    const int64_t unit = blockIdx.x;
+    if (tid < 32) {
+        const float2 st = lane < kThreads / 32 ? s_stat[lane] : make_float2(-INFINITY, 0.f);
+        ms = st.x, s = st.y;
+        join_warp(ms, s);
+        if (lane == 0) a.stats[unit] = make_float2(ms, s);
     }
-    if (tid == 0) s_count = 0;
-    if ((tid & 31) == 0) s_stat[tid >> 5] = make_float2(m, s);
-    const uint64_t low = nth_largest(mine, n, s_sorted, &s_nth);
-    if (tid == 0) {
-        for (int i = 1; i < kThreads / 32; ++i) join(m, s, s_stat[i].x, s_stat[i].y);
-        a.stats[unit] = make_float2(m, s);
-    }
-    if (mine && mine >= low)
-        for (int at = begin; at < end; at += kThreads * N) {
-            float x[N];
-            load<IO>(x_row, mask, mask_whole, at, a.vocab, x);
+    if (mine && mine >= low) s_list[atomicAdd(&s_listed, 1)] = tid;
+    __syncthreads();
+    for (int e = tid >> 5; e < s_listed; e += kThreads / 32)
+        for (int v = first + s_list[e] * N + lane * STEP; v < end; v += 32 * STEP) {
+            const uint4 u = x.load(v);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const uint64_t key = make_key(x[i], at + i);
+                const uint64_t key = make_key(Pack<IO>::get(u, i), v + i);
                 if (key && key >= low) s_got[atomicAdd(&s_count, 1)] = key;
             }
         }
@@ -206,70 +279,90 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) k_beam_scan(c
 }
 
 __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
-    extern __shared__ uint64_t s_got[];  // n * n, or n times a thread's heads where that is more
-    __shared__ uint64_t s_sorted[kThreads], s_nth;
+    extern __shared__ uint64_t s_got[];
+    __shared__ Nth sh;
     __shared__ float s_norm[GDN_BEAM_MAX], s_score[GDN_BEAM_MAX];
     __shared__ uint8_t s_done[GDN_BEAM_MAX];
     __shared__ int s_count;
     const int tid = threadIdx.x, lane = tid & 31, n = a.n, W = a.W, b = blockIdx.x;
-    const int lists = W * a.n_chunks;
-    const uint64_t *keys = a.keys + (int64_t)b * lists * n;
-    for (int w = tid >> 5; w < W; w += kThreads / 32) {
-        const bool done = a.finished && a.finished[b * W + w];
-        float m = -INFINITY, s = 0.f;
-        if (!done)
-            for (int i = lane; i < a.n_chunks; i += 32) {
-                const float2 st = a.stats[(int64_t)(b * W + w) * a.n_chunks + i];
-                join(m, s, st.x, st.y);
-            }
-#pragma unroll
-        for (int step = 16; step; step >>= 1) {
-            const float m2 = __shfl_xor_sync(~0u, m, step), s2 = __shfl_xor_sync(~0u, s, step);
-            join(m, s, m2, s2);
-        }
-        if (lane == 0) s_norm[w] = m + logf(s), s_score[w] = a.scores[b * W + w], s_done[w] = done;
-    }
+    const int lists = W * a.n_chunks, total = lists * n;
+    const uint64_t *keys = a.keys + (int64_t)b * total;
+    if (tid < W) s_score[tid] = a.scores[b * W + tid], s_done[tid] = a.finished && a.finished[b * W + tid];
     if (tid == 0) s_count = 0;
     __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const bool few = total <= kPickKeys * kThreads;
+    uint64_t held[kPickKeys];
+    if (few) {
+#pragma unroll
+        for (int i = 0; i < kPickKeys; ++i) held[i] = tid + i * kThreads < total ? __ldcg(keys + tid + i * kThreads) : 0;
+    }
+    for (int w = tid >> 5; w < W; w += kThreads / 32) {
+        float m = -INFINITY, s = 0.f;
+        if (!s_done[w])
+            for (int i = lane; i < a.n_chunks; i += 32) {
+                const float2 st = __ldcg(a.stats + (int64_t)(b * W + w) * a.n_chunks + i);
+                join(m, s, st.x, st.y);
+            }
+        join_warp(m, s);
+        if (lane == 0) s_norm[w] = normaliser(m, s);
+    }
+    __syncthreads();
 
-    // entry j of a list, as a key of its score and its place in the search
-    auto entry = [&](int list, int j) -> uint64_t {
+    // key j of a list, as a key of its score and its place in the search
+    auto entry = [&](int list, int j, uint64_t key) -> uint64_t {
         const int w = list / a.n_chunks;
         if (s_done[w]) return j == 0 && list == w * a.n_chunks ? make_key(s_score[w], (uint32_t)w * a.vocab) : 0;
-        const uint64_t key = keys[(int64_t)list * n + j];
         if (!key) return 0;
         return make_key(s_score[w] + (key_value(key) - s_norm[w]), (uint32_t)w * a.vocab + key_index(key));
     };
+    auto read = [&](int list, int j) { return entry(list, j, __ldcg(keys + (int64_t)list * n + j)); };
     uint64_t mine = 0;
-    for (int l = tid; l < lists; l += kThreads) {
-        const uint64_t head = entry(l, 0);
-        mine = head > mine ? head : mine;
-    }
-    uint64_t low = nth_largest(mine, n, s_sorted, &s_nth);
-    if (lists > kThreads) {  // the n-th largest head itself, so that no more than n lists are opened
-        if (mine && mine >= low)
-            for (int l = tid; l < lists; l += kThreads) {
-                const uint64_t head = entry(l, 0);
-                if (head && head >= low) s_got[atomicAdd(&s_count, 1)] = head;
-            }
-        __syncthreads();
-        const int count = s_count;
-        for (int e = tid; e < count; e += kThreads) {
-            int rank = 0;
-            for (int i = 0; i < count; ++i) rank += s_got[i] > s_got[e];
-            if (rank == n - 1) s_nth = s_got[e];
+    if (few) {
+#pragma unroll
+        for (int i = 0; i < kPickKeys; ++i) {
+            const int e = tid + i * kThreads;
+            if (e < total) held[i] = entry(e / n, e % n, held[i]);
+            mine = held[i] > mine ? held[i] : mine;
         }
-        __syncthreads();
-        low = count >= n ? s_nth : 0;
-        if (tid == 0) s_count = 0;
-        __syncthreads();
-    }
-    for (int l = tid; l < lists; l += kThreads) {
-        const uint64_t head = entry(l, 0);
-        if (!head || head < low) continue;
-        for (int j = 0; j < n; ++j) {
-            const uint64_t key = entry(l, j);
-            if (key && key >= low) s_got[atomicAdd(&s_count, 1)] = key;
+        const uint64_t low = nth_largest(mine, n, sh);
+        if (mine >= low)
+#pragma unroll
+            for (int i = 0; i < kPickKeys; ++i)
+                if (held[i] && held[i] >= low) s_got[atomicAdd(&s_count, 1)] = held[i];
+    } else {  // by the heads of the sorted lists
+        for (int l = tid; l < lists; l += kThreads) {
+            const uint64_t head = read(l, 0);
+            mine = head > mine ? head : mine;
+        }
+        uint64_t low = nth_largest(mine, n, sh);
+        if (lists > kThreads) {  // the n-th largest head itself, so that no more than n lists are opened
+            if (mine && mine >= low)
+                for (int l = tid; l < lists; l += kThreads) {
+                    const uint64_t head = read(l, 0);
+                    if (head && head >= low) s_got[atomicAdd(&s_count, 1)] = head;
+                }
+            __syncthreads();  // all have the first bound
+            if (tid == 0) sh.answer = 0;
+            __syncthreads();
+            const int count = s_count;
+            for (int e = tid; e < count; e += kThreads) {
+                int rank = 0;
+                for (int i = 0; i < count; ++i) rank += s_got[i] > s_got[e];
+                if (rank == n - 1) sh.answer = s_got[e];
+            }
+            __syncthreads();
+            low = sh.answer;
+            if (tid == 0) s_count = 0;
+            __syncthreads();
+        }
+        for (int l = tid; l < lists; l += kThreads) {
+            const uint64_t head = read(l, 0);
+            if (!head || head < low) continue;
+            for (int j = 0; j < n; ++j) {
+                const uint64_t key = read(l, j);
+                if (key && key >= low) s_got[atomicAdd(&s_count, 1)] = key;
+            }
         }
     }
     __syncthreads();
@@ -296,26 +389,39 @@ __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
 }
 
 template <typename IO> cudaError_t launch(const BeamArgs &a, cudaStream_t st) {
-    const int per = (a.W * a.n_chunks + kThreads - 1) / kThreads;  // heads per thread
-    const int scan = a.n * (a.chunk / kThreads) * 8, pick = a.n * (a.n > per ? a.n : per) * 8;
-    cudaError_t e = cudaFuncSetAttribute(k_beam_scan<IO>, cudaFuncAttributeMaxDynamicSharedMemorySize, GDN_BEAM_MAX * kMaxPer * 8);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(k_beam_scan<IO>, kMaxGot * 8, done);
     if (e != cudaSuccess) return e;
-    k_beam_scan<IO><<<(unsigned)((int64_t)a.B * a.W * a.n_chunks), kThreads, scan, st>>>(a);
+    const int lists = a.W * a.n_chunks;
+    k_beam_scan<IO><<<(unsigned)(a.B * lists), kThreads, a.n * (a.chunk / kThreads) * 8, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    k_beam_pick<<<(unsigned)a.B, kThreads, pick, st>>>(a);
-    return cudaGetLastError();
+    // keys collected at once: n threads' or n lists', or the heads of n threads' lists
+    const int per = lists * a.n <= kPickKeys * kThreads ? kPickKeys : a.n, heads = (lists + kThreads - 1) / kThreads;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.B);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)a.n * (per > heads ? per : heads) * 8;
+    cfg.stream = st;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_beam_pick, a);
 }
 
 }  // namespace
 
-// Elements of a row that one CTA takes: enough CTAs for four on every SM where the rows allow it, a vector per
-// thread at least, kMaxPer elements per thread at most.
-int beam_chunk(int64_t rows, int64_t vocab, gdn_dtype io) {
-    const int64_t least = kThreads * (io == GDN_BF16 ? 8 : 4), most = (int64_t)kThreads * kMaxPer;
-    const int64_t per_row = rows >= 152 * 4 ? 1 : rows < 1 ? 1 : (152 * 4 + rows - 1) / rows;
-    int64_t c = (vocab + per_row - 1) / per_row;
-    c = (c + least - 1) / least * least;
-    return (int)(c < least ? least : c > most ? most : c);
+// Elements of a row that one CTA takes: enough CTAs for eight on every SM where the rows allow it, a vector per
+// thread at least, and no more than the keys in shared memory allow.  Equal chunks: up to seven elements are added
+// for a row that begins inside a vector.
+int beam_chunk(int64_t rows, int64_t vocab, int64_t n, gdn_dtype io) {
+    const int64_t wanted = 152 * 8, least = kThreads * (io == GDN_BF16 ? 8 : 4), per = kMaxGot / n < 512 ? kMaxGot / n : 512;
+    const int64_t most = kThreads * per / least * least;
+    int64_t chunks = rows < 1 ? 1 : (wanted + rows - 1) / rows;
+    const int64_t fewest = (vocab + 7 + most - 1) / most;
+    if (chunks < fewest) chunks = fewest;
+    return (int)(((vocab + 7 + chunks - 1) / chunks + least - 1) / least * least);
 }
 
 cudaError_t launch_beam(const BeamArgs &a, gdn_dtype io, cudaStream_t st) {

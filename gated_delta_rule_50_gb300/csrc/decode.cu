@@ -5,19 +5,27 @@
 // the state's registers serves k and q and a second one updates it.
 //
 // A warp holds a [K][32] tile of the state in registers: lane = (r, c) with c = 0..7 has the four columns
-// 4c .. 4c+3 of the rows 16 i + 4 r + j (K values of 32 bits per lane, K/4 loads of 16 bytes, each a full
+// 4c .. 4c+3 of the rows 16 i + 4 r + j (K values of 32 bits per lane, K/4 accesses of 16 bytes, each a full
 // 128-byte line per row across the lanes).  The value columns are independent, so nothing crosses warps;
 // the four r lanes of a column group meet through shuffles.
+//
+// Up to about eight tokens the states' way through memory bounds the step (each is read and written once).  Two
+// kernels share the arithmetic: k_recurrent, a CTA per (row, head, part of the columns), for few heads, and
+// k_recurrent_flow, a CTA per SM that has the next states on the way in shared memory while it works, for many.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
 #include "decode.h"
+#include "tc.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kTok = 8;   // tokens staged in shared memory at a time
-constexpr int kTile = 32; // state columns per warp
+using namespace tc;
+
+template <typename IO> constexpr int kTok = 16 / (int)sizeof(IO);  // tokens staged in shared memory at a time
+constexpr int kTile = 32;  // state columns per warp
+constexpr int kSMs = 152;
 
 // Sums x[0..3] (the lane's four columns) over the four r lanes; lane (r, c) gets column 4c + r.
 __device__ __forceinline__ float reduce_columns(const float (&x)[4], int r) {
@@ -28,147 +36,376 @@ __device__ __forceinline__ float reduce_columns(const float (&x)[4], int r) {
     return (r1 ? b : a) + __shfl_xor_sync(~0u, r1 ? a : b, 16);
 }
 
-template <int K, typename IO>
-__global__ void __launch_bounds__(128) k_recurrent(const DecodeArgs a) {
-    constexpr int NR = K / 4;  // rows per lane
-    __shared__ float4 s_k4[kTok][K / 4], s_q4[kTok][K / 4];
-    __shared__ float s_v[kTok][128], s_a[kTok], s_b[kTok];
-    __shared__ int s_tok[kTok];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int c = lane & 7, r = lane >> 3;
-    const int n = blockIdx.x / a.Hv, h = blockIdx.x - n * a.Hv, hq = h / a.G;
-    const int cta_cols = blockDim.x;  // 32 columns per warp
-    const int col0 = blockIdx.y * cta_cols;
-
-    // the row's tokens: [bos, bos + len) of batch row b, or its list
-    int64_t bos = 0, row = n;
-    int b = n, len = a.token_indices ? a.n_steps : a.T;
+// What one row runs through: tokens [bos, bos + len) of batch row b, or a list of len tokens at most
+struct Run {
+    int64_t bos, out_row, slot;
+    int b, len;
+    bool valid;  // the row's offsets lie in the tensor
+};
+__device__ __forceinline__ Run run_of(const DecodeArgs &a, int n) {
+    Run u;
+    u.valid = true, u.bos = 0, u.b = n;
+    u.len = a.token_indices ? a.n_steps : a.T;
+    u.out_row = (int64_t)n * u.len;
     if (a.cu) {
         const int lo = a.cu[n], hi = a.cu[n + 1];
-        if (lo < 0 || hi < lo || hi > a.T) return;  // not offsets of this tensor
-        b = 0, bos = lo, len = hi - lo, row = 0;
+        u.valid = lo >= 0 && hi >= lo && hi <= a.T;
+        u.b = 0, u.bos = u.out_row = lo, u.len = hi - lo;
     }
-    const int64_t out_row = (a.cu ? bos : row * (int64_t)len);  // first row of o
-    const int64_t slot = a.state_indices ? a.state_indices[n] : n;
-    const bool idle = slot < 0;
-    IO *o = static_cast<IO *>(a.o);
-    if (idle || slot >= a.n_slots) {
-        if (o)
-            for (int t = 0; t < len; ++t)
-                o[((out_row + t) * a.Hv + h) * a.V + col0 + tid] = from_f<IO>(idle ? 0.f : __int_as_float(0x7fffffff));
-        return;
+    u.slot = a.state_indices ? a.state_indices[n] : n;
+    return u;
+}
+
+// Up to kTok tokens for `cols` threads, one state column each
+template <int K, typename IO> struct Stage {
+    alignas(16) IO k[kTok<IO>][K], q[kTok<IO>][K], v[kTok<IO>][128];
+    float a[kTok<IO>], b[kTok<IO>];
+    int tok[kTok<IO>];
+};
+__device__ __forceinline__ float4 load4(const float *x) { return *reinterpret_cast<const float4 *>(x); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *x) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(x);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+// The threads of one head (tid = 0 .. cols - 1, columns col0 + tid) and their barrier
+template <int K, typename IO> struct Head {
+    static constexpr int NR = K / 4;
+    const DecodeArgs &a;
+    Stage<K, IO> &s;
+    const Run u;
+    const IO *q, *k, *v;
+    const float *g, *beta;
+    IO *o;  // row out_row of this head, this thread's column
+    int n, tid, cols, bar;
+
+    __device__ __forceinline__ Head(const DecodeArgs &a, Stage<K, IO> &s, const Run &u, int n, int h, int hq, int col0, int tid, int cols, int bar)
+        : a(a), s(s), u(u), n(n), tid(tid), cols(cols), bar(bar) {
+        q = static_cast<const IO *>(a.q) + u.b * a.sq.batch + hq * a.sq.head;
+        k = static_cast<const IO *>(a.k) + u.b * a.sk.batch + hq * a.sk.head;
+        v = static_cast<const IO *>(a.v) + u.b * a.sv.batch + h * a.sv.head + col0 + tid;
+        g = a.g + u.b * a.sg.batch + h * a.sg.head;
+        beta = a.beta + u.b * a.sb.batch + h * a.sb.head;
+        o = a.o ? static_cast<IO *>(a.o) + (u.out_row * a.Hv + h) * a.V + col0 : nullptr;
     }
-
-    const int64_t head = (int64_t)h * K * a.V + col0 + warp * kTile + 4 * c;
-    const float *src = a.state + slot * a.slot_stride + head;
-    float4 S[NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-        S[i] = *reinterpret_cast<const float4 *>(src + (int64_t)(16 * (i >> 2) + 4 * r + (i & 3)) * a.V);
-
-    const IO *q = static_cast<const IO *>(a.q) + b * a.sq.batch + hq * a.sq.head;
-    const IO *k = static_cast<const IO *>(a.k) + b * a.sk.batch + hq * a.sk.head;
-    const IO *v = static_cast<const IO *>(a.v) + b * a.sv.batch + (int64_t)h * a.sv.head + col0;
-    const float *g = a.g + b * a.sg.batch + h * a.sg.head, *beta = a.beta + b * a.sb.batch + h * a.sb.head;
-    float *s_k = reinterpret_cast<float *>(s_k4), *s_q = reinterpret_cast<float *>(s_q4);
-
-    bool bad = false;
-    int t0 = 0;
-    for (bool more = true; more && t0 < len; t0 += kTok) {
-        int m = min(kTok, len - t0);
-        if (t0) __syncthreads();
+    __device__ __forceinline__ int64_t o_tok() const { return (int64_t)a.Hv * a.V; }
+    // o of tokens [from, len): 0, or NaN where an index was none
+    __device__ __forceinline__ void fill(int from, bool bad) const {
+        if (!o) return;
+        for (int t = from; t < u.len; ++t) o[t * o_tok() + tid] = from_f<IO>(bad ? __int_as_float(0x7fffffff) : 0.f);
+    }
+    // Tokens t0 .. t0 + kTok - 1 into the stage; how many there are, and whether the row ends in them
+    __device__ __forceinline__ int stage(int t0, bool &more, bool &bad) const {
+        int m = min(kTok<IO>, u.len - t0);
         if (a.token_indices) {
-            if (tid < m) s_tok[tid] = a.token_indices[(int64_t)n * a.n_steps + t0 + tid];
-            __syncthreads();
+            if (tid < m) s.tok[tid] = a.token_indices[(int64_t)n * a.n_steps + t0 + tid];
+            named_bar(bar, cols);
             for (int t = 0; t < m; ++t) {
-                const int at = s_tok[t];
+                const int at = s.tok[t];
                 if (at >= 0 && at < a.T) continue;
                 bad = at >= 0;
                 m = t, more = false;
                 break;
             }
         }
-        for (int e = tid; e < m * K; e += cta_cols) {
+        for (int e = tid; e < m * K; e += cols) {
             const int t = e / K, x = e % K;
-            const int64_t at = a.token_indices ? s_tok[t] : bos + t0 + t;
-            s_k[e] = to_f<IO>(k[at * a.sk.token + x]);
-            if (o) s_q[e] = to_f<IO>(q[at * a.sq.token + x]);
+            const int64_t at = a.token_indices ? s.tok[t] : u.bos + t0 + t;
+            s.k[t][x] = k[at * a.sk.token + x];
+            if (o) s.q[t][x] = q[at * a.sq.token + x];
         }
         for (int t = 0; t < m; ++t) {
-            const int64_t at = a.token_indices ? s_tok[t] : bos + t0 + t;
-            s_v[t][tid] = to_f<IO>(v[at * a.sv.token + tid]);
-            if (tid == 0) s_a[t] = expf(g[at * a.sg.token]), s_b[t] = beta[at * a.sb.token];
+            const int64_t at = a.token_indices ? s.tok[t] : u.bos + t0 + t;
+            s.v[t][tid] = v[at * a.sv.token];
+            if (tid == t) s.a[t] = expf(g[at * a.sg.token]), s.b[t] = beta[at * a.sb.token];
         }
-        __syncthreads();
-
+        return m;
+    }
+    // m staged tokens, the first of them the t0-th of the row
+    __device__ __forceinline__ void advance(float4 (&S)[NR], int t0, int m) const {
+        const int lane = tid & 31, c = lane & 7, r = lane >> 3;
+        const int col = (tid & ~31) + 4 * c + r;  // the column whose sums this lane gets
+#pragma unroll 1
         for (int t = 0; t < m; ++t) {
             float ks[4] = {0.f, 0.f, 0.f, 0.f}, qs[4] = {0.f, 0.f, 0.f, 0.f}, qk = 0.f;
 #pragma unroll
             for (int i = 0; i < K / 16; ++i) {
-                const float4 kk = s_k4[t][4 * i + r];
+                const float4 kk = load4(s.k[t] + 16 * i + 4 * r);
                 const float kj[4] = {kk.x, kk.y, kk.z, kk.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float4 s = S[4 * i + j];
-                    ks[0] = fmaf(kj[j], s.x, ks[0]);
-                    ks[1] = fmaf(kj[j], s.y, ks[1]);
-                    ks[2] = fmaf(kj[j], s.z, ks[2]);
-                    ks[3] = fmaf(kj[j], s.w, ks[3]);
+                    const float4 x = S[4 * i + j];
+                    ks[0] = fmaf(kj[j], x.x, ks[0]);
+                    ks[1] = fmaf(kj[j], x.y, ks[1]);
+                    ks[2] = fmaf(kj[j], x.z, ks[2]);
+                    ks[3] = fmaf(kj[j], x.w, ks[3]);
                 }
                 if (o) {
-                    const float4 qq = s_q4[t][4 * i + r];
+                    const float4 qq = load4(s.q[t] + 16 * i + 4 * r);
                     const float qj[4] = {qq.x, qq.y, qq.z, qq.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 s = S[4 * i + j];
-                        qs[0] = fmaf(qj[j], s.x, qs[0]);
-                        qs[1] = fmaf(qj[j], s.y, qs[1]);
-                        qs[2] = fmaf(qj[j], s.z, qs[2]);
-                        qs[3] = fmaf(qj[j], s.w, qs[3]);
+                        const float4 x = S[4 * i + j];
+                        qs[0] = fmaf(qj[j], x.x, qs[0]);
+                        qs[1] = fmaf(qj[j], x.y, qs[1]);
+                        qs[2] = fmaf(qj[j], x.z, qs[2]);
+                        qs[3] = fmaf(qj[j], x.w, qs[3]);
                         qk = fmaf(qj[j], kj[j], qk);
                     }
                 }
             }
-            const float al = s_a[t];
-            const int col = warp * kTile + 4 * c + r;
-            const float d = s_b[t] * (s_v[t][col] - al * reduce_columns(ks, r));
+            const float al = s.a[t];
+            const float d = s.b[t] * (to_f<IO>(s.v[t][col]) - al * reduce_columns(ks, r));
             if (o) {
                 qk += __shfl_xor_sync(~0u, qk, 8);
                 qk += __shfl_xor_sync(~0u, qk, 16);
-                const float out = a.scale * fmaf(qk, d, al * reduce_columns(qs, r));
-                o[((out_row + t0 + t) * a.Hv + h) * a.V + col0 + col] = from_f<IO>(out);
+                o[(t0 + t) * o_tok() + col] = from_f<IO>(a.scale * fmaf(qk, d, al * reduce_columns(qs, r)));
             }
             float dj[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) dj[j] = __shfl_sync(~0u, d, c + 8 * j);
 #pragma unroll
             for (int i = 0; i < K / 16; ++i) {
-                const float4 kk = s_k4[t][4 * i + r];
+                const float4 kk = load4(s.k[t] + 16 * i + 4 * r);
                 const float kj[4] = {kk.x, kk.y, kk.z, kk.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float4 &s = S[4 * i + j];
-                    s.x = fmaf(kj[j], dj[0], al * s.x);
-                    s.y = fmaf(kj[j], dj[1], al * s.y);
-                    s.z = fmaf(kj[j], dj[2], al * s.z);
-                    s.w = fmaf(kj[j], dj[3], al * s.w);
+                    float4 &x = S[4 * i + j];
+                    x.x = fmaf(kj[j], dj[0], al * x.x);
+                    x.y = fmaf(kj[j], dj[1], al * x.y);
+                    x.z = fmaf(kj[j], dj[2], al * x.z);
+                    x.w = fmaf(kj[j], dj[3], al * x.w);
                 }
             }
         }
-        if (!more && o)  // past the end of a list of tokens, or at an index that is none
-            for (int t = t0 + m; t < len; ++t)
-                o[((out_row + t) * a.Hv + h) * a.V + col0 + tid] = from_f<IO>(bad ? __int_as_float(0x7fffffff) : 0.f);
     }
-    if (bad) return;
-    float *dst = (a.out_state ? a.out_state + (int64_t)n * a.Hv * K * a.V : a.state + slot * a.slot_stride) + head;
+    // The row from its first m tokens, which all threads see in the stage, to its end; whether the new state is to be
+    // kept
+    __device__ __forceinline__ bool run(float4 (&S)[NR], int m, bool more, bool bad) const {
+        int t0 = 0;
+        for (;;) {
+            advance(S, t0, m);
+            t0 += m;
+            if (!more || t0 >= u.len) break;
+            named_bar(bar, cols);
+            m = stage(t0, more, bad);
+            named_bar(bar, cols);
+            if (m == 0) break;
+        }
+        if (t0 < u.len) fill(t0, bad);
+        return !bad;
+    }
+    __device__ __forceinline__ float *out(int h) const {
+        return a.out_state ? a.out_state + ((int64_t)n * a.Hv + h) * K * a.V
+                           : a.state + u.slot * a.slot_stride + (int64_t)h * K * a.V;
+    }
+};
+
+// grid (rows, q/k heads, value heads of one * parts of the columns)
+template <int K, typename IO> __global__ void __launch_bounds__(128) k_recurrent(const __grid_constant__ DecodeArgs a) {
+    constexpr int NR = K / 4;
+    __shared__ Stage<K, IO> s;
+    const int tid = threadIdx.x, cols = blockDim.x;
+    const int n = blockIdx.x, hq = blockIdx.y, h = hq * a.G + blockIdx.z % a.G, col0 = blockIdx.z / a.G * cols;
+    const Run u = run_of(a, n);
+    if (!u.valid) return;
+    const Head<K, IO> head(a, s, u, n, h, hq, col0, tid, cols, 1);
+    if (u.slot < 0 || u.slot >= a.n_slots) {
+        head.fill(0, u.slot >= 0);
+        return;
+    }
+    const int c = tid & 7, r = (tid & 31) >> 3;
+    const int at = 4 * r * a.V + col0 + (tid & ~31) + 4 * c;
+    const float *src = a.state + u.slot * a.slot_stride + (int64_t)h * K * a.V + at;
+    float4 S[NR];
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
-        *reinterpret_cast<float4 *>(dst + (int64_t)(16 * (i >> 2) + 4 * r + (i & 3)) * a.V) = S[i];
+    for (int i = 0; i < NR; ++i) S[i] = *reinterpret_cast<const float4 *>(src + (16 * (i >> 2) + (i & 3)) * a.V);
+    bool more = true, bad = false;
+    const int m = head.stage(0, more, bad);
+    named_bar(1, cols);
+    if (!head.run(S, m, more, bad)) return;
+    float *dst = head.out(h) + at;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) *reinterpret_cast<float4 *>(dst + (16 * (i >> 2) + (i & 3)) * a.V) = S[i];
+}
+
+// Shared memory of k_recurrent_flow: a ring of slots, each a state and the first tokens of its row (k, q, v as they
+// are), what there is to know of the slots, a stage per group, barriers
+constexpr int kMaxSlots = 8;
+struct SlotInfo {
+    float a[8], b[8];
+    int m, more, bad;
+};
+struct Flow {
+    int groups, slots, state_bytes, slot_bytes, stage_bytes, bytes;
+};
+template <int K, typename IO> Flow flow_of(int V) {
+    Flow f;
+    f.groups = 256 / V;
+    f.state_bytes = K * V * 4;
+    f.slot_bytes = f.state_bytes + kTok<IO> * (2 * K + V) * (int)sizeof(IO);
+    f.stage_bytes = (int)sizeof(Stage<K, IO>);
+    const int rest = 128 + f.groups * f.stage_bytes + kMaxSlots * (int)sizeof(SlotInfo) + 256;
+    const int room = (232448 - rest) / f.slot_bytes;  // 227 KB
+    f.slots = room < kMaxSlots ? room : kMaxSlots;
+    f.bytes = rest + f.slots * f.slot_bytes;
+    return f;
+}
+
+// One CTA per SM: groups of V threads take the states of this CTA's heads in turn from the ring into registers, ask
+// at once for what comes next into the slot, run theirs and write it back from the registers.  What a fetch itself
+// depends on (slot, token numbers, gates) is read one round earlier, while the group waits for its state.
+template <int K, typename IO>
+__global__ void __launch_bounds__(256, 1) k_recurrent_flow(const __grid_constant__ DecodeArgs a, const __grid_constant__ Flow f, int heads) {
+    constexpr int NR = K / 4, AHEAD = kTok<IO>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
+    unsigned char *stages = sm + f.slots * f.slot_bytes;
+    SlotInfo *info = reinterpret_cast<SlotInfo *>(stages + f.groups * f.stage_bytes);
+    unsigned char *bars = reinterpret_cast<unsigned char *>(info + kMaxSlots);
+    const uint32_t full = smem_u32(bars);
+    volatile int *issued = reinterpret_cast<volatile int *>(bars + 64), *abort_flag = issued + 8;
+    const int group = threadIdx.x / a.V, tid = threadIdx.x - group * a.V, bar = 1 + group, lane = tid & 31;
+
+    struct Ahead {  // of a head that is to be fetched; lane t has its t-th token
+        Run u;
+        int64_t tok;
+        float g, beta;
+        int m, more, bad, h;
+    };
+    auto look = [&](int item) {  // a whole warp
+        Ahead x;
+        const int n = item / a.Hv;
+        x.h = item - n * a.Hv;
+        x.u = run_of(a, n);
+        const bool live = x.u.valid && x.u.slot >= 0 && x.u.slot < a.n_slots;
+        x.m = live ? min(AHEAD, x.u.len) : 0;
+        x.more = 1, x.bad = 0;
+        x.tok = x.u.bos + lane;
+        if (a.token_indices) {
+            const int at = lane < x.m ? a.token_indices[(int64_t)n * a.n_steps + lane] : 0;
+            const uint32_t none = __ballot_sync(~0u, at < 0 || at >= a.T) & ((1u << x.m) - 1u);
+            if (none) {
+                x.m = __ffs(none) - 1;
+                x.more = 0, x.bad = __shfl_sync(~0u, at, x.m) >= 0;
+            }
+            x.tok = at;
+        }
+        x.g = x.beta = 0.f;
+        if (lane < x.m) {
+            x.g = a.g[x.u.b * a.sg.batch + x.h * a.sg.head + x.tok * a.sg.token];
+            x.beta = a.beta[x.u.b * a.sb.batch + x.h * a.sb.head + x.tok * a.sb.token];
+        }
+        return x;
+    };
+    auto fetch = [&](int i, const Ahead &x) {  // a whole warp: the i-th head of this CTA into its slot
+        const int slot = i % f.slots, hq = x.h / a.G;
+        const uint32_t at = smem_u32(sm) + slot * f.slot_bytes, bar_f = full + 8 * slot;
+        const bool live = x.u.valid && x.u.slot >= 0 && x.u.slot < a.n_slots;
+        if (lane < x.m) info[slot].a[lane] = expf(x.g), info[slot].b[lane] = x.beta;
+        __syncwarp();
+        if (lane == 0) {
+            info[slot].m = x.m, info[slot].more = x.more, info[slot].bad = x.bad;
+            issued[slot] = i / f.slots + 1;
+            const uint32_t row = (uint32_t)((a.o ? 2 : 1) * K + a.V) * (uint32_t)sizeof(IO);
+            if (live) {
+                mbar_arrive_expect_tx(bar_f, (uint32_t)f.state_bytes + x.m * row);
+                bulk_load(at, a.state + x.u.slot * a.slot_stride + (int64_t)x.h * K * a.V, (uint32_t)f.state_bytes, bar_f);
+            } else {
+                mbar_arrive(bar_f);
+            }
+        }
+        __syncwarp();
+        if (lane < x.m) {
+            const IO *k = static_cast<const IO *>(a.k) + x.u.b * a.sk.batch + hq * a.sk.head + x.tok * a.sk.token;
+            const IO *v = static_cast<const IO *>(a.v) + x.u.b * a.sv.batch + x.h * a.sv.head + x.tok * a.sv.token;
+            const uint32_t kb = K * sizeof(IO), vb = a.V * sizeof(IO), to = at + f.state_bytes;
+            bulk_load(to + lane * kb, k, kb, bar_f);
+            bulk_load(to + 2 * AHEAD * kb + lane * vb, v, vb, bar_f);
+            if (a.o) {
+                const IO *q = static_cast<const IO *>(a.q) + x.u.b * a.sq.batch + hq * a.sq.head + x.tok * a.sq.token;
+                bulk_load(to + (AHEAD + lane) * kb, q, kb, bar_f);
+            }
+        }
+    };
+    if (threadIdx.x < 32) {
+        if (lane == 0) {
+            for (int i = 0; i < f.slots; ++i) mbar_init(full + 8 * i, 1), issued[i] = 0;
+            *abort_flag = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        for (int i = 0, item = blockIdx.x; i < f.slots && item < heads; ++i, item += gridDim.x) fetch(i, look(item));
+    }
+    __syncthreads();
+    const int c = tid & 7, r = lane >> 3, at = 4 * r * a.V + (tid & ~31) + 4 * c;
+    Stage<K, IO> &s = *reinterpret_cast<Stage<K, IO> *>(stages + group * f.stage_bytes);
+    int i = group;
+    for (int item = blockIdx.x + group * gridDim.x; item < heads; item += f.groups * gridDim.x, i += f.groups) {
+        const int slot = i % f.slots, n = item / a.Hv, h = item - n * a.Hv;
+        const int next = item + f.slots * gridDim.x;
+        Ahead ahead;
+        if (tid < 32 && next < heads) ahead = look(next);
+        const Run u = run_of(a, n);
+        const Head<K, IO> head(a, s, u, n, h, h / a.G, 0, tid, a.V, bar);
+        const bool live = u.valid && u.slot >= 0 && u.slot < a.n_slots;
+        named_bar(bar, a.V);  // the stage is free
+        const bool ok = mbar_wait_warp(full + 8 * slot, (i / f.slots) & 1, abort_flag);
+        const unsigned char *from = sm + slot * f.slot_bytes;
+        const int m = info[slot].m;
+        const bool more = info[slot].more, bad = info[slot].bad;
+        float4 S[NR];
+        const float *src = reinterpret_cast<const float *>(from) + at;
+#pragma unroll
+        for (int j = 0; j < NR; ++j) S[j] = *reinterpret_cast<const float4 *>(src + (16 * (j >> 2) + (j & 3)) * a.V);
+        const uint4 *raw = reinterpret_cast<const uint4 *>(from + f.state_bytes);
+        constexpr int ROW = K * (int)sizeof(IO) / 16;
+        uint4 *sk = reinterpret_cast<uint4 *>(s.k), *sq = reinterpret_cast<uint4 *>(s.q);
+        for (int e = tid; e < m * ROW; e += a.V) {
+            sk[e] = raw[e];
+            if (a.o) sq[e] = raw[AHEAD * ROW + e];
+        }
+        const IO *raw_v = reinterpret_cast<const IO *>(raw + 2 * AHEAD * ROW) + tid;
+        for (int t = 0; t < m; ++t) s.v[t][tid] = raw_v[t * a.V];
+        if (tid < m) s.a[tid] = info[slot].a[tid], s.b[tid] = info[slot].b[tid];
+        if (!named_bar_and(bar, a.V, ok)) {  // a copy did not arrive in a second: none is left in flight
+            if (tid == 0)
+                for (int j = 0; j < f.slots; ++j)
+                    if (issued[j]) mbar_drain(full + 8 * j, (issued[j] - 1) & 1);
+            if (u.valid) head.fill(0, true);
+            return;
+        }
+        if (tid < 32 && next < heads) fetch(i + f.slots, ahead);
+        if (!live) {
+            if (u.valid) head.fill(0, u.slot >= 0);
+            continue;
+        }
+        if (!head.run(S, m, more, bad)) continue;
+        float *dst = head.out(h) + at;
+#pragma unroll
+        for (int j = 0; j < NR; ++j) *reinterpret_cast<float4 *>(dst + (16 * (j >> 2) + (j & 3)) * a.V) = S[j];
+    }
 }
 
 template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
-    const dim3 grid((unsigned)(a.n_seqs * a.Hv), 1);
-    k_recurrent<K, IO><<<grid, a.V, 0, st>>>(a);
+    const int64_t heads = (int64_t)a.n_seqs * a.Hv;
+    // rows that a bulk copy can take: multiples of 16 bytes apart
+    const int64_t strides = a.sk.batch | a.sk.token | a.sk.head | a.sv.batch | a.sv.token | a.sv.head |
+                            (a.o ? a.sq.batch | a.sq.token | a.sq.head : 0);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                         (a.o ? reinterpret_cast<uintptr_t>(a.q) : 0);
+    const bool rows16 = !((strides * (int64_t)sizeof(IO)) & 15) && !(at & 15);
+    if (heads >= 2 * kSMs && rows16) {  // several states for every SM
+        const Flow f = flow_of<K, IO>(a.V);
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = allow_smem(k_recurrent_flow<K, IO>, 232448, done);
+        if (e != cudaSuccess) return e;
+        k_recurrent_flow<K, IO><<<kSMs, 256, f.bytes, st>>>(a, f, (int)heads);
+    } else {  // a warp per CTA where that spreads the heads over more SMs
+        const int cols = heads * (a.V / kTile) <= 4 * kSMs ? kTile : a.V;
+        k_recurrent<K, IO><<<dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)(a.G * (a.V / cols))), cols, 0, st>>>(a);
+    }
     return cudaGetLastError();
 }
 

@@ -2,6 +2,8 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace gdn {
@@ -21,6 +23,19 @@ struct DecodeArgs {
     float scale;
 };
 
+// Allows a kernel `bytes` of dynamic shared memory, once per device and kernel (the setting stays with the context, and
+// setting it again costs about as much as a launch).
+template <typename Kernel> cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 cudaError_t launch_recurrent(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st);
 cudaError_t launch_tree(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st);
 
@@ -38,7 +53,7 @@ struct BeamArgs {
     float *out_scores;
     int32_t *out_tokens, *out_parents;
 };
-int beam_chunk(int64_t rows, int64_t vocab, gdn_dtype io);
+int beam_chunk(int64_t rows, int64_t vocab, int64_t n, gdn_dtype io);
 cudaError_t launch_beam(const BeamArgs &a, gdn_dtype io, cudaStream_t st);
 
 constexpr int kMaxViews = 32;

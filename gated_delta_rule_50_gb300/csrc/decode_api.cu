@@ -23,11 +23,11 @@ gdn_status decode_args(const gdn_decode_problem *p, const void *q, const void *k
         return GDN_ERR_INVALID_ARG;
     if (p->io_dtype != GDN_F32 && p->io_dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
     if ((p->K != 64 && p->K != 128) || (p->V != 64 && p->V != 128)) return GDN_ERR_UNSUPPORTED;
-    if (p->B > INT32_MAX || p->T > INT32_MAX || p->n_seqs > INT32_MAX || p->n_steps > INT32_MAX || p->Hv > 65535)
+    if (p->B > INT32_MAX || p->T > INT32_MAX || p->n_seqs > INT32_MAX || p->n_steps > INT32_MAX || p->Hv > 16383)
         return GDN_ERR_UNSUPPORTED;
     if (p->n_seqs < 0 || p->n_steps < 0 || p->n_slots < 0) return GDN_ERR_INVALID_ARG;
     if (p->cu_seqlens ? (p->B != 1 || p->token_indices) : p->n_seqs != p->B) return GDN_ERR_INVALID_ARG;
-    if (p->n_seqs * p->Hv > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (p->n_seqs * p->Hv > INT32_MAX / 2) return GDN_ERR_UNSUPPORTED;
     if (p->n_slots > 1 && p->slot_stride < p->Hv * p->K * p->V) return GDN_ERR_INVALID_ARG;
     if (p->slot_stride < 0 || p->slot_stride % 4) return GDN_ERR_INVALID_ARG;
     if (!p->state_indices && p->n_seqs > p->n_slots) return GDN_ERR_INVALID_ARG;
@@ -62,8 +62,7 @@ gdn_status beam_args(const gdn_beam_problem *p, BeamArgs *a) {
     a->logits_batch = p->logits_batch, a->logits_beam = p->logits_beam;
     a->mask_batch = p->mask_batch, a->mask_beam = p->mask_beam;
     a->B = (int)p->B, a->W = (int)p->W, a->vocab = (int)p->vocab, a->n = (int)p->n;
-    a->chunk = beam_chunk(p->B * p->W, p->vocab, p->logits_dtype);
-    // a row's vectors begin up to 7 elements before it
+    a->chunk = beam_chunk(p->B * p->W, p->vocab, p->n, p->logits_dtype);
     a->n_chunks = (int)((p->vocab + 7 + a->chunk - 1) / a->chunk);
     if (p->B * p->W * a->n_chunks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;

@@ -140,8 +140,8 @@ template <int K, typename IO> __global__ void __launch_bounds__(128) k_tree(cons
 
 template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
     const int bytes = tree_floats(a.T, K, a.V) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(k_tree<K, IO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               tree_floats(GDN_TREE_MAX, K, 128) * 4);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(k_tree<K, IO>, tree_floats(GDN_TREE_MAX, K, 128) * 4, done);
     if (e != cudaSuccess) return e;
     k_tree<K, IO><<<(unsigned)(a.n_seqs * a.Hv), a.V, bytes, st>>>(a);
     return cudaGetLastError();

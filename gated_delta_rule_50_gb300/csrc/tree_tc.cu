@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
 template <int K, int TP> cudaError_t launch(const DecodeArgs &a, bool vec, cudaStream_t st) {
     constexpr int bytes = (int)Map<K, TP>::bytes;
     static_assert(2 * (bytes + 1024) <= 233472, "two CTAs per SM");
-    const cudaError_t e = cudaFuncSetAttribute(k_tree_tc<K, TP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(k_tree_tc<K, TP>, bytes, done);
     if (e != cudaSuccess) return e;
     k_tree_tc<K, TP><<<dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)a.G), NT, bytes, st>>>(a, vec);
     return cudaGetLastError();

@@ -15,9 +15,11 @@ graph.  There is no CPU path and no backward: training runs through ``chunk_gate
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Sequence, Union
 
 import torch
+from torch._C import _cuda_getCurrentRawStream as _raw_stream
 
 from . import GDN_BF16, GDN_F32, GdnError, load_library
 
@@ -30,27 +32,15 @@ _CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 _I64 = ctypes.c_int64
 _P = ctypes.c_void_p
 
-
-class _Strides(ctypes.Structure):
-    _fields_ = [("batch", _I64), ("token", _I64), ("head", _I64)]
-
-
-class _DecodeProblem(ctypes.Structure):
-    _fields_ = ([(n, _I64) for n in ("B", "T", "Hq", "Hv", "K", "V")]
-                + [(n, _Strides) for n in ("q", "k", "v", "g", "beta")]
-                + [("io_dtype", ctypes.c_int), ("scale", ctypes.c_float), ("n_slots", _I64), ("slot_stride", _I64),
-                   ("state_indices", _P), ("n_seqs", _I64), ("cu_seqlens", _P), ("token_indices", _P),
-                   ("n_steps", _I64)])
-
-
-class _BeamProblem(ctypes.Structure):
-    _fields_ = ([(n, _I64) for n in ("B", "W", "vocab", "n", "logits_batch", "logits_beam", "mask_batch", "mask_beam")]
-                + [("logits_dtype", ctypes.c_int)])
-
-
-class _StateView(ctypes.Structure):
-    _fields_ = [("data", _P), ("slot_stride", _I64), ("slot_bytes", _I64)]
-
+# A decoding call takes a few microseconds on the GPU, so its way there is kept short: the C structures are packed
+# in one go (a ctypes structure of this size takes longer to fill than a launch) and the stream is taken as a number.
+#   gdn_decode_problem: B T Hq Hv K V, (batch, token, head) strides of q k v g beta, io_dtype scale, n_slots
+#   slot_stride, state_indices, n_seqs, cu_seqlens, token_indices, n_steps
+_DECODE = struct.Struct("@6q15qif2qPqPPq")
+#   gdn_beam_problem: B W vocab n, strides of logits and mask, dtype
+_BEAM = struct.Struct("@8qi0q")
+#   gdn_state_view
+_VIEW = struct.Struct("@P2q")
 
 _lib = None
 
@@ -59,13 +49,13 @@ def _library():
     global _lib
     if _lib is None:
         lib = load_library()
-        dp, bp = ctypes.POINTER(_DecodeProblem), ctypes.POINTER(_BeamProblem)
-        lib.gdn_recurrent.argtypes = [dp] + [_P] * 9
-        lib.gdn_tree.argtypes = [dp] + [_P] * 9
-        lib.gdn_beam_search_workspace_bytes.argtypes = [bp]
+        C = ctypes.c_char_p
+        lib.gdn_recurrent.argtypes = [C] + [_P] * 9
+        lib.gdn_tree.argtypes = [C] + [_P] * 9
+        lib.gdn_beam_search_workspace_bytes.argtypes = [C]
         lib.gdn_beam_search_workspace_bytes.restype = ctypes.c_size_t
-        lib.gdn_beam_search.argtypes = [bp] + [_P] * 8 + [ctypes.c_size_t, _P]
-        lib.gdn_reorder_states.argtypes = [ctypes.POINTER(_StateView)] + [_I64] * 4 + [_P] * 3
+        lib.gdn_beam_search.argtypes = [C] + [_P] * 8 + [ctypes.c_size_t, _P]
+        lib.gdn_reorder_states.argtypes = [C] + [_I64] * 4 + [_P] * 3
         for f in (lib.gdn_recurrent, lib.gdn_tree, lib.gdn_beam_search, lib.gdn_reorder_states):
             f.restype = ctypes.c_int
         _lib = lib
@@ -98,37 +88,44 @@ def _ints(t: Optional[torch.Tensor], name: str, shape, device) -> Optional[torch
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _call(where: str, fn, device: torch.device, *args):
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = fn(*args, _raw_stream(index))
     else:
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        rc = fn(*args, _raw_stream(index))
     if rc != 0:
         raise GdnError(rc, where)
 
 
-def _problem(q, k, v, g, beta, state, scale, state_indices):
-    """Checks what the two state operators share; returns (problem, tensors that it points to)."""
+def _inputs(q, k, v, g, beta, state):
+    """Checks what the two state operators share and makes the layouts that the kernels read."""
     dev = _device(k, "k")
     if k.dim() != 4 or v.dim() != 4:
         raise ValueError("k and v must have four dimensions: [B, T, heads, width]")
-    B, T, Hq, K = k.shape
-    Hv, V = v.shape[2], v.shape[3]
-    if k.dtype not in _CODES:
-        raise TypeError(f"unsupported io dtype {k.dtype} (bfloat16 or float32)")
+    B, T, _, K = k.shape
+    Hv, V = v.shape[2:]
+    dtype = k.dtype
+    if dtype not in _CODES:
+        raise TypeError(f"unsupported io dtype {dtype} (bfloat16 or float32)")
+    grad = k.requires_grad or v.requires_grad or g.requires_grad or beta.requires_grad or state.requires_grad
     if q is not None:
         _shape(q, "q", k.shape, dev)
+        if q.dtype != dtype:
+            raise TypeError("q, k and v must have one dtype")
+        grad = grad or q.requires_grad
+        if q.stride(3) != 1:
+            q = q.contiguous()
     _shape(v, "v", (B, T, Hv, V), dev)
-    for t, name in ((g, "g"), (beta, "beta")):
-        _shape(t, name, (B, T, Hv), dev)
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+    _shape(g, "g", (B, T, Hv), dev)
+    _shape(beta, "beta", (B, T, Hv), dev)
+    if v.dtype != dtype:
         raise TypeError("q, k and v must have one dtype")
-    if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad or g.requires_grad or beta.requires_grad
-                                    or state.requires_grad or (q is not None and q.requires_grad)):
+    if grad and torch.is_grad_enabled():
         raise ValueError("the decoding operators have no backward: call them under torch.no_grad(), or train through "
                          "chunk_gated_delta_rule")
     if state.dim() != 4 or state.shape[1:] != (Hv, K, V):
@@ -137,28 +134,28 @@ def _problem(q, k, v, g, beta, state, scale, state_indices):
         raise TypeError(f"state must be float32, got {state.dtype}")
     if state.device != dev:
         raise ValueError(f"state must be on {dev}, got {state.device}")
-    if state.numel() and state.stride()[1:] != (K * V, V, 1):
+    if not state.is_contiguous() and state.stride()[1:] != (K * V, V, 1):
         raise ValueError("every slot of state must be contiguous")
     if k.stride(3) != 1:
         k = k.contiguous()
     if v.stride(3) != 1:
         v = v.contiguous()
-    if q is not None and q.stride(3) != 1:
-        q = q.contiguous()
     if g.dtype != torch.float32:
         g = g.float()
     if beta.dtype != torch.float32:
         beta = beta.float()
-    p = _DecodeProblem()
-    p.B, p.T, p.Hq, p.Hv, p.K, p.V = B, T, Hq, Hv, K, V
-    if q is not None:
-        p.q = q.stride()[:3]
-    p.k, p.v, p.g, p.beta = k.stride()[:3], v.stride()[:3], g.stride(), beta.stride()
-    p.io_dtype = _CODES[k.dtype]
-    p.scale = K ** -0.5 if scale is None else scale
-    p.n_slots, p.slot_stride = state.shape[0], state.stride(0)
-    p.state_indices = _ptr(state_indices)
-    return p, q, k, v, g, beta
+    return dev, q, k, v, g, beta
+
+
+def _problem(q, k, v, g, beta, state, scale, state_indices, n_seqs, cu_seqlens=None, token_indices=None, n_steps=0):
+    B, T, Hq, K = k.shape
+    Hv, V = v.shape[2:]
+    k0, k1, k2, _ = k.stride()
+    q0, q1, q2, _ = k.stride() if q is None else q.stride()
+    v0, v1, v2, _ = v.stride()
+    return _DECODE.pack(B, T, Hq, Hv, K, V, q0, q1, q2, k0, k1, k2, v0, v1, v2, *g.stride(), *beta.stride(),
+                        _CODES[k.dtype], K ** -0.5 if scale is None else scale, state.shape[0], state.stride(0),
+                        _ptr(state_indices), n_seqs, _ptr(cu_seqlens), _ptr(token_indices), n_steps)
 
 
 def recurrent_gated_delta_rule(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
@@ -181,10 +178,11 @@ def recurrent_gated_delta_rule(q: Optional[torch.Tensor], k: torch.Tensor, v: to
                        share a slot, as beams that continue one parent do.  Must not overlap ``state``.
     q = None           only the states move; returns None.
     """
-    dev = _device(k, "k")
-    n_seqs = k.shape[0]
+    dev, q, k, v, g, beta = _inputs(q, k, v, g, beta, state)
+    B, steps, Hv, V = v.shape
+    n_seqs = B
     if cu_seqlens is not None:
-        if k.shape[0] != 1:
+        if B != 1:
             raise ValueError("cu_seqlens needs B = 1")
         if token_indices is not None:
             raise ValueError("token_indices and cu_seqlens exclude each other")
@@ -192,22 +190,19 @@ def recurrent_gated_delta_rule(q: Optional[torch.Tensor], k: torch.Tensor, v: to
             raise ValueError("cu_seqlens must have one dimension and at least one entry")
         cu_seqlens = _ints(cu_seqlens, "cu_seqlens", cu_seqlens.shape, dev)
         n_seqs = cu_seqlens.shape[0] - 1
-    state_indices = _ints(state_indices, "state_indices", (n_seqs,), dev)
-    p, q, k, v, g, beta = _problem(q, k, v, g, beta, state, scale, state_indices)
-    B, T, Hv, V = v.shape
-    p.n_seqs, p.cu_seqlens = n_seqs, _ptr(cu_seqlens)
-    steps = T
     if token_indices is not None:
         if token_indices.dim() != 2:
             raise ValueError("token_indices must have two dimensions")
         steps = token_indices.shape[1]
         token_indices = _ints(token_indices, "token_indices", (B, steps), dev)
-        p.token_indices, p.n_steps = _ptr(token_indices), steps
+    state_indices = _ints(state_indices, "state_indices", (n_seqs,), dev)
     if out_state is not None:
         _shape(out_state, "out_state", (n_seqs,) + state.shape[1:], dev)
         if out_state.dtype != torch.float32 or not out_state.is_contiguous():
             raise ValueError("out_state must be contiguous float32")
-    o = None if q is None else torch.empty(B, steps, Hv, V, dtype=k.dtype, device=dev)
+    p = _problem(q, k, v, g, beta, state, scale, state_indices, n_seqs, cu_seqlens, token_indices,
+                 0 if token_indices is None else steps)
+    o = None if q is None else torch.empty((B, steps, Hv, V), dtype=k.dtype, device=dev)
     _call("gdn_recurrent", _library().gdn_recurrent, dev, p, _ptr(q), k.data_ptr(), v.data_ptr(), g.data_ptr(),
           beta.data_ptr(), state.data_ptr(), _ptr(out_state), _ptr(o))
     return o
@@ -223,13 +218,13 @@ def tree_gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
     arguments as recurrent_gated_delta_rule.  Returns o [B,T,Hv,V]: what each token's path would give.  Move the
     state along the accepted path with recurrent_gated_delta_rule(None, ..., token_indices=path).
     """
-    dev = _device(k, "k")
     if q is None:
         raise ValueError("q must be given")
-    state_indices = _ints(state_indices, "state_indices", (k.shape[0],), dev)
+    dev, q, k, v, g, beta = _inputs(q, k, v, g, beta, state)
+    B = k.shape[0]
+    state_indices = _ints(state_indices, "state_indices", (B,), dev)
     parents = _ints(parents, "parents", k.shape[:2], dev)
-    p, q, k, v, g, beta = _problem(q, k, v, g, beta, state, scale, state_indices)
-    p.n_seqs = k.shape[0]
+    p = _problem(q, k, v, g, beta, state, scale, state_indices, B)
     o = torch.empty(v.shape, dtype=k.dtype, device=dev)
     _call("gdn_tree", _library().gdn_tree, dev, p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
           beta.data_ptr(), parents.data_ptr(), state.data_ptr(), o.data_ptr())
@@ -263,7 +258,7 @@ def beam_search_step(logits: torch.Tensor, scores: torch.Tensor, finished: Optio
     if logits.stride(2) != 1:
         logits = logits.contiguous()
     scores = scores.contiguous()
-    p = _BeamProblem(B, W, vocab, n, logits.stride(0), logits.stride(1), 0, 0, _CODES[logits.dtype])
+    mask_batch = mask_beam = 0
     if finished is not None:
         _shape(finished, "finished", (B, W), dev)
         if finished.dtype != torch.bool:
@@ -280,17 +275,17 @@ def beam_search_step(logits: torch.Tensor, scores: torch.Tensor, finished: Optio
             raise ValueError(f"mask must be broadcastable to {(B, W, vocab)}, got {tuple(mask.shape)}") from None
         if mask.stride(2) != 1:
             mask = mask.contiguous()
-        p.mask_batch, p.mask_beam = mask.stride(0), mask.stride(1)
+        mask_batch, mask_beam, _ = mask.stride()
     lib = _library()
+    p = _BEAM.pack(B, W, vocab, n, logits.stride(0), logits.stride(1), mask_batch, mask_beam, _CODES[logits.dtype])
     need = lib.gdn_beam_search_workspace_bytes(p)
     if need == 0:
         raise GdnError(2, "gdn_beam_search")
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    out_scores = torch.empty(B, n, dtype=torch.float32, device=dev)
-    tokens = torch.empty(2, B, n, dtype=torch.int32, device=dev)
-    parents = tokens[1]
-    tokens = tokens[0]
+    out_scores = torch.empty((B, n), dtype=torch.float32, device=dev)
+    tokens = torch.empty((B, n), dtype=torch.int32, device=dev)
+    parents = torch.empty((B, n), dtype=torch.int32, device=dev)
     _call("gdn_beam_search", lib.gdn_beam_search, dev, p, logits.data_ptr(), scores.data_ptr(), _ptr(finished),
           _ptr(mask), out_scores.data_ptr(), tokens.data_ptr(), parents.data_ptr(), workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
@@ -319,16 +314,15 @@ def reorder_states(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents:
     parents = _ints(parents, "parents", (B, W), dev)
     state_indices = _ints(state_indices, "state_indices", (B, W), dev)
     slots = states[0].shape[0]
-    views = (_StateView * len(states))()
-    for view, s in zip(views, states):
+    views = b""
+    for s in states:
         if s.dim() < 1 or s.shape[0] != slots:
             raise ValueError("all states must have the same number of slots")
         if s.device != dev:
             raise ValueError(f"states must be on {dev}, got {s.device}")
-        if s.numel() and not s[0].is_contiguous():
+        if not s.is_contiguous() and s.numel() and not s[0].is_contiguous():
             raise ValueError("every slot of a state must be contiguous")
         size = s.element_size()
-        view.data, view.slot_stride = s.data_ptr(), s.stride(0) * size
-        view.slot_bytes = s.numel() // slots * size if slots else 0
+        views += _VIEW.pack(s.data_ptr(), s.stride(0) * size, s.numel() // slots * size if slots else 0)
     _call("gdn_reorder_states", _library().gdn_reorder_states, dev, views, len(states), slots, B, W,
           parents.data_ptr(), _ptr(state_indices))

@@ -1,5 +1,4 @@
 """What the decoding calls refuse, and with which error; nothing here reaches a kernel."""
-import ctypes
 import os
 import subprocess
 import sys
@@ -144,13 +143,10 @@ sys.path.insert(0, ROOT)
 from gated_delta_rule_50_gb300 import decode as d
 lib = d._library()
 A = 4096
-def prob(**kw):
-    p = d._DecodeProblem()
-    p.B, p.T, p.Hq, p.Hv, p.K, p.V = 2, 3, 2, 4, 128, 128
-    p.io_dtype, p.scale, p.n_slots, p.slot_stride, p.n_seqs = 1, 0.1, 5, 4 * 128 * 128, 2
-    for k, v in kw.items():
-        setattr(p, k, v)
-    return p
+def prob(B=2, T=3, Hq=2, Hv=4, K=128, V=128, io_dtype=1, n_slots=5, slot_stride=4 * 128 * 128, state_indices=0, n_seqs=2,
+         cu_seqlens=0, token_indices=0, n_steps=0):
+    return d._DECODE.pack(B, T, Hq, Hv, K, V, *[128] * 15, io_dtype, 0.1, n_slots, slot_stride, state_indices, n_seqs,
+                          cu_seqlens, token_indices, n_steps)
 def rec(p, q=A, k=A, v=A, g=A, b=A, s=A, out=None, o=A):
     return lib.gdn_recurrent(p, q, k, v, g, b, s, out, o, None)
 def tree(p, q=A, k=A, v=A, g=A, b=A, par=A, s=A, o=A):
@@ -165,11 +161,8 @@ out = dict(
     overlap=rec(prob(), out=A + 4 * 128 * 128 * 4 * 4), nothing=rec(prob(B=0, n_seqs=0)),
     t_parents=tree(prob(), par=None), t_wide=tree(prob(T=65)), t_cu=tree(prob(B=1, n_seqs=1, cu_seqlens=A)),
     t_nothing=tree(prob(T=0)))
-def beam(**kw):
-    p = d._BeamProblem(2, 3, 100, 4, 300, 100, 0, 0, 1)
-    for k, v in kw.items():
-        setattr(p, k, v)
-    return p
+def beam(B=2, W=3, vocab=100, n=4, logits_dtype=1):
+    return d._BEAM.pack(B, W, vocab, n, 300, 100, 0, 0, logits_dtype)
 def search(p, logits=A, scores=A, o=A, ws=A, n=1 << 30):
     return lib.gdn_beam_search(p, logits, scores, None, None, o, A, A, ws, n, None)
 out.update(b_ws=lib.gdn_beam_search_workspace_bytes(beam()) > 0, b_bad=lib.gdn_beam_search_workspace_bytes(beam(n=0)),
@@ -177,8 +170,7 @@ out.update(b_ws=lib.gdn_beam_search_workspace_bytes(beam()) > 0, b_bad=lib.gdn_b
     b_dtype=search(beam(logits_dtype=5)), b_null=search(beam(), logits=None), b_odd=search(beam(), logits=A + 1),
     b_small=search(beam(), n=64), b_ws_odd=search(beam(), ws=A + 16), b_nothing=search(beam(B=0)))
 def reorder(data=A, stride=64, size=64, slots=8, B=2, W=4, par=A):
-    v = (d._StateView * 1)(d._StateView(data, stride, size))
-    return lib.gdn_reorder_states(v, 1, slots, B, W, par, None, None)
+    return lib.gdn_reorder_states(d._VIEW.pack(data or 0, stride, size), 1, slots, B, W, par, None, None)
 out.update(r_null=reorder(data=None), r_stride=reorder(stride=32), r_slots=reorder(slots=7), r_W=reorder(W=65),
     r_parents=reorder(par=None), r_nothing=reorder(B=0), r_views=lib.gdn_reorder_states(None, 1, 8, 2, 4, A, None, None))
 print(repr(out))
@@ -201,7 +193,7 @@ def test_c_entries_refuse_on_the_host():
 
 
 def test_struct_sizes_match_the_header(tmp_path):
-    """The ctypes mirrors have the C structures' sizes."""
+    """What the binding packs has the C structures' sizes."""
     import shutil
     if shutil.which("gcc") is None:
         pytest.skip("no C compiler")
@@ -211,4 +203,4 @@ def test_struct_sizes_match_the_header(tmp_path):
     exe = tmp_path / "s"
     subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     sizes = [int(n) for n in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
-    assert sizes == [ctypes.sizeof(c) for c in (decode._DecodeProblem, decode._BeamProblem, decode._StateView)]
+    assert sizes == [c.size for c in (decode._DECODE, decode._BEAM, decode._VIEW)]
