@@ -7,7 +7,7 @@
 // threads hold anything above it; a warp reads each of those threads' elements again (from the caches) and what
 // is left, at most n times a thread's elements whatever the order of the input, is ranked by counting.
 // k_beam_pick: a CTA per search joins the chunks' sums into the beams' normalisers, turns the keys into
-// scores and selects in the same way.  It is launched beside the first kernel and waits for its end on the GPU.
+// scores and selects in the same way.
 // No result depends on the order in which threads arrive: places of collected keys do, their ranks do not.
 //
 // The sum is one of 2^(c x - m) with c = log2 e in fp32: one multiply-add and one exp2 per logit, and the same c
@@ -71,31 +71,29 @@ __device__ __forceinline__ float normaliser(float m, float s) {
 }
 
 struct Nth {  // shared memory of nth_largest
-    uint64_t warp[kThreads / 32], heads[kThreads], answer;
+    uint32_t warp[kThreads / 32];
+    uint64_t heads[kThreads], answer;
     int count;
 };
 // The n-th largest of the 256 threads' keys (all different, but for 0) to all threads; 0 if there are fewer.
-// The n-th largest of any one warp bounds it from below: each warp sorts its keys, what reaches the best of the
-// eight bounds is ranked by counting.
-__device__ __forceinline__ uint64_t nth_largest(uint64_t key, int n, Nth &sh) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t x = key;
+// `value` is the upper half of this thread's key, key() the whole of it, asked for where it can matter: the least of
+// the maxima of n groups or more bounds the n-th largest from below, and what reaches it is ranked by counting.
+template <typename Key>
+__device__ __forceinline__ uint64_t nth_largest(uint32_t value, Key key, int n, Nth &sh) {
+    const int groups = n <= 8 ? 1 : n <= 16 ? 2 : n <= 32 ? 4 : 8;  // of a warp
+    uint32_t v = value;
 #pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int step = size >> 1; step; step >>= 1) {
-            const uint64_t y = __shfl_xor_sync(~0u, x, step);
-            const bool larger = ((lane & step) == 0) == ((lane & size) == 0);  // descending
-            x = (x > y) == larger ? x : y;
-        }
-    const uint64_t bound = __shfl_sync(~0u, x, n <= 32 ? n - 1 : 31);
-    if (lane == 0) sh.warp[warp] = n <= 32 ? bound : 0;
+    for (int step = 1; step < 32; step <<= 1) {
+        const uint32_t y = __shfl_xor_sync(~0u, v, step);
+        v = step * groups < 32 ? max(v, y) : min(v, y);
+    }
+    if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = v;
     if (threadIdx.x == 0) sh.answer = 0, sh.count = 0;
     __syncthreads();
-    uint64_t low = 0;
+    uint32_t low = ~0u;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) low = sh.warp[w] > low ? sh.warp[w] : low;
-    if (key && key >= low) sh.heads[atomicAdd(&sh.count, 1)] = key;
+    for (int w = 0; w < kThreads / 32; ++w) low = min(low, sh.warp[w]);
+    if (value && value >= low) sh.heads[atomicAdd(&sh.count, 1)] = key();
     __syncthreads();
     const int count = sh.count;
     if ((int)threadIdx.x < count) {
@@ -106,6 +104,25 @@ __device__ __forceinline__ uint64_t nth_largest(uint64_t key, int n, Nth &sh) {
     }
     __syncthreads();
     return sh.answer;
+}
+// Two fp32 operations at once, on a pair of registers
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void halves(uint64_t p, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 template <typename IO> struct Pack;
@@ -152,45 +169,42 @@ template <> struct Pack<float> {
 };
 
 // One beam's logits as vectors on 16-byte boundaries: the first may begin before the row, the last end after it
-template <typename IO> struct Row {
+template <typename IO, bool MASK> struct Row {
     static constexpr int N = Pack<IO>::N;
     const IO *x;
     const uint8_t *mask;
     bool mask_whole;  // a vector's mask bytes are aligned too
     int vocab;
 
-    // elements [at, at + N); what is outside or masked is -inf
-    __device__ __forceinline__ uint4 load(int at) const {
-        uint4 u;
-        if (at >= 0 && at + N <= vocab) {
-            u = *reinterpret_cast<const uint4 *>(x + at);
-            if (mask) {
-                if (mask_whole) {
-                    Pack<IO>::apply(u, mask + at);
-                } else {
-                    alignas(8) uint32_t m[2] = {0, 0};
+    // elements [at, at + N), all in the row; what is masked is -inf
+    __device__ __forceinline__ uint4 inside(int at) const {
+        uint4 u = *reinterpret_cast<const uint4 *>(x + at);
+        if (MASK) {
+            if (mask_whole) {
+                Pack<IO>::apply(u, mask + at);
+            } else {
+                alignas(8) uint32_t m[2] = {0, 0};
 #pragma unroll
-                    for (int i = 0; i < N; ++i) m[i >> 2] |= (uint32_t)mask[at + i] << (8 * (i & 3));
-                    Pack<IO>::apply(u, reinterpret_cast<const uint8_t *>(m));
-                }
+                for (int i = 0; i < N; ++i) m[i >> 2] |= (uint32_t)mask[at + i] << (8 * (i & 3));
+                Pack<IO>::apply(u, reinterpret_cast<const uint8_t *>(m));
             }
-        } else {
-            u = edge(at);
         }
         return u;
     }
+    // elements [at, at + N); what is outside too is -inf
+    __device__ __forceinline__ uint4 load(int at) const { return at >= 0 && at + N <= vocab ? inside(at) : edge(at); }
     __device__ __noinline__ uint4 edge(int at) const {
         IO v[N];
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            v[i] = at + i >= 0 && at + i < vocab && (!mask || mask[at + i]) ? x[at + i] : from_f<IO>(-INFINITY);
+            v[i] = at + i >= 0 && at + i < vocab && (!MASK || mask[at + i]) ? x[at + i] : from_f<IO>(-INFINITY);
         uint4 u;
         memcpy(&u, v, 16);
         return u;
     }
 };
 
-template <typename IO> __global__ void __launch_bounds__(kThreads, 6) k_beam_scan(const BeamArgs a) {
+template <typename IO, bool MASK> __global__ void __launch_bounds__(kThreads, 6) k_beam_scan(const BeamArgs a) {
     constexpr int N = Pack<IO>::N, STEP = kThreads * N;
     extern __shared__ uint64_t s_got[];  // n times the elements per thread
     __shared__ Nth sh;
@@ -198,56 +212,69 @@ template <typename IO> __global__ void __launch_bounds__(kThreads, 6) k_beam_sca
     __shared__ int s_count, s_list[GDN_BEAM_MAX], s_listed;
     const int tid = threadIdx.x, lane = tid & 31, n = a.n;
     const int row = blockIdx.x / a.n_chunks, chunk = blockIdx.x - row * a.n_chunks;
-    asm volatile("griddepcontrol.launch_dependents;");  // the next kernel may take its place; it waits for this one's end
+    wait_for_previous();
     if (a.finished && a.finished[row]) return;
     const int b = row / a.W, w = row - b * a.W;
-    Row<IO> x;
+    Row<IO, MASK> x;
     x.x = static_cast<const IO *>(a.logits) + b * a.logits_batch + w * a.logits_beam;
-    x.mask = a.mask ? a.mask + b * a.mask_batch + w * a.mask_beam : nullptr;
+    x.mask = MASK ? a.mask + b * a.mask_batch + w * a.mask_beam : nullptr;
     x.vocab = a.vocab;
     const int shift = (int)((reinterpret_cast<uintptr_t>(x.x) & 15) / sizeof(IO));
     x.mask_whole = ((reinterpret_cast<uintptr_t>(x.mask) - shift) & (N - 1)) == 0;
     const int first = chunk * a.chunk - shift, begin = first + tid * N;
     const int end = min(first + a.chunk, a.vocab);
 
-    float best = -INFINITY, m = 0.f, s0 = 0.f, s1 = 0.f;  // m: at most c * best, 0 before there is one
+    float best = -INFINITY, m = 0.f;  // m: at most c * best, 0 before there is one
+    uint64_t sum = 0, neg_m = 0;      // pairs: the even and the odd elements' sums; -m twice
+    const uint64_t c2 = pair_of(kLog2e, kLog2e);
     int best_at = begin;
     auto take = [&](const uint4 &u, int at) {
         const float top = Pack<IO>::max(u);
         if (top > best) {
             if (best == -INFINITY || fmaf(top, kLog2e, -m) > kSlack) {
                 const float f = best == -INFINITY ? 1.f : exp2_of(fmaf(top, -kLog2e, m));
-                s0 *= f, s1 *= f, m = kLog2e * top;
+                sum = fma2(sum, pair_of(f, f), 0);
+                m = kLog2e * top, neg_m = pair_of(-m, -m);
             }
             best = top, best_at = at;
         }
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            s0 += exp2_of(fmaf(Pack<IO>::get(u, i), kLog2e, -m));
-            s1 += exp2_of(fmaf(Pack<IO>::get(u, i + 1), kLog2e, -m));
+            float e0, e1;
+            halves(fma2(pair_of(Pack<IO>::get(u, i), Pack<IO>::get(u, i + 1)), c2, neg_m), e0, e1);
+            sum = add2(sum, pair_of(exp2_of(e0), exp2_of(e1)));
         }
     };
+    // a row's first vector may begin before it and its last one end after it: all others are read as they are
     int at = begin;
-    for (; at + 3 * STEP < end; at += 4 * STEP) {
+    if (at < 0) take(x.edge(at), at), at += STEP;
+    const int whole = min(end, a.vocab - N + 1);
+    for (; at + 3 * STEP < whole; at += 4 * STEP) {
         uint4 u[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = x.load(at + j * STEP);
+        for (int j = 0; j < 4; ++j) u[j] = x.inside(at + j * STEP);
 #pragma unroll
         for (int j = 0; j < 4; ++j) take(u[j], at + j * STEP);
     }
-    for (; at < end; at += STEP) take(x.load(at), at);
-    uint64_t mine = 0;
-    if (best > -INFINITY) {
-        const uint4 u = x.load(best_at);
-#pragma unroll
-        for (int i = N - 1; i >= 0; --i)
-            if (Pack<IO>::get(u, i) == best) mine = make_key(best, best_at + i);
-    }
-    float ms = best == -INFINITY ? -INFINITY : m, s = s0 + s1;
+    for (; at < whole; at += STEP) take(x.inside(at), at);
+    if (at < end) take(x.edge(at), at);
+    float s, s_odd, ms = best == -INFINITY ? -INFINITY : m;
+    halves(sum, s, s_odd);
+    s += s_odd;
     join_warp(ms, s);
     if (tid == 0) s_count = 0, s_listed = 0;
     if (lane == 0) s_stat[tid >> 5] = make_float2(ms, s);
-    const uint64_t low = nth_largest(mine, n, sh);
+    uint64_t mine = 0;
+    const uint64_t low = nth_largest(
+        best > -INFINITY ? ordered(best) : 0u,
+        [&] {
+            const uint4 u = x.load(best_at);
+#pragma unroll
+            for (int i = N - 1; i >= 0; --i)
+                if (Pack<IO>::get(u, i) == best) mine = make_key(best, best_at + i);
+            return mine;
+        },
+        n, sh);
     const int64_t unit = blockIdx.x;
     if (tid < 32) {
         const float2 st = lane < kThreads / 32 ? s_stat[lane] : make_float2(-INFINITY, 0.f);
@@ -256,10 +283,12 @@ template <typename IO> __global__ void __launch_bounds__(kThreads, 6) k_beam_sca
         if (lane == 0) a.stats[unit] = make_float2(ms, s);
     }
     if (mine && mine >= low) s_list[atomicAdd(&s_listed, 1)] = tid;
+    const float low_value = low ? key_value(low) : -INFINITY;
     __syncthreads();
     for (int e = tid >> 5; e < s_listed; e += kThreads / 32)
         for (int v = first + s_list[e] * N + lane * STEP; v < end; v += 32 * STEP) {
             const uint4 u = x.load(v);
+            if (Pack<IO>::max(u) < low_value) continue;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const uint64_t key = make_key(Pack<IO>::get(u, i), v + i);
@@ -286,17 +315,17 @@ __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
     __shared__ int s_count;
     const int tid = threadIdx.x, lane = tid & 31, n = a.n, W = a.W, b = blockIdx.x;
     const int lists = W * a.n_chunks, total = lists * n;
+    wait_for_previous();
     const uint64_t *keys = a.keys + (int64_t)b * total;
     if (tid < W) s_score[tid] = a.scores[b * W + tid], s_done[tid] = a.finished && a.finished[b * W + tid];
     if (tid == 0) s_count = 0;
-    __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const bool few = total <= kPickKeys * kThreads;
     uint64_t held[kPickKeys];
     if (few) {
 #pragma unroll
         for (int i = 0; i < kPickKeys; ++i) held[i] = tid + i * kThreads < total ? __ldcg(keys + tid + i * kThreads) : 0;
     }
+    __syncthreads();
     for (int w = tid >> 5; w < W; w += kThreads / 32) {
         float m = -INFINITY, s = 0.f;
         if (!s_done[w])
@@ -325,7 +354,7 @@ __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
             if (e < total) held[i] = entry(e / n, e % n, held[i]);
             mine = held[i] > mine ? held[i] : mine;
         }
-        const uint64_t low = nth_largest(mine, n, sh);
+        const uint64_t low = nth_largest((uint32_t)(mine >> 32), [&] { return mine; }, n, sh);
         if (mine >= low)
 #pragma unroll
             for (int i = 0; i < kPickKeys; ++i)
@@ -335,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
             const uint64_t head = read(l, 0);
             mine = head > mine ? head : mine;
         }
-        uint64_t low = nth_largest(mine, n, sh);
+        uint64_t low = nth_largest((uint32_t)(mine >> 32), [&] { return mine; }, n, sh);
         if (lists > kThreads) {  // the n-th largest head itself, so that no more than n lists are opened
             if (mine && mine >= low)
                 for (int l = tid; l < lists; l += kThreads) {
@@ -388,26 +417,20 @@ __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
     }
 }
 
-template <typename IO> cudaError_t launch(const BeamArgs &a, cudaStream_t st) {
+template <typename IO, bool MASK> cudaError_t scan(const BeamArgs &a, int lists, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = allow_smem(k_beam_scan<IO>, kMaxGot * 8, done);
+    const cudaError_t e = allow_smem(k_beam_scan<IO, MASK>, kMaxGot * 8, done);
     if (e != cudaSuccess) return e;
+    return launch_behind(k_beam_scan<IO, MASK>, dim3((unsigned)(a.B * lists)), kThreads, (size_t)a.n * (a.chunk / kThreads) * 8, st, a);
+}
+
+template <typename IO> cudaError_t launch(const BeamArgs &a, cudaStream_t st) {
     const int lists = a.W * a.n_chunks;
-    k_beam_scan<IO><<<(unsigned)(a.B * lists), kThreads, a.n * (a.chunk / kThreads) * 8, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaError_t e = a.mask ? scan<IO, true>(a, lists, st) : scan<IO, false>(a, lists, st);
+    if (e != cudaSuccess) return e;
     // keys collected at once: n threads' or n lists', or the heads of n threads' lists
     const int per = lists * a.n <= kPickKeys * kThreads ? kPickKeys : a.n, heads = (lists + kThreads - 1) / kThreads;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.B);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)a.n * (per > heads ? per : heads) * 8;
-    cfg.stream = st;
-    cudaLaunchAttribute at = {};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_beam_pick, a);
+    return launch_behind(k_beam_pick, dim3((unsigned)a.B), kThreads, (size_t)a.n * (per > heads ? per : heads) * 8, st, a);
 }
 
 }  // namespace

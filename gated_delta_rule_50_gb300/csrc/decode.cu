@@ -208,6 +208,7 @@ template <int K, typename IO> __global__ void __launch_bounds__(128) k_recurrent
     __shared__ Stage<K, IO> s;
     const int tid = threadIdx.x, cols = blockDim.x;
     const int n = blockIdx.x, hq = blockIdx.y, h = hq * a.G + blockIdx.z % a.G, col0 = blockIdx.z / a.G * cols;
+    wait_for_previous();
     const Run u = run_of(a, n);
     if (!u.valid) return;
     const Head<K, IO> head(a, s, u, n, h, hq, col0, tid, cols, 1);
@@ -336,8 +337,10 @@ __global__ void __launch_bounds__(256, 1) k_recurrent_flow(const __grid_constant
             fence_mbar_init();
         }
         __syncwarp();
+        wait_for_previous();
         for (int i = 0, item = blockIdx.x; i < f.slots && item < heads; ++i, item += gridDim.x) fetch(i, look(item));
     }
+    if (threadIdx.x >= 32) wait_for_previous();
     __syncthreads();
     const int c = tid & 7, r = lane >> 3, at = 4 * r * a.V + (tid & ~31) + 4 * c;
     Stage<K, IO> &s = *reinterpret_cast<Stage<K, IO> *>(stages + group * f.stage_bytes);
@@ -401,12 +404,11 @@ template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = allow_smem(k_recurrent_flow<K, IO>, 232448, done);
         if (e != cudaSuccess) return e;
-        k_recurrent_flow<K, IO><<<kSMs, 256, f.bytes, st>>>(a, f, (int)heads);
+        return launch_behind(k_recurrent_flow<K, IO>, dim3(kSMs), 256, f.bytes, st, a, f, (int)heads);
     } else {  // a warp per CTA where that spreads the heads over more SMs
         const int cols = heads * (a.V / kTile) <= 4 * kSMs ? kTile : a.V;
-        k_recurrent<K, IO><<<dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)(a.G * (a.V / cols))), cols, 0, st>>>(a);
+        return launch_behind(k_recurrent<K, IO>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)(a.G * (a.V / cols))), cols, 0, st, a);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace

@@ -36,6 +36,27 @@ template <typename Kernel> cudaError_t allow_smem(Kernel kernel, int bytes, std:
     return e;
 }
 
+// The decoding kernels follow each other closely: each is launched so that its CTAs may take their places while the
+// stream's previous kernel ends, and waits on the GPU for that end (and for its writes) before it touches memory.
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... Params>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int block, size_t smem, cudaStream_t st, Params... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_recurrent(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st);
 cudaError_t launch_tree(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st);
 

@@ -44,6 +44,7 @@ template <int K, typename IO> __global__ void __launch_bounds__(128) k_tree(cons
     IO *o = static_cast<IO *>(a.o) + ((int64_t)n * T * a.Hv + h) * V;
     const int64_t o_tok = (int64_t)a.Hv * V;
 
+    wait_for_previous();
     const int64_t slot = a.state_indices ? a.state_indices[n] : n;
     if (slot < 0 || slot >= a.n_slots) {
         for (int t = 0; t < T; ++t) o[t * o_tok + tid] = from_f<IO>(slot < 0 ? 0.f : __int_as_float(0x7fffffff));
@@ -143,8 +144,7 @@ template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k_tree<K, IO>, tree_floats(GDN_TREE_MAX, K, 128) * 4, done);
     if (e != cudaSuccess) return e;
-    k_tree<K, IO><<<(unsigned)(a.n_seqs * a.Hv), a.V, bytes, st>>>(a);
-    return cudaGetLastError();
+    return launch_behind(k_tree<K, IO>, dim3((unsigned)(a.n_seqs * a.Hv)), a.V, bytes, st, a);
 }
 
 }  // namespace

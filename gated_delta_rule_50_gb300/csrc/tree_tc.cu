@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)n * T * a.Hv + h) * V;
     const int64_t o_tok = (int64_t)a.Hv * V;
 
+    wait_for_previous();
     const int64_t slot = a.state_indices ? a.state_indices[n] : n;
     int2 *s_up = reinterpret_cast<int2 *>(sm + M::VEC);  // e^g (its bits) and the parent
     float *s_b = reinterpret_cast<float *>(s_up + TP), *s_bg = s_b + TP, *s_sg = s_bg + TP;
@@ -482,8 +483,7 @@ template <int K, int TP> cudaError_t launch(const DecodeArgs &a, bool vec, cudaS
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k_tree_tc<K, TP>, bytes, done);
     if (e != cudaSuccess) return e;
-    k_tree_tc<K, TP><<<dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)a.G), NT, bytes, st>>>(a, vec);
-    return cudaGetLastError();
+    return launch_behind(k_tree_tc<K, TP>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)a.G), NT, bytes, st, a, vec);
 }
 
 template <int K> cudaError_t launch_width(const DecodeArgs &a, bool vec, cudaStream_t st) {
