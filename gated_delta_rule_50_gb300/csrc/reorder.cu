@@ -16,38 +16,45 @@ template <> __device__ __forceinline__ uint8_t filled<uint8_t>() { return 0xFF; 
 
 // grid: (offsets, searches, views); MAXW slots at once in registers
 template <int MAXW, typename Vec> __global__ void __launch_bounds__(256) k_reorder(const __grid_constant__ ReorderArgs a) {
-    __shared__ int64_t s_slot[MAXW];
-    __shared__ uint64_t s_followers[MAXW], s_fill;
+    __shared__ unsigned char *s_from[MAXW], *s_to[MAXW], *s_fill[MAXW];  // slots; followers by source; slots to fill
+    __shared__ uint64_t s_followers[MAXW];
+    __shared__ int s_begin[MAXW], s_count[MAXW], s_listed, s_fills;
     const int b = blockIdx.y, tid = threadIdx.x, W = a.W;
     const auto &view = a.view[blockIdx.z];
+    const int64_t n = view.bytes / (int64_t)sizeof(Vec), first = blockIdx.x * (int64_t)blockDim.x + tid;
+    if (first - tid >= n) return;
     wait_for_previous();
-    int64_t slot = -1;
+    unsigned char *slot = nullptr;
     int p = -1;
     if (tid < W) {
         p = a.parents[(int64_t)b * W + tid];
-        slot = a.state_indices ? a.state_indices[(int64_t)b * W + tid] : (int64_t)b * W + tid;
-        if (slot >= a.n_slots) slot = -1;
+        const int64_t i = a.state_indices ? a.state_indices[(int64_t)b * W + tid] : (int64_t)b * W + tid;
+        if (i >= 0 && i < a.n_slots) slot = view.data + i * view.stride;
     }
-    if (tid < MAXW) s_slot[tid] = slot, s_followers[tid] = 0;
-    if (tid == 0) s_fill = 0;
+    if (tid < MAXW) s_from[tid] = slot, s_followers[tid] = 0;
+    if (tid == 0) s_listed = s_fills = 0;
     __syncthreads();
-    if (tid < W && slot >= 0 && p >= 0 && p != tid) {
-        const bool none = p >= W || s_slot[p] < 0;
-        atomicOr(reinterpret_cast<unsigned long long *>(none ? &s_fill : &s_followers[p]), 1ull << tid);
+    const bool moves = tid < W && slot && p >= 0 && p != tid, follows = moves && p < W && s_from[p];
+    if (follows) atomicOr(reinterpret_cast<unsigned long long *>(&s_followers[p]), 1ull << tid);
+    if (moves && !follows) s_fill[atomicAdd(&s_fills, 1)] = slot;
+    __syncthreads();
+    if (tid < MAXW) {
+        s_count[tid] = __popcll(s_followers[tid]);
+        s_begin[tid] = atomicAdd(&s_listed, s_count[tid]);
     }
     __syncthreads();
-    const int64_t n = view.bytes / (int64_t)sizeof(Vec);
-    for (int64_t e = blockIdx.x * (int64_t)blockDim.x + tid; e < n; e += (int64_t)gridDim.x * blockDim.x) {
+    if (follows) s_to[s_begin[p] + __popcll(s_followers[p] & ((1ull << tid) - 1))] = slot;
+    __syncthreads();
+    const int fills = s_fills;
+    for (int64_t e = first; e < n; e += (int64_t)gridDim.x * blockDim.x) {
         Vec x[MAXW];
 #pragma unroll
         for (int j = 0; j < MAXW; ++j)
-            if (s_followers[j]) x[j] = reinterpret_cast<const Vec *>(view.data + s_slot[j] * view.stride)[e];
+            if (s_count[j]) x[j] = reinterpret_cast<const Vec *>(s_from[j])[e];
 #pragma unroll
         for (int j = 0; j < MAXW; ++j)
-            for (uint64_t f = s_followers[j]; f; f &= f - 1)
-                reinterpret_cast<Vec *>(view.data + s_slot[__ffsll(f) - 1] * view.stride)[e] = x[j];
-        for (uint64_t f = s_fill; f; f &= f - 1)
-            reinterpret_cast<Vec *>(view.data + s_slot[__ffsll(f) - 1] * view.stride)[e] = filled<Vec>();
+            for (int k = 0, at = s_begin[j]; k < s_count[j]; ++k) reinterpret_cast<Vec *>(s_to[at + k])[e] = x[j];
+        for (int k = 0; k < fills; ++k) reinterpret_cast<Vec *>(s_fill[k])[e] = filled<Vec>();
     }
 }
 
@@ -60,8 +67,10 @@ template <int MAXW, typename Vec> cudaError_t launch_width(const ReorderArgs &a,
 template <typename Vec> cudaError_t launch(const ReorderArgs &a, cudaStream_t st) {
     int64_t most = 0;
     for (int i = 0; i < a.n_views; ++i) most = a.view[i].bytes > most ? a.view[i].bytes : most;
-    const int64_t blocks = (most / (int64_t)sizeof(Vec) + 255) / 256;
-    const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024), (unsigned)a.B, (unsigned)a.n_views);
+    // a vector per thread, or as many as leave sixteen CTAs for every SM: a CTA sets out with a chain of small reads
+    const int64_t blocks = (most / (int64_t)sizeof(Vec) + 255) / 256, share = 152 * 16 / ((int64_t)a.B * a.n_views);
+    const int64_t x = blocks < share ? blocks : share;
+    const dim3 grid((unsigned)(x < 1 ? 1 : x), (unsigned)a.B, (unsigned)a.n_views);
     if (a.W <= 4) return launch_width<4, Vec>(a, grid, st);
     if (a.W <= 8) return launch_width<8, Vec>(a, grid, st);
     if (a.W <= 16) return launch_width<16, Vec>(a, grid, st);
