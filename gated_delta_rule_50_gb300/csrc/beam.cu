@@ -62,12 +62,17 @@ __device__ __forceinline__ void join_warp(float &m, float &s) {
     m = top;
 }
 
-// The logarithm of the sum: (m + log2 s) / c, the exponent of s apart so that the rounding is that of the result.
+// The logarithm of the sum, (m + log2 s) / c: the exponent of s apart and the rest carried along, so that the
+// rounding is that of the result.
 __device__ __forceinline__ float normaliser(float m, float s) {
     if (!(s > 0.f)) return s == 0.f ? -INFINITY : s;
-    const int e = (int)(__float_as_uint(s) >> 23) - 127;  // s is at least 1, up to rounding, and no infinity
-    const float f = __uint_as_float((__float_as_uint(s) & 0x007FFFFFu) | 0x3F800000u);
-    return (float)(((double)m + (double)e + (double)log2f(f)) * (1.0 / (double)kLog2e));
+    const float e = (float)((int)(__float_as_uint(s) >> 23) - 127);  // s is at least 1, up to rounding, and no infinity
+    const float f = log2f(__uint_as_float((__float_as_uint(s) & 0x007FFFFFu) | 0x3F800000u));
+    const float a = m + e, v = a - m, rest = (m - (a - v)) + (e - v) + f;  // a + rest = m + log2 s
+    constexpr double inv = 1.0 / (double)kLog2e;
+    constexpr float hi = (float)inv, lo = (float)(inv - (double)hi);
+    const float p = a * hi;
+    return p + (fmaf(a, hi, -p) + fmaf(a, lo, rest * hi));
 }
 
 struct Nth {  // shared memory of nth_largest
@@ -315,6 +320,8 @@ __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
     __shared__ int s_count;
     const int tid = threadIdx.x, lane = tid & 31, n = a.n, W = a.W, b = blockIdx.x;
     const int lists = W * a.n_chunks, total = lists * n;
+    // quotients by n and n_chunks as products: exact below 2^20 over the divisor, and few keys are far below that
+    const uint32_t by_n = (1u << 20) / (uint32_t)n + 1, by_chunks = (1u << 20) / (uint32_t)a.n_chunks + 1;
     wait_for_previous();
     const uint64_t *keys = a.keys + (int64_t)b * total;
     if (tid < W) s_score[tid] = a.scores[b * W + tid], s_done[tid] = a.finished && a.finished[b * W + tid];
@@ -339,19 +346,18 @@ __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
     __syncthreads();
 
     // key j of a list, as a key of its score and its place in the search
-    auto entry = [&](int list, int j, uint64_t key) -> uint64_t {
-        const int w = list / a.n_chunks;
+    auto entry = [&](int w, int list, int j, uint64_t key) -> uint64_t {
         if (s_done[w]) return j == 0 && list == w * a.n_chunks ? make_key(s_score[w], (uint32_t)w * a.vocab) : 0;
         if (!key) return 0;
         return make_key(s_score[w] + (key_value(key) - s_norm[w]), (uint32_t)w * a.vocab + key_index(key));
     };
-    auto read = [&](int list, int j) { return entry(list, j, __ldcg(keys + (int64_t)list * n + j)); };
+    auto read = [&](int list, int j) { return entry(list / a.n_chunks, list, j, __ldcg(keys + (int64_t)list * n + j)); };
     uint64_t mine = 0;
     if (few) {
 #pragma unroll
         for (int i = 0; i < kPickKeys; ++i) {
-            const int e = tid + i * kThreads;
-            if (e < total) held[i] = entry(e / n, e % n, held[i]);
+            const uint32_t e = tid + i * kThreads, list = e * by_n >> 20, w = list * by_chunks >> 20;
+            if ((int)e < total) held[i] = entry(w, list, e - list * n, held[i]);
             mine = held[i] > mine ? held[i] : mine;
         }
         const uint64_t low = nth_largest((uint32_t)(mine >> 32), [&] { return mine; }, n, sh);
@@ -435,11 +441,11 @@ template <typename IO> cudaError_t launch(const BeamArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Elements of a row that one CTA takes: enough CTAs for eight on every SM where the rows allow it, a vector per
+// Elements of a row that one CTA takes: enough CTAs for six on every SM where the rows allow it, a vector per
 // thread at least, and no more than the keys in shared memory allow.  Equal chunks: up to seven elements are added
 // for a row that begins inside a vector.
 int beam_chunk(int64_t rows, int64_t vocab, int64_t n, gdn_dtype io) {
-    const int64_t wanted = 152 * 8, least = kThreads * (io == GDN_BF16 ? 8 : 4), per = kMaxGot / n < 512 ? kMaxGot / n : 512;
+    const int64_t wanted = 152 * 6, least = kThreads * (io == GDN_BF16 ? 8 : 4), per = kMaxGot / n < 512 ? kMaxGot / n : 512;
     const int64_t most = kThreads * per / least * least;
     int64_t chunks = rows < 1 ? 1 : (wanted + rows - 1) / rows;
     const int64_t fewest = (vocab + 7 + most - 1) / most;

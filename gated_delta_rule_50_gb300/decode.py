@@ -269,10 +269,11 @@ def beam_search_step(logits: torch.Tensor, scores: torch.Tensor, finished: Optio
             raise TypeError(f"mask must be bool, got {mask.dtype}")
         if mask.device != dev:
             raise ValueError(f"mask must be on {dev}, got {mask.device}")
-        try:
-            mask = mask.expand(B, W, vocab)
-        except RuntimeError:
-            raise ValueError(f"mask must be broadcastable to {(B, W, vocab)}, got {tuple(mask.shape)}") from None
+        if mask.shape != logits.shape:
+            try:
+                mask = mask.expand(B, W, vocab)
+            except RuntimeError:
+                raise ValueError(f"mask must be broadcastable to {(B, W, vocab)}, got {tuple(mask.shape)}") from None
         if mask.stride(2) != 1:
             mask = mask.contiguous()
         mask_batch, mask_beam, _ = mask.stride()
