@@ -1,17 +1,22 @@
-"""Builds libgdn.so (the C-ABI CUDA library) in-tree for sm_103a with nvcc.
+"""Builds libgdn.so (the C-ABI CUDA library) in-tree for sm_103a with nvcc, and
+beside it the extension module that the decoding calls of the Python package go
+through (g++, against PyTorch's and Python's headers).
 
 Each translation unit under csrc/ is compiled in parallel, then linked into
-``gated_delta_rule_50_gb300/_build/libgdn.so``.  A stamp of the sources and
-flags skips the rebuild when nothing changed.
+``gated_delta_rule_50_gb300/_build/libgdn.so``; csrc/binding.cpp becomes
+``_build/_gdn_decode.so``, which links to it.  A stamp of the sources, flags and
+PyTorch version skips the rebuild when nothing changed.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +24,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgdn.so")
+BINDING = os.path.join(BUILD, "_gdn_decode.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -36,10 +42,20 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _torch() -> str:
+    """PyTorch's folder, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found")
+    return list(spec.submodule_search_locations)[0]
+
+
 def _stamp(extra) -> str:
     h = hashlib.sha256()
+    with open(os.path.join(_torch(), "version.py"), "rb") as fh:
+        h.update(fh.read())
     for f in sorted(_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-                    + glob.glob(os.path.join(INCLUDE, "*.h"))):
+                    + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h"))):
         h.update(f.encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
@@ -51,7 +67,7 @@ def build(verbose: bool = False, extra_flags=(), force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     stamp_file = os.path.join(BUILD, "stamp")
     stamp = _stamp(extra_flags)
-    if not force and os.path.exists(LIB) and os.path.exists(stamp_file):
+    if not force and os.path.exists(LIB) and os.path.exists(BINDING) and os.path.exists(stamp_file):
         if open(stamp_file).read() == stamp:
             return LIB
     nvcc = _nvcc()
@@ -67,13 +83,35 @@ def build(verbose: bool = False, extra_flags=(), force: bool = False) -> str:
             print(r.stdout, r.stderr)
         return obj
 
+    def compile_binding():
+        torch, obj = _torch(), os.path.join(BUILD, "binding.o")
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+        include = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                   sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-w", *[x for i in include for x in ("-I", i)], "-c",
+               os.path.join(CSRC, "binding.cpp"), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj
+
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, _sources()))
+        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    torch_lib = os.path.join(_torch(), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    r = subprocess.run(["g++", "-shared", "-o", tmp, binding, "-L", BUILD, "-lgdn", "-L", torch_lib, "-ltorch_python", "-ltorch_cuda",
+                        "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     with open(stamp_file, "w") as fh:
         fh.write(stamp)
     return LIB

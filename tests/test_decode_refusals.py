@@ -1,5 +1,6 @@
 """What the decoding calls refuse, and with which error; nothing here reaches a kernel."""
 import os
+import struct
 import subprocess
 import sys
 
@@ -7,7 +8,6 @@ import pytest
 import torch
 
 import gated_delta_rule_50_gb300 as gdn
-from gated_delta_rule_50_gb300 import decode
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -16,6 +16,19 @@ def step_args(device="cpu", dtype=torch.bfloat16, B=2, T=1, Hq=2, Hv=4, K=64, V=
     mk = lambda *s, dt=dtype: torch.zeros(*s, dtype=dt, device=device)
     return dict(q=mk(B, T, Hq, K), k=mk(B, T, Hq, K), v=mk(B, T, Hv, V), g=mk(B, T, Hv, dt=torch.float32),
                 beta=mk(B, T, Hv, dt=torch.float32), state=mk(slots, Hv, K, V, dt=torch.float32))
+
+
+def test_not_tensors():
+    a = step_args()
+    for name in ("k", "v", "g", "beta", "state"):
+        with pytest.raises(TypeError, match="tensor"):
+            gdn.recurrent_gated_delta_rule(**dict(a, **{name: 1.0}))
+    with pytest.raises(TypeError, match="tensor"):
+        gdn.beam_search_step([[1.0]], torch.zeros(1, 1))
+    with pytest.raises(TypeError):
+        gdn.reorder_states(3, torch.zeros(1, 1))
+    with pytest.raises(TypeError, match="tensor"):
+        gdn.reorder_states([None], torch.zeros(1, 1))
 
 
 def test_no_cpu_path():
@@ -137,15 +150,25 @@ def test_reorder_refusals():
 
 
 # The C entries with placeholder addresses, in a child process that sees no GPU: a launch could only fail.
-_NO_GPU = r"""
-import ctypes, sys
+# gdn_decode_problem, gdn_beam_problem and gdn_state_view, packed as the C compiler lays them out
+LAYOUTS = """
+DECODE = struct.Struct("@6q15qif2qPqPPq")
+BEAM = struct.Struct("@8qi0q")
+VIEW = struct.Struct("@P2q")
+"""
+_NO_GPU = "import ctypes, struct, sys" + LAYOUTS + r"""
 sys.path.insert(0, ROOT)
-from gated_delta_rule_50_gb300 import decode as d
-lib = d._library()
+import gated_delta_rule_50_gb300 as gdn
+lib, P, I, C = gdn.load_library(), ctypes.c_void_p, ctypes.c_int64, ctypes.c_char_p
+lib.gdn_recurrent.argtypes = lib.gdn_tree.argtypes = [C] + [P] * 9
+lib.gdn_beam_search_workspace_bytes.argtypes = [C]
+lib.gdn_beam_search_workspace_bytes.restype = ctypes.c_size_t
+lib.gdn_beam_search.argtypes = [C] + [P] * 8 + [ctypes.c_size_t, P]
+lib.gdn_reorder_states.argtypes = [C] + [I] * 4 + [P] * 3
 A = 4096
 def prob(B=2, T=3, Hq=2, Hv=4, K=128, V=128, io_dtype=1, n_slots=5, slot_stride=4 * 128 * 128, state_indices=0, n_seqs=2,
          cu_seqlens=0, token_indices=0, n_steps=0):
-    return d._DECODE.pack(B, T, Hq, Hv, K, V, *[128] * 15, io_dtype, 0.1, n_slots, slot_stride, state_indices, n_seqs,
+    return DECODE.pack(B, T, Hq, Hv, K, V, *[128] * 15, io_dtype, 0.1, n_slots, slot_stride, state_indices, n_seqs,
                           cu_seqlens, token_indices, n_steps)
 def rec(p, q=A, k=A, v=A, g=A, b=A, s=A, out=None, o=A):
     return lib.gdn_recurrent(p, q, k, v, g, b, s, out, o, None)
@@ -162,7 +185,7 @@ out = dict(
     t_parents=tree(prob(), par=None), t_wide=tree(prob(T=65)), t_cu=tree(prob(B=1, n_seqs=1, cu_seqlens=A)),
     t_nothing=tree(prob(T=0)))
 def beam(B=2, W=3, vocab=100, n=4, logits_dtype=1):
-    return d._BEAM.pack(B, W, vocab, n, 300, 100, 0, 0, logits_dtype)
+    return BEAM.pack(B, W, vocab, n, 300, 100, 0, 0, logits_dtype)
 def search(p, logits=A, scores=A, o=A, ws=A, n=1 << 30):
     return lib.gdn_beam_search(p, logits, scores, None, None, o, A, A, ws, n, None)
 out.update(b_ws=lib.gdn_beam_search_workspace_bytes(beam()) > 0, b_bad=lib.gdn_beam_search_workspace_bytes(beam(n=0)),
@@ -170,7 +193,7 @@ out.update(b_ws=lib.gdn_beam_search_workspace_bytes(beam()) > 0, b_bad=lib.gdn_b
     b_dtype=search(beam(logits_dtype=5)), b_null=search(beam(), logits=None), b_odd=search(beam(), logits=A + 1),
     b_small=search(beam(), n=64), b_ws_odd=search(beam(), ws=A + 16), b_nothing=search(beam(B=0)))
 def reorder(data=A, stride=64, size=64, slots=8, B=2, W=4, par=A):
-    return lib.gdn_reorder_states(d._VIEW.pack(data or 0, stride, size), 1, slots, B, W, par, None, None)
+    return lib.gdn_reorder_states(VIEW.pack(data or 0, stride, size), 1, slots, B, W, par, None, None)
 out.update(r_null=reorder(data=None), r_stride=reorder(stride=32), r_slots=reorder(slots=7), r_W=reorder(W=65),
     r_parents=reorder(par=None), r_nothing=reorder(B=0), r_views=lib.gdn_reorder_states(None, 1, 8, 2, 4, A, None, None))
 print(repr(out))
@@ -193,7 +216,7 @@ def test_c_entries_refuse_on_the_host():
 
 
 def test_struct_sizes_match_the_header(tmp_path):
-    """What the binding packs has the C structures' sizes."""
+    """The layouts that the test above packs have the C structures' sizes."""
     import shutil
     if shutil.which("gcc") is None:
         pytest.skip("no C compiler")
@@ -203,4 +226,6 @@ def test_struct_sizes_match_the_header(tmp_path):
     exe = tmp_path / "s"
     subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     sizes = [int(n) for n in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
-    assert sizes == [c.size for c in (decode._DECODE, decode._BEAM, decode._VIEW)]
+    layouts = {"struct": struct}
+    exec(LAYOUTS, layouts)
+    assert sizes == [layouts[n].size for n in ("DECODE", "BEAM", "VIEW")]
