@@ -56,6 +56,10 @@ __device__ __forceinline__ Run run_of(const DecodeArgs &a, int n) {
     return u;
 }
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // Up to kTok tokens for `cols` threads, one state column each
 template <int K, typename IO> struct Stage {
     alignas(16) IO k[kTok<IO>][K], q[kTok<IO>][K], v[kTok<IO>][128];
@@ -79,9 +83,11 @@ template <int K, typename IO> struct Head {
     const float *g, *beta;
     IO *o;  // row out_row of this head, this thread's column
     int n, tid, cols, bar;
+    bool rows16;  // rows of q, k and v begin on 16-byte boundaries
 
-    __device__ __forceinline__ Head(const DecodeArgs &a, Stage<K, IO> &s, const Run &u, int n, int h, int hq, int col0, int tid, int cols, int bar)
-        : a(a), s(s), u(u), n(n), tid(tid), cols(cols), bar(bar) {
+    __device__ __forceinline__ Head(const DecodeArgs &a, Stage<K, IO> &s, const Run &u, int n, int h, int hq, int col0, int tid, int cols, int bar,
+                                    bool rows16)
+        : a(a), s(s), u(u), n(n), tid(tid), cols(cols), bar(bar), rows16(rows16) {
         q = static_cast<const IO *>(a.q) + u.b * a.sq.batch + hq * a.sq.head;
         k = static_cast<const IO *>(a.k) + u.b * a.sk.batch + hq * a.sk.head;
         v = static_cast<const IO *>(a.v) + u.b * a.sv.batch + h * a.sv.head + col0 + tid;
@@ -109,17 +115,31 @@ template <int K, typename IO> struct Head {
                 break;
             }
         }
-        for (int e = tid; e < m * K; e += cols) {
-            const int t = e / K, x = e % K;
-            const int64_t at = a.token_indices ? s.tok[t] : u.bos + t0 + t;
-            s.k[t][x] = k[at * a.sk.token + x];
-            if (o) s.q[t][x] = q[at * a.sq.token + x];
+        auto token = [&](int t) -> int64_t { return a.token_indices ? s.tok[t] : u.bos + t0 + t; };
+        if (rows16) {
+            constexpr int PIECE = 16 / (int)sizeof(IO), PIECES = K / PIECE;
+            for (int e = tid; e < m * PIECES; e += cols) {
+                const int t = e / PIECES, x = e % PIECES * PIECE;
+                cp_async16(&s.k[t][x], k + token(t) * a.sk.token + x);
+                if (o) cp_async16(&s.q[t][x], q + token(t) * a.sq.token + x);
+            }
+            const int pieces = cols / PIECE;
+            for (int e = tid; e < m * pieces; e += cols) {
+                const int t = e / pieces, x = (e - t * pieces) * PIECE;
+                cp_async16(&s.v[t][x], v - tid + token(t) * a.sv.token + x);
+            }
+        } else {
+#pragma unroll 4
+            for (int e = tid; e < m * K; e += cols) {
+                const int t = e / K, x = e % K;
+                s.k[t][x] = k[token(t) * a.sk.token + x];
+                if (o) s.q[t][x] = q[token(t) * a.sq.token + x];
+            }
+#pragma unroll 4
+            for (int t = 0; t < m; ++t) s.v[t][tid] = v[token(t) * a.sv.token];
         }
-        for (int t = 0; t < m; ++t) {
-            const int64_t at = a.token_indices ? s.tok[t] : u.bos + t0 + t;
-            s.v[t][tid] = v[at * a.sv.token];
-            if (tid == t) s.a[t] = expf(g[at * a.sg.token]), s.b[t] = beta[at * a.sb.token];
-        }
+        if (tid < m) s.a[tid] = expf(g[token(tid) * a.sg.token]), s.b[tid] = beta[token(tid) * a.sb.token];
+        asm volatile("cp.async.wait_all;" ::: "memory");
         return m;
     }
     // m staged tokens, the first of them the t0-th of the row
@@ -203,7 +223,7 @@ template <int K, typename IO> struct Head {
 };
 
 // grid (rows, q/k heads, value heads of one * parts of the columns)
-template <int K, typename IO> __global__ void __launch_bounds__(128) k_recurrent(const __grid_constant__ DecodeArgs a) {
+template <int K, typename IO> __global__ void __launch_bounds__(128) k_recurrent(const __grid_constant__ DecodeArgs a, bool rows16) {
     constexpr int NR = K / 4;
     __shared__ Stage<K, IO> s;
     const int tid = threadIdx.x, cols = blockDim.x;
@@ -211,7 +231,7 @@ template <int K, typename IO> __global__ void __launch_bounds__(128) k_recurrent
     wait_for_previous();
     const Run u = run_of(a, n);
     if (!u.valid) return;
-    const Head<K, IO> head(a, s, u, n, h, hq, col0, tid, cols, 1);
+    const Head<K, IO> head(a, s, u, n, h, hq, col0, tid, cols, 1, rows16);
     if (u.slot < 0 || u.slot >= a.n_slots) {
         head.fill(0, u.slot >= 0);
         return;
@@ -351,7 +371,7 @@ __global__ void __launch_bounds__(256, 1) k_recurrent_flow(const __grid_constant
         Ahead ahead;
         if (tid < 32 && next < heads) ahead = look(next);
         const Run u = run_of(a, n);
-        const Head<K, IO> head(a, s, u, n, h, h / a.G, 0, tid, a.V, bar);
+        const Head<K, IO> head(a, s, u, n, h, h / a.G, 0, tid, a.V, bar, true);
         const bool live = u.valid && u.slot >= 0 && u.slot < a.n_slots;
         named_bar(bar, a.V);  // the stage is free
         const bool ok = mbar_wait_warp(full + 8 * slot, (i / f.slots) & 1, abort_flag);
@@ -393,7 +413,7 @@ __global__ void __launch_bounds__(256, 1) k_recurrent_flow(const __grid_constant
 
 template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
     const int64_t heads = (int64_t)a.n_seqs * a.Hv;
-    // rows that a bulk copy can take: multiples of 16 bytes apart
+    // rows that a bulk copy, or 16-byte ones, can take: multiples of 16 bytes apart
     const int64_t strides = a.sk.batch | a.sk.token | a.sk.head | a.sv.batch | a.sv.token | a.sv.head |
                             (a.o ? a.sq.batch | a.sq.token | a.sq.head : 0);
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
@@ -407,7 +427,7 @@ template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream
         return launch_behind(k_recurrent_flow<K, IO>, dim3(kSMs), 256, f.bytes, st, a, f, (int)heads);
     } else {  // a warp per CTA where that spreads the heads over more SMs
         const int cols = heads * (a.V / kTile) <= 4 * kSMs ? kTile : a.V;
-        return launch_behind(k_recurrent<K, IO>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)(a.G * (a.V / cols))), cols, 0, st, a);
+        return launch_behind(k_recurrent<K, IO>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)(a.G * (a.V / cols))), cols, 0, st, a, rows16);
     }
 }
 

@@ -32,14 +32,14 @@ constexpr uint32_t kBlock = 16384;  // 128 rows of 64 bf16: one K block of [K; Q
 constexpr uint32_t kCols = 256;     // TMEM: S^T hi, lo (K columns), later R^T hi, lo and D2 | G, later D1
 constexpr uint32_t kRlo = 32, kD2 = 64, kD1 = 128;
 enum { BAR_S = 0, BAR_G = 8, BAR_D = 16, BAR_O = 24 };  // mbarriers: the state, G, D1, D2
-enum { NB_STATE = 1, NB_B = 2, NB_FREE = 3, NB_A = 4, NB_OUT = 5 };  // named barriers
+enum { NB_STATE = 1, NB_B = 2, NB_FREE = 3, NB_A = 4, NB_DIAG = 5, NB_OUT = 6 };  // named barriers
 
-template <int K, int TP> struct Map {
+template <int K, int V, int TP> struct Map {
     // over the state once it is in TMEM: P in fp32, then row by row W (eight rows of hi, then of lo, in the place of
     // eight of P), then o; L hi and lo; the blocks of L on the diagonal in fp32, by columns; their inverses; v
     static constexpr uint32_t PW = 0, LHI = TP * 256, LLO = LHI + TP * 128, DIAG = LLO + TP * 128, DS = 20;
     static constexpr uint32_t INV = DIAG + TP * DS * 4, INV_BLOCK = 16 * 48;  // hi, then lo; rows of 48 bytes
-    static constexpr uint32_t V = INV + TP / 16 * 2 * INV_BLOCK, scratch = V + TP * 256, state = K * 128 * 4;
+    static constexpr uint32_t VAL = INV + TP / 16 * 2 * INV_BLOCK, scratch = VAL + TP * V * 2, state = K * V * 4;
     static constexpr uint32_t KQ = ((scratch > state ? scratch : state) + 1023) / 1024 * 1024;
     // the products of e^g from node i to node t >= i: rows t and TP - 1 - t share one (see table_row); the stride
     // puts eight neighbouring rows on different banks
@@ -92,7 +92,8 @@ __device__ __forceinline__ void mma16816(float *c, const uint32_t (&a)[4], uint3
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// c += a B for a 16 x 16 block B [k][n] of bf16 hi and lo in shared memory; each lane gives the address of its row
+// c += a B for a 16 x 16 block B [k][n] of bf16 hi and lo in shared memory; each lane gives the address of its row.
+// The small products have sums of their own, so that no more than two follow each other.
 __device__ __forceinline__ void block_product(float (&c)[8], const Frag &a, uint32_t b_hi, uint32_t b_lo) {
     uint32_t h[4], l[4];
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -103,22 +104,25 @@ __device__ __forceinline__ void block_product(float (&c)[8], const Frag &a, uint
                  : "=r"(l[0]), "=r"(l[1]), "=r"(l[2]), "=r"(l[3])
                  : "r"(b_lo)
                  : "memory");
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         mma16816(c + 4 * j, a.hi, h[2 * j], h[2 * j + 1]);
-        mma16816(c + 4 * j, a.lo, h[2 * j], h[2 * j + 1]);
-        mma16816(c + 4 * j, a.hi, l[2 * j], l[2 * j + 1]);
+        mma16816(x + 4 * j, a.lo, h[2 * j], h[2 * j + 1]);
+        mma16816(x + 4 * j, a.hi, l[2 * j], l[2 * j + 1]);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] += x[i];
 }
 
-template <int K, int TP>
+template <int K, int V, int TP>
 __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec) {
-    using M = Map<K, TP>;
+    using M = Map<K, V, TP>;
     constexpr uint32_t ID_1 = idesc_bf16(128, TP, 0, 0), ID_2 = idesc_bf16(128, 2 * TP, 0, 0);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_align1024(smem_raw);
     const uint32_t sb = smem_u32(sm), bars = sb + M::BAR;
-    const int t = threadIdx.x, warp = t >> 5, T = a.T, V = a.V, lane_row = t & (GROUP - 1);
+    const int t = threadIdx.x, warp = t >> 5, T = a.T, lane_row = t & (GROUP - 1);
     const int n = blockIdx.x, hq = blockIdx.y, h = hq * a.G + blockIdx.z;
     const float nan = __int_as_float(0x7fffffff);
     constexpr int SETUP = 7;  // the warp that sets up, and issues G
@@ -265,16 +269,20 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
                 p[c ^ (node & 15)] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
         } else if (has_row) {
 #pragma unroll
-            for (int c = 0; c < TP / 8; ++c) {
-                st_split_chunk(sb + M::LHI, sb + M::LLO, node, c, x + 8 * c);
+            for (int c = 0; c < TP / 8; ++c)
                 if ((node >> 4) == (c >> 1)) {
                     float *diag = reinterpret_cast<float *>(sm + M::DIAG) + ((node & ~15) + 8 * (c & 1)) * M::DS + (node & 15);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) diag[i * M::DS] = x[8 * c + i];
                 }
-            }
         }
-        named_bar(NB_B, GROUP);
+        // the inverses need the diagonal alone: the warps that make them go on while the others split L
+        constexpr int INV_WARP = (GROUP - TP) / 32;  // the first warp of the group with a column of an inverse
+        if ((warp & 3) >= INV_WARP) named_bar(NB_DIAG, GROUP);
+        else bar_arrive(NB_DIAG, GROUP);
+        if (has_row && !is_p)
+#pragma unroll
+            for (int c = 0; c < TP / 8; ++c) st_split_chunk(sb + M::LHI, sb + M::LLO, node, c, x + 8 * c);
         if (row >= GROUP - TP) {  // a column of an inverse per thread: a finished y_i at once into all rows below it
             const int u = row - (GROUP - TP), j0 = u & 15;
             const float *diag = reinterpret_cast<const float *>(sm + M::DIAG) + (u & ~15) * M::DS;
@@ -383,8 +391,8 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
             __syncwarp();
         } else {
             const int c = t & (V / 8 - 1);
-            const uint32_t dst = sb + M::V + 16 * c;
-            const int pieces = V == 128 ? 4 : 3, step = (GROUP - 32) >> pieces;
+            const uint32_t dst = sb + M::VAL + 16 * c;
+            constexpr int pieces = V == 128 ? 4 : 3, step = (GROUP - 32) >> pieces;
             if (vec) {
 #pragma unroll 4
                 for (int r = (t - 32) >> pieces; r < T; r += step) cp_async16(dst + 2 * V * r, v + r * a.sv.token + 8 * c, true);
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
         tc_fence_after();
         named_bar(NB_A, GROUP);  // v is there
         const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
-        const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sm + M::V) + t;
+        const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sm + M::VAL) + t;
         if (column)
 #pragma unroll 1
             for (int c = 0; c < TP / 16; ++c) {
@@ -458,7 +466,8 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
             }
             named_bar(NB_OUT, NT);
         }
-        const int c = t & (V / 8 - 1), pieces = V == 128 ? 4 : 3;
+        constexpr int pieces = V == 128 ? 4 : 3;
+        const int c = t & (V / 8 - 1);
         for (int r = t >> pieces; r < T; r += NT >> pieces)
             *reinterpret_cast<uint4 *>(o + r * o_tok + 8 * c) = *reinterpret_cast<const uint4 *>(s_o + r * V + 8 * c);
     }
@@ -477,20 +486,23 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
     }
 }
 
-template <int K, int TP> cudaError_t launch(const DecodeArgs &a, bool vec, cudaStream_t st) {
-    constexpr int bytes = (int)Map<K, TP>::bytes;
+template <int K, int V, int TP> cudaError_t launch(const DecodeArgs &a, bool vec, cudaStream_t st) {
+    constexpr int bytes = (int)Map<K, V, TP>::bytes;
     static_assert(2 * (bytes + 1024) <= 233472, "two CTAs per SM");
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(k_tree_tc<K, TP>, bytes, done);
+    const cudaError_t e = allow_smem(k_tree_tc<K, V, TP>, bytes, done);
     if (e != cudaSuccess) return e;
-    return launch_behind(k_tree_tc<K, TP>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)a.G), NT, bytes, st, a, vec);
+    return launch_behind(k_tree_tc<K, V, TP>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)a.G), NT, bytes, st, a, vec);
 }
 
+template <int K, int V> cudaError_t launch_nodes(const DecodeArgs &a, bool vec, cudaStream_t st) {
+    if (a.T <= 16) return launch<K, V, 16>(a, vec, st);
+    if (a.T <= 32) return launch<K, V, 32>(a, vec, st);
+    if (a.T <= 48) return launch<K, V, 48>(a, vec, st);
+    return launch<K, V, 64>(a, vec, st);
+}
 template <int K> cudaError_t launch_width(const DecodeArgs &a, bool vec, cudaStream_t st) {
-    if (a.T <= 16) return launch<K, 16>(a, vec, st);
-    if (a.T <= 32) return launch<K, 32>(a, vec, st);
-    if (a.T <= 48) return launch<K, 48>(a, vec, st);
-    return launch<K, 64>(a, vec, st);
+    return a.V == 128 ? launch_nodes<K, 128>(a, vec, st) : launch_nodes<K, 64>(a, vec, st);
 }
 
 }  // namespace
