@@ -32,7 +32,7 @@ constexpr uint32_t kBlock = 16384;  // 128 rows of 64 bf16: one K block of [K; Q
 constexpr uint32_t kCols = 256;     // TMEM: S^T hi, lo (K columns), later R^T hi, lo and D2 | G, later D1
 constexpr uint32_t kRlo = 32, kD2 = 64, kD1 = 128;
 enum { BAR_S = 0, BAR_G = 8, BAR_D = 16, BAR_O = 24 };  // mbarriers: the state, G, D1, D2
-enum { NB_STATE = 1, NB_B = 2, NB_FREE = 3, NB_A = 4, NB_DIAG = 5, NB_OUT = 6 };  // named barriers
+enum { NB_STATE = 1, NB_B = 2, NB_FREE = 3, NB_A = 4, NB_DIAG = 5, NB_OUT = 6, NB_WALK = 7 };  // named barriers
 
 template <int K, int V, int TP> struct Map {
     // over the state once it is in TMEM: P in fp32, then row by row W (eight rows of hi, then of lo, in the place of
@@ -44,8 +44,9 @@ template <int K, int V, int TP> struct Map {
     // the products of e^g from node i to node t >= i: rows t and TP - 1 - t share one (see table_row); the stride
     // puts eight neighbouring rows on different banks
     static constexpr uint32_t TABLE = KQ + K / 64 * kBlock, LS = TP + 4;
-    static constexpr uint32_t VEC = TABLE + TP / 2 * LS * 4;  // (a, parent), beta, beta Gam, scale Gam: TP each
-    static constexpr uint32_t BAR = VEC + 5 * TP * 4;
+    // (a, parent), the same of the parent, beta, beta Gam, scale Gam: TP each
+    static constexpr uint32_t VEC = TABLE + TP / 2 * LS * 4;
+    static constexpr uint32_t BAR = VEC + 7 * TP * 4;
     static constexpr uint32_t MISC = BAR + 32;
     static constexpr uint32_t bytes = MISC + 32 + 1024;
 };
@@ -73,6 +74,20 @@ __device__ __forceinline__ void copy_piece(uint32_t dst, const __nv_bfloat16 *sr
         for (int i = 0; i < 4; ++i)
             w[i] = (uint32_t)__bfloat16_as_ushort(src[2 * i]) | (uint32_t)__bfloat16_as_ushort(src[2 * i + 1]) << 16;
     st_shared_v4(dst, w[0], w[1], w[2], w[3]);
+}
+// Two fp32 products at once, on a pair of registers
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void halves(uint64_t p, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 // Fragments of 16 x 16 blocks: C as two 16 x 8 accumulators, A as hi and lo of four registers each.
 struct Frag {
@@ -132,7 +147,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
 
     wait_for_previous();
     const int64_t slot = a.state_indices ? a.state_indices[n] : n;
-    int2 *s_up = reinterpret_cast<int2 *>(sm + M::VEC);  // e^g (its bits) and the parent
+    int4 *s_up = reinterpret_cast<int4 *>(sm + M::VEC);  // e^g (its bits) and the parent, then the parent's
     float *s_b = reinterpret_cast<float *>(s_up + TP), *s_bg = s_b + TP, *s_sg = s_bg + TP;
     float *table = reinterpret_cast<float *>(sm + M::TABLE);
     uint32_t *misc = reinterpret_cast<uint32_t *>(sm + M::MISC);
@@ -188,7 +203,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
     }
     for (int e = t; e < TP / 2 * (int)M::LS / 4; e += NT) reinterpret_cast<float4 *>(table)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t < TP) {
-        s_up[t] = make_int2(__float_as_int(expf(ga)), up);
+        *reinterpret_cast<int2 *>(s_up + t) = make_int2(__float_as_int(expf(ga)), up);
         s_b[t] = be;
     }
     cp_async_wait();
@@ -210,18 +225,27 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
         const int row = lane_row, node = row < TP ? row : row - TP;
         const bool has_row = row < 2 * TP, is_p = row >= TP;
         float *mine = table + table_row<TP>(has_row ? node : 0);
+        constexpr int WALKERS = (TP + 31) / 32 * 32;  // the first warps of the group
+        if (row < WALKERS) {  // each node's parent beside it: two steps for one access
+            if (row < TP) {
+                const int up = s_up[node].y;
+                if (up >= 0 && up < node) reinterpret_cast<int2 *>(s_up + node)[1] = *reinterpret_cast<const int2 *>(s_up + up);
+            }
+            named_bar(NB_WALK, WALKERS);
+        }
         if (row < TP) {  // from the node up to the state, leaving the products of e^g on the way
             float prod = 1.f;
             int p = node, kind = 0;
-            while (p >= 0) {
+            auto step = [&](int a_bits, int up) {  // whether there is another node above p
                 mine[p] = prod;
-                const int2 up = s_up[p];
-                if (up.y >= p || up.y < -1) {
-                    kind = up.y < -1 ? 1 : 2;
-                    break;
-                }
-                prod *= __int_as_float(up.x);
-                p = up.y;
+                if (up >= p || up < -1) kind = up < -1 ? 1 : 2;
+                prod *= kind ? 1.f : __int_as_float(a_bits);
+                p = up;
+                return !kind && up >= 0;
+            };
+            for (;;) {
+                const int4 up = s_up[p];
+                if (!step(up.x, up.y) || !step(up.z, up.w)) break;
             }
             if (kind) {  // nothing of such a node is used, whatever it holds
                 for (int i = 0; i <= node; ++i) mine[i] = 0.f;
@@ -248,17 +272,25 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec)
         const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
         if (has_row) {
             const float b = is_p ? 1.f : s_b[node];
-            const int last = is_p ? node : node - 1;  // P has its diagonal, L does not
+            const uint64_t bb = pair_of(b, b);
 #pragma unroll
             for (int c = 0; c < TP / 4; ++c) {
-                const float4 f = reinterpret_cast<const float4 *>(mine)[c];  // past the node: anything
-                const float d[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[4 * c + i] = 4 * c + i <= last ? b * d[i] * x[4 * c + i] : 0.f;
-                if (dead)
+                const ulonglong2 d = reinterpret_cast<const ulonglong2 *>(mine)[c];
+                const uint64_t lo = mul2(mul2(bb, d.x), pair_of(x[4 * c], x[4 * c + 1]));
+                const uint64_t hi = mul2(mul2(bb, d.y), pair_of(x[4 * c + 2], x[4 * c + 3]));
+                // four entries past the node's are another row's; those of its own four are 0, and the diagonal of L,
+                // which nothing reads, may stay
+                const bool own = 4 * c <= node;
+                halves(own ? lo : 0, x[4 * c], x[4 * c + 1]);
+                halves(own ? hi : 0, x[4 * c + 2], x[4 * c + 3]);
+                if (dead) {
+                    float f[4];
+                    halves(d.x, f[0], f[1]);
+                    halves(d.y, f[2], f[3]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (d[i] == 0.f) x[4 * c + i] = 0.f;
+                        if (f[i] == 0.f) x[4 * c + i] = 0.f;
+                }
             }
         }
         named_bar(NB_FREE, NT);  // the state's place is free
