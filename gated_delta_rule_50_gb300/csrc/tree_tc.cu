@@ -15,7 +15,8 @@
 // q and k are bf16 as given; S, R, L, P and W enter products as hi + lo bf16 pairs (16 bits; one bf16 rounding of
 // them would cost as much as the rounding of o) and are kept in fp32 between them.
 // S arrives by one bulk copy (a head's state is contiguous); its place in shared memory then holds L, P, W and o.
-// Two CTAs fit on an SM (107 KB, 256 TMEM columns each), so that one's copies run under the other's arithmetic.
+// Two CTAs stay on each SM (109 KB, 256 TMEM columns each) and take head after head, so that one's copies run under
+// the other's arithmetic; k, q and the gates of a CTA's next head come while group B finishes W.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -27,7 +28,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int GROUP = 128, NT = 2 * GROUP;
+constexpr int GROUP = 128, NT = 2 * GROUP, kSMs = 152;
 constexpr uint32_t kBlock = 16384;  // 128 rows of 64 bf16: one K block of [K; Q]
 constexpr uint32_t kCols = 256;     // TMEM: S^T hi, lo (K columns), later R^T hi, lo and D2 | G, later D1
 constexpr uint32_t kRlo = 32, kD2 = 64, kD1 = 128;
@@ -131,390 +132,415 @@ __device__ __forceinline__ void block_product(float (&c)[8], const Frag &a, uint
 }
 
 template <int K, int V, int TP>
-__global__ void __launch_bounds__(NT, 2) k_tree_tc(const DecodeArgs a, bool vec) {
+__global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ DecodeArgs a, bool vec, int heads) {
     using M = Map<K, V, TP>;
     constexpr uint32_t ID_1 = idesc_bf16(128, TP, 0, 0), ID_2 = idesc_bf16(128, 2 * TP, 0, 0);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_align1024(smem_raw);
     const uint32_t sb = smem_u32(sm), bars = sb + M::BAR;
     const int t = threadIdx.x, warp = t >> 5, T = a.T, lane_row = t & (GROUP - 1);
-    const int n = blockIdx.x, hq = blockIdx.y, h = hq * a.G + blockIdx.z;
     const float nan = __int_as_float(0x7fffffff);
-    constexpr int SETUP = 7;  // the warp that sets up, and issues G
+    constexpr int SETUP = 7;  // the warp that sets up, copies the state and issues G
     const bool group_b = t >= GROUP, column = lane_row < V;  // the same for a whole warp
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)n * T * a.Hv + h) * V;
     const int64_t o_tok = (int64_t)a.Hv * V;
-
-    wait_for_previous();
-    const int64_t slot = a.state_indices ? a.state_indices[n] : n;
     int4 *s_up = reinterpret_cast<int4 *>(sm + M::VEC);  // e^g (its bits) and the parent, then the parent's
     float *s_b = reinterpret_cast<float *>(s_up + TP), *s_bg = s_b + TP, *s_sg = s_bg + TP;
     float *table = reinterpret_cast<float *>(sm + M::TABLE);
     uint32_t *misc = reinterpret_cast<uint32_t *>(sm + M::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     uint32_t *s_absent = misc + 2, *s_bad = misc + 4;  // nodes of each kind, a bit each
-    const bool live = slot >= 0 && slot < a.n_slots;
-    if (warp == SETUP && live) {
+    if (warp == SETUP) {
         if (t == 32 * SETUP) {
             for (int i = 0; i < 4; ++i) mbar_init(bars + 8 * i, 1);
-            for (int i = 1; i < 6; ++i) misc[i] = 0;
+            misc[1] = 0;
             fence_mbar_init();
+        }
+        __syncwarp();
+    }
+    wait_for_previous();
+    // What a head's turn begins with: rows of k and q on the way to shared memory (group A, 16 bytes per thread and a
+    // multiple of eight rows at a time), gates and parent of this thread's node, the slot
+    struct Ahead {
+        int64_t slot;
+        float g, beta;
+        int up;
+    };
+    auto look = [&](int head) {
+        const int n = head / a.Hv, h = head - n * a.Hv, hq = h / a.G;
+        Ahead f = {a.state_indices ? a.state_indices[n] : n, 0.f, 0.f, -1};
+        if (!group_b) {
+            constexpr int PIECES = K / 8, ROWS = GROUP / PIECES;
+            const int x = t % PIECES, r0 = t / PIECES;
+            const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + n * a.sk.batch + hq * a.sk.head + 8 * x;
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + n * a.sq.batch + hq * a.sq.head + 8 * x;
+            const uint32_t dst = sw128_addr(sb + M::KQ + (x >> 3) * kBlock, r0, x & 7);
+            if (t < T) {
+                f.g = a.g[n * a.sg.batch + h * a.sg.head + t * a.sg.token];
+                f.beta = a.beta[n * a.sb.batch + h * a.sb.head + t * a.sb.token];
+                f.up = a.parents[(int64_t)n * T + t];
+            }
+            if (vec) {
+#pragma unroll
+                for (int r = 0; r < TP; r += ROWS) {
+                    const bool in = r0 + r < T;
+                    cp_async16(dst + r * 128, in ? k + (r0 + r) * a.sk.token : k, in);
+                    cp_async16(dst + (TP + r) * 128, in ? q + (r0 + r) * a.sq.token : q, in);
+                }
+            } else {
+#pragma unroll 1
+                for (int r = 0; r < TP; r += ROWS) {
+                    copy_piece(dst + r * 128, k + (r0 + r) * a.sk.token, r0 + r < T);
+                    copy_piece(dst + (TP + r) * 128, q + (r0 + r) * a.sq.token, r0 + r < T);
+                }
+            }
+        }
+        return f;
+    };
+    Ahead ahead = look(blockIdx.x);
+    bool ok = true, first = true;
+    uint32_t phase = 0;  // of every mbarrier: each is used once per head
+    for (int head = blockIdx.x; head < heads; head += gridDim.x) {
+        const int n = head / a.Hv, h = head - n * a.Hv;
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)n * T * a.Hv + h) * V;
+        const int64_t slot = ahead.slot;
+        const float ga = ahead.g, be = ahead.beta;
+        const int up = ahead.up;
+        const bool more = head + gridDim.x < heads;
+        if (slot < 0 || slot >= a.n_slots || !ok) {  // an idle row, no such slot, or a wait that ran out before
+            if (t < V)
+                for (int i = 0; i < T; ++i) o[i * o_tok + t] = __float2bfloat16_rn(slot < 0 ? 0.f : nan);
+            cp_async_wait();
+            if (more) ahead = look(head + gridDim.x);
+            continue;
+        }
+        if (t == 32 * SETUP) {
             const uint32_t bytes = (uint32_t)(K * V * 4);
             mbar_arrive_expect_tx(bars + BAR_S, bytes);
             bulk_load(sb, a.state + slot * a.slot_stride + (int64_t)h * K * V, bytes, bars + BAR_S);
+            for (int i = 2; i < 6; ++i) misc[i] = 0;
         }
-        __syncwarp();
-        tmem_alloc(sb + M::MISC, kCols);
-    }
-    {  // rows of k and q, 16 bytes per thread, a multiple of eight rows at a time
-        constexpr int PIECES = K / 8, ROWS = NT / PIECES;
-        const int x = t % PIECES, r0 = t / PIECES;
-        const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + n * a.sk.batch + hq * a.sk.head + 8 * x;
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + n * a.sq.batch + hq * a.sq.head + 8 * x;
-        const uint32_t dst = sw128_addr(sb + M::KQ + (x >> 3) * kBlock, r0, x & 7);
-        if (vec) {
-#pragma unroll
-            for (int r = 0; r < TP; r += ROWS) {
-                if (r0 + r >= TP) break;
-                const bool in = r0 + r < T;
-                cp_async16(dst + r * 128, in ? k + (r0 + r) * a.sk.token : k, in);
-                cp_async16(dst + (TP + r) * 128, in ? q + (r0 + r) * a.sq.token : q, in);
-            }
-        } else {
-#pragma unroll 1
-            for (int r = 0; r0 + r < TP; r += ROWS) {
-                copy_piece(dst + r * 128, k + (r0 + r) * a.sk.token, r0 + r < T);
-                copy_piece(dst + (TP + r) * 128, q + (r0 + r) * a.sq.token, r0 + r < T);
-            }
-        }
-    }
-    float ga = 0.f, be = 0.f;
-    int up = -1;
-    if (t < T) {
-        ga = a.g[n * a.sg.batch + h * a.sg.head + t * a.sg.token];
-        be = a.beta[n * a.sb.batch + h * a.sb.head + t * a.sb.token];
-        up = a.parents[(int64_t)n * T + t];
-    }
-    if (!live) {
-        if (t < V)
-            for (int i = 0; i < T; ++i) o[i * o_tok + t] = __float2bfloat16_rn(slot < 0 ? 0.f : nan);
-        cp_async_wait();
-        return;
-    }
-    for (int e = t; e < TP / 2 * (int)M::LS / 4; e += NT) reinterpret_cast<float4 *>(table)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (t < TP) {
-        *reinterpret_cast<int2 *>(s_up + t) = make_int2(__float_as_int(expf(ga)), up);
-        s_b[t] = be;
-    }
-    cp_async_wait();
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = misc[0], lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    bool ok = true;
-    if (group_b) {
-        if (warp == SETUP) {
-            if (t == 32 * SETUP) {
-                for (int kb = 0; kb < K / 64; ++kb)
-                    mma_chain<4, 2, 2>(tmem + kD1, kdesc(sb + M::KQ + kb * kBlock), kdesc(sb + M::KQ + kb * kBlock), ID_1, kb);
-                mma_commit(bars + BAR_G);
-            }
+        if (warp == SETUP && first) {
             __syncwarp();
+            tmem_alloc(sb + M::MISC, kCols);
         }
-        const int row = lane_row, node = row < TP ? row : row - TP;
-        const bool has_row = row < 2 * TP, is_p = row >= TP;
-        float *mine = table + table_row<TP>(has_row ? node : 0);
-        constexpr int WALKERS = (TP + 31) / 32 * 32;  // the first warps of the group
-        if (row < WALKERS) {  // each node's parent beside it: two steps for one access
-            if (row < TP) {
-                const int up = s_up[node].y;
-                if (up >= 0 && up < node) reinterpret_cast<int2 *>(s_up + node)[1] = *reinterpret_cast<const int2 *>(s_up + up);
-            }
-            named_bar(NB_WALK, WALKERS);
+        first = false;
+        for (int e = t; e < TP / 2 * (int)M::LS / 4; e += NT) reinterpret_cast<float4 *>(table)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < TP) {
+            *reinterpret_cast<int2 *>(s_up + t) = make_int2(__float_as_int(expf(ga)), up);
+            s_b[t] = be;
         }
-        if (row < TP) {  // from the node up to the state, leaving the products of e^g on the way
-            float prod = 1.f;
-            int p = node, kind = 0;
-            auto step = [&](int a_bits, int up) {  // whether there is another node above p
-                mine[p] = prod;
-                if (up >= p || up < -1) kind = up < -1 ? 1 : 2;
-                prod *= kind ? 1.f : __int_as_float(a_bits);
-                p = up;
-                return !kind && up >= 0;
-            };
-            for (;;) {
-                const int4 up = s_up[p];
-                if (!step(up.x, up.y) || !step(up.z, up.w)) break;
-            }
-            if (kind) {  // nothing of such a node is used, whatever it holds
-                for (int i = 0; i <= node; ++i) mine[i] = 0.f;
-                atomicOr(&(kind == 1 ? s_absent : s_bad)[node >> 5], 1u << (node & 31));
-            }
-            const float b = kind ? 0.f : s_b[node];
-            s_b[node] = b;
-            s_bg[node] = kind ? 0.f : b * prod;
-            s_sg[node] = kind ? 0.f : a.scale * prod;
-        }
-        ok = mbar_wait_warp(bars + BAR_G, 0, abort_flag);
+        cp_async_wait();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
         tc_fence_after();
-        float x[TP];
-#pragma unroll
-        for (int c = 0; c < TP / 16; ++c) {
-            uint32_t r[16];
-            tmem_ld16(lanes + kD1 + 16 * c, r);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[16 * c + i] = __uint_as_float(r[i]);
-        }
-        tc_fence_before();
-        bar_arrive(NB_STATE, NT);
-        named_bar(NB_B, GROUP);  // the products are there
-        const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
-        if (has_row) {
-            const float b = is_p ? 1.f : s_b[node];
-            const uint64_t bb = pair_of(b, b);
-#pragma unroll
-            for (int c = 0; c < TP / 4; ++c) {
-                const ulonglong2 d = reinterpret_cast<const ulonglong2 *>(mine)[c];
-                const uint64_t lo = mul2(mul2(bb, d.x), pair_of(x[4 * c], x[4 * c + 1]));
-                const uint64_t hi = mul2(mul2(bb, d.y), pair_of(x[4 * c + 2], x[4 * c + 3]));
-                // four entries past the node's are another row's; those of its own four are 0, and the diagonal of L,
-                // which nothing reads, may stay
-                const bool own = 4 * c <= node;
-                halves(own ? lo : 0, x[4 * c], x[4 * c + 1]);
-                halves(own ? hi : 0, x[4 * c + 2], x[4 * c + 3]);
-                if (dead) {
-                    float f[4];
-                    halves(d.x, f[0], f[1]);
-                    halves(d.y, f[2], f[3]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (f[i] == 0.f) x[4 * c + i] = 0.f;
-                }
-            }
-        }
-        named_bar(NB_FREE, NT);  // the state's place is free
-        if (has_row && is_p) {
-            float4 *p = reinterpret_cast<float4 *>(sm + M::PW + node * 256);
-#pragma unroll
-            for (int c = 0; c < TP / 4; ++c)
-                p[c ^ (node & 15)] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-        } else if (has_row) {
-#pragma unroll
-            for (int c = 0; c < TP / 8; ++c)
-                if ((node >> 4) == (c >> 1)) {
-                    float *diag = reinterpret_cast<float *>(sm + M::DIAG) + ((node & ~15) + 8 * (c & 1)) * M::DS + (node & 15);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) diag[i * M::DS] = x[8 * c + i];
-                }
-        }
-        // the inverses need the diagonal alone: the warps that make them go on while the others split L
-        constexpr int INV_WARP = (GROUP - TP) / 32;  // the first warp of the group with a column of an inverse
-        if ((warp & 3) >= INV_WARP) named_bar(NB_DIAG, GROUP);
-        else bar_arrive(NB_DIAG, GROUP);
-        if (has_row && !is_p)
-#pragma unroll
-            for (int c = 0; c < TP / 8; ++c) st_split_chunk(sb + M::LHI, sb + M::LLO, node, c, x + 8 * c);
-        if (row >= GROUP - TP) {  // a column of an inverse per thread: a finished y_i at once into all rows below it
-            const int u = row - (GROUP - TP), j0 = u & 15;
-            const float *diag = reinterpret_cast<const float *>(sm + M::DIAG) + (u & ~15) * M::DS;
-            float y[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = j == j0 ? 1.f : 0.f;
-#pragma unroll
-            for (int i = 0; i < 15; ++i) {
-                float l[16];
-#pragma unroll
-                for (int j = (i + 1) / 4 * 4; j < 16; j += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(diag + i * M::DS + j);
-                    l[j] = f.x, l[j + 1] = f.y, l[j + 2] = f.z, l[j + 3] = f.w;
-                }
-#pragma unroll
-                for (int j = i + 1; j < 16; ++j) y[j] = fmaf(-l[j], y[i], y[j]);
-            }
-            unsigned char *inv = sm + M::INV + (u >> 4) * 2 * M::INV_BLOCK + 2 * j0;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(y[j]);
-                *reinterpret_cast<__nv_bfloat16 *>(inv + j * 48) = hi;
-                *reinterpret_cast<__nv_bfloat16 *>(inv + M::INV_BLOCK + j * 48) = __float2bfloat16_rn(y[j] - __bfloat162float(hi));
-            }
-        }
-        named_bar(NB_B, GROUP);
-        const int w = warp - 4, lane = t & 31;
-        if (16 * w < TP) {  // rows 16 w .. 16 w + 15 of W: blocks beyond the w-th are 0
-            const int g = lane >> 2, q2 = lane & 3;
-            float c[TP / 16][8];
-#pragma unroll
-            for (int b = 0; b < TP / 16; ++b)
-                if (b <= w)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // (rows g, g + 8) x (columns 2 q2, 2 q2 + 1 of each half)
-                        const int r = 16 * w + g + 8 * (i & 1), col = 16 * b + 8 * (i >> 1) + 2 * q2;
-                        const float2 f = *reinterpret_cast<const float2 *>(sm + M::PW + r * 256 + ((col >> 2) ^ (r & 15)) * 16 +
-                                                                           (col & 2) * 4);
-                        c[b][4 * (i >> 1) + 2 * (i & 1)] = f.x;
-                        c[b][4 * (i >> 1) + 2 * (i & 1) + 1] = f.y;
-                    }
-            __syncwarp();  // W takes the place of P's rows
-            // the row of a 16 x 16 block whose address this lane gives, and the half
-            const int br = (lane & 7) + (lane & 8), bh = lane >> 4;
-#pragma unroll
-            for (int b = TP / 16 - 1; b >= 0; --b) {
-                Frag f;
-                if (b <= w) {
-                    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    const uint32_t inv = sb + M::INV + b * 2 * M::INV_BLOCK + br * 48 + bh * 16;
-                    block_product(y, split_frag(c[b], false), inv, inv + M::INV_BLOCK);
-                    f = split_frag(y, false);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f.hi[i] = f.lo[i] = 0u;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * w + g + 8 * (i & 1);
-                    const uint32_t at = sb + M::PW + (r >> 3) * 2048 + (r & 7) * 128 + (((2 * b + (i >> 1)) ^ (r & 7)) << 4) + 4 * q2;
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(f.hi[i]) : "memory");
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024), "r"(f.lo[i]) : "memory");
-                }
-                if (b <= w) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f.hi[i] ^= 0x80008000u, f.lo[i] ^= 0x80008000u;
-#pragma unroll
-                    for (int e = 0; e < b; ++e)
-                        block_product(c[e], f, sw128_addr(sb + M::LHI, 16 * b + br, 2 * e + bh),
-                                      sw128_addr(sb + M::LLO, 16 * b + br, 2 * e + bh));
-                }
-            }
-            fence_proxy_async_smem();
-        }
-    } else {
-        // v has its place once the state has left it; until then its lines come as far as L2
-        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + n * a.sv.batch + h * a.sv.head;
-        for (int e = t; e < T * V / 64; e += GROUP)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(v + (e >> (V == 128)) * a.sv.token + (V == 128 ? e & 1 : 0) * 64));
-        ok = mbar_wait_warp(bars + BAR_S, 0, abort_flag);
-        if (column) {
-            const float *s = reinterpret_cast<const float *>(sm) + t;
-#pragma unroll 1
-            for (int c = 0; c < K / 32; ++c) {
-                float y[32];
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) y[i] = s[i * V];
-                s += 32 * V;
-                split_pack16(y, hi, lo);
-                tmem_st16x2(lanes + 16 * c, hi, lanes + K / 2 + 16 * c, lo);
-            }
-        }
-        tc_fence_before();
-        bar_arrive(NB_FREE, NT);
-        named_bar(NB_STATE, NT);  // the state is in TMEM, G has been read
-        if (warp == 0) {
-            tc_fence_after();
-            if (t == 0) {
-                for (int part = 0; part < 2; ++part)
+        const uint32_t tmem = misc[0], lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        if (group_b) {
+            if (warp == SETUP) {
+                if (t == 32 * SETUP) {
                     for (int kb = 0; kb < K / 64; ++kb)
-                        mma_chain_ta<4, 2>(tmem + kD1, tmem + part * (K / 2) + 32 * kb, kdesc(sb + M::KQ + kb * kBlock), ID_2,
-                                           part + kb);
-                mma_commit(bars + BAR_D);
+                        mma_chain<4, 2, 2>(tmem + kD1, kdesc(sb + M::KQ + kb * kBlock), kdesc(sb + M::KQ + kb * kBlock), ID_1, kb);
+                    mma_commit(bars + BAR_G);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-        } else {
-            const int c = t & (V / 8 - 1);
-            const uint32_t dst = sb + M::VAL + 16 * c;
-            constexpr int pieces = V == 128 ? 4 : 3, step = (GROUP - 32) >> pieces;
-            if (vec) {
-#pragma unroll 4
-                for (int r = (t - 32) >> pieces; r < T; r += step) cp_async16(dst + 2 * V * r, v + r * a.sv.token + 8 * c, true);
-            } else {
-#pragma unroll 1
-                for (int r = (t - 32) >> pieces; r < T; r += step) copy_piece(dst + 2 * V * r, v + r * a.sv.token + 8 * c, true);
+            const int row = lane_row, node = row < TP ? row : row - TP;
+            const bool has_row = row < 2 * TP, is_p = row >= TP;
+            float *mine = table + table_row<TP>(has_row ? node : 0);
+            constexpr int WALKERS = (TP + 31) / 32 * 32;  // the first warps of the group
+            if (row < WALKERS) {  // each node's parent beside it: two steps for one access
+                if (row < TP) {
+                    const int up = s_up[node].y;
+                    if (up >= 0 && up < node) reinterpret_cast<int2 *>(s_up + node)[1] = *reinterpret_cast<const int2 *>(s_up + up);
+                }
+                named_bar(NB_WALK, WALKERS);
             }
-        }
-        cp_async_wait();
-        ok = mbar_wait_warp(bars + BAR_D, 0, abort_flag) && ok;
-        tc_fence_after();
-        named_bar(NB_A, GROUP);  // v is there
-        const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
-        const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sm + M::VAL) + t;
-        if (column)
-#pragma unroll 1
-            for (int c = 0; c < TP / 16; ++c) {
-                uint32_t ks[16], hi[8], lo[8];
-                float b[16], bg[16], y[16];
-                tmem_ld16(lanes + kD1 + 16 * c, ks);
-                lds16f(s_b + 16 * c, b);
-                lds16f(s_bg + 16 * c, bg);
+            if (row < TP) {  // from the node up to the state, leaving the products of e^g on the way
+                float prod = 1.f;
+                int p = node, kind = 0;
+                auto step = [&](int a_bits, int up) {  // whether there is another node above p
+                    mine[p] = prod;
+                    if (up >= p || up < -1) kind = up < -1 ? 1 : 2;
+                    prod *= kind ? 1.f : __int_as_float(a_bits);
+                    p = up;
+                    return !kind && up >= 0;
+                };
+                for (;;) {
+                    const int4 up = s_up[p];
+                    if (!step(up.x, up.y) || !step(up.z, up.w)) break;
+                }
+                if (kind) {  // nothing of such a node is used, whatever it holds
+                    for (int i = 0; i <= node; ++i) mine[i] = 0.f;
+                    atomicOr(&(kind == 1 ? s_absent : s_bad)[node >> 5], 1u << (node & 31));
+                }
+                const float b = kind ? 0.f : s_b[node];
+                s_b[node] = b;
+                s_bg[node] = kind ? 0.f : b * prod;
+                s_sg[node] = kind ? 0.f : a.scale * prod;
+            }
+            ok = mbar_wait_warp(bars + BAR_G, phase, abort_flag);
+            tc_fence_after();
+            float x[TP];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    y[j] = fmaf(-bg[j], __uint_as_float(ks[j]), b[j] * __bfloat162float(vs[(16 * c + j) * V]));
-                if (16 * c + 16 > T || dead) {  // past the last node v was not written
-                    const uint32_t gone = (s_absent[c >> 1] | s_bad[c >> 1]) >> (16 * (c & 1));
+            for (int c = 0; c < TP / 16; ++c) {
+                uint32_t r[16];
+                tmem_ld16(lanes + kD1 + 16 * c, r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[16 * c + i] = __uint_as_float(r[i]);
+            }
+            tc_fence_before();
+            bar_arrive(NB_STATE, NT);
+            named_bar(NB_B, GROUP);  // the products are there
+            const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
+            if (has_row) {
+                const float b = is_p ? 1.f : s_b[node];
+                const uint64_t bb = pair_of(b, b);
+#pragma unroll
+                for (int c = 0; c < TP / 4; ++c) {
+                    const ulonglong2 d = reinterpret_cast<const ulonglong2 *>(mine)[c];
+                    const uint64_t lo = mul2(mul2(bb, d.x), pair_of(x[4 * c], x[4 * c + 1]));
+                    const uint64_t hi = mul2(mul2(bb, d.y), pair_of(x[4 * c + 2], x[4 * c + 3]));
+                    // four entries past the node's are another row's; those of its own four are 0, and the diagonal of L,
+                    // which nothing reads, may stay
+                    const bool own = 4 * c <= node;
+                    halves(own ? lo : 0, x[4 * c], x[4 * c + 1]);
+                    halves(own ? hi : 0, x[4 * c + 2], x[4 * c + 3]);
+                    if (dead) {
+                        float f[4];
+                        halves(d.x, f[0], f[1]);
+                        halves(d.y, f[2], f[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (f[i] == 0.f) x[4 * c + i] = 0.f;
+                    }
+                }
+            }
+            named_bar(NB_FREE, NT);  // the state's place is free
+            if (has_row && is_p) {
+                float4 *p = reinterpret_cast<float4 *>(sm + M::PW + node * 256);
+#pragma unroll
+                for (int c = 0; c < TP / 4; ++c)
+                    p[c ^ (node & 15)] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            } else if (has_row) {
+#pragma unroll
+                for (int c = 0; c < TP / 8; ++c)
+                    if ((node >> 4) == (c >> 1)) {
+                        float *diag = reinterpret_cast<float *>(sm + M::DIAG) + ((node & ~15) + 8 * (c & 1)) * M::DS + (node & 15);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) diag[i * M::DS] = x[8 * c + i];
+                    }
+            }
+            // the inverses need the diagonal alone: the warps that make them go on while the others split L
+            constexpr int INV_WARP = (GROUP - TP) / 32;  // the first warp of the group with a column of an inverse
+            if ((warp & 3) >= INV_WARP) named_bar(NB_DIAG, GROUP);
+            else bar_arrive(NB_DIAG, GROUP);
+            if (has_row && !is_p)
+#pragma unroll
+                for (int c = 0; c < TP / 8; ++c) st_split_chunk(sb + M::LHI, sb + M::LLO, node, c, x + 8 * c);
+            if (row >= GROUP - TP) {  // a column of an inverse per thread: a finished y_i at once into all rows below it
+                const int u = row - (GROUP - TP), j0 = u & 15;
+                const float *diag = reinterpret_cast<const float *>(sm + M::DIAG) + (u & ~15) * M::DS;
+                float y[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = j == j0 ? 1.f : 0.f;
+#pragma unroll
+                for (int i = 0; i < 15; ++i) {
+                    float l[16];
+#pragma unroll
+                    for (int j = (i + 1) / 4 * 4; j < 16; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(diag + i * M::DS + j);
+                        l[j] = f.x, l[j + 1] = f.y, l[j + 2] = f.z, l[j + 3] = f.w;
+                    }
+#pragma unroll
+                    for (int j = i + 1; j < 16; ++j) y[j] = fmaf(-l[j], y[i], y[j]);
+                }
+                unsigned char *inv = sm + M::INV + (u >> 4) * 2 * M::INV_BLOCK + 2 * j0;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(y[j]);
+                    *reinterpret_cast<__nv_bfloat16 *>(inv + j * 48) = hi;
+                    *reinterpret_cast<__nv_bfloat16 *>(inv + M::INV_BLOCK + j * 48) = __float2bfloat16_rn(y[j] - __bfloat162float(hi));
+                }
+            }
+            named_bar(NB_B, GROUP);
+            const int w = warp - 4, lane = t & 31;
+            if (16 * w < TP) {  // rows 16 w .. 16 w + 15 of W: blocks beyond the w-th are 0
+                const int g = lane >> 2, q2 = lane & 3;
+                float c[TP / 16][8];
+#pragma unroll
+                for (int b = 0; b < TP / 16; ++b)
+                    if (b <= w)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {  // (rows g, g + 8) x (columns 2 q2, 2 q2 + 1 of each half)
+                            const int r = 16 * w + g + 8 * (i & 1), col = 16 * b + 8 * (i >> 1) + 2 * q2;
+                            const float2 f = *reinterpret_cast<const float2 *>(sm + M::PW + r * 256 + ((col >> 2) ^ (r & 15)) * 16 +
+                                                                               (col & 2) * 4);
+                            c[b][4 * (i >> 1) + 2 * (i & 1)] = f.x;
+                            c[b][4 * (i >> 1) + 2 * (i & 1) + 1] = f.y;
+                        }
+                __syncwarp();  // W takes the place of P's rows
+                // the row of a 16 x 16 block whose address this lane gives, and the half
+                const int br = (lane & 7) + (lane & 8), bh = lane >> 4;
+#pragma unroll
+                for (int b = TP / 16 - 1; b >= 0; --b) {
+                    Frag f;
+                    if (b <= w) {
+                        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        const uint32_t inv = sb + M::INV + b * 2 * M::INV_BLOCK + br * 48 + bh * 16;
+                        block_product(y, split_frag(c[b], false), inv, inv + M::INV_BLOCK);
+                        f = split_frag(y, false);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f.hi[i] = f.lo[i] = 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 16 * w + g + 8 * (i & 1);
+                        const uint32_t at = sb + M::PW + (r >> 3) * 2048 + (r & 7) * 128 + (((2 * b + (i >> 1)) ^ (r & 7)) << 4) + 4 * q2;
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(f.hi[i]) : "memory");
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024), "r"(f.lo[i]) : "memory");
+                    }
+                    if (b <= w) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f.hi[i] ^= 0x80008000u, f.lo[i] ^= 0x80008000u;
+#pragma unroll
+                        for (int e = 0; e < b; ++e)
+                            block_product(c[e], f, sw128_addr(sb + M::LHI, 16 * b + br, 2 * e + bh),
+                                          sw128_addr(sb + M::LLO, 16 * b + br, 2 * e + bh));
+                    }
+                }
+                fence_proxy_async_smem();
+            }
+        } else {
+            // v has its place once the state has left it; until then its lines come as far as L2
+            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + n * a.sv.batch + h * a.sv.head;
+            for (int e = t; e < T * V / 64; e += GROUP)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(v + (e >> (V == 128)) * a.sv.token + (V == 128 ? e & 1 : 0) * 64));
+            ok = mbar_wait_warp(bars + BAR_S, phase, abort_flag);
+            if (column) {
+                const float *s = reinterpret_cast<const float *>(sm) + t;
+#pragma unroll 1
+                for (int c = 0; c < K / 32; ++c) {
+                    float y[32];
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] = s[i * V];
+                    s += 32 * V;
+                    split_pack16(y, hi, lo);
+                    tmem_st16x2(lanes + 16 * c, hi, lanes + K / 2 + 16 * c, lo);
+                }
+            }
+            tc_fence_before();
+            bar_arrive(NB_FREE, NT);
+            named_bar(NB_STATE, NT);  // the state is in TMEM, G has been read
+            if (warp == 0) {
+                tc_fence_after();
+                if (t == 0) {
+                    for (int part = 0; part < 2; ++part)
+                        for (int kb = 0; kb < K / 64; ++kb)
+                            mma_chain_ta<4, 2>(tmem + kD1, tmem + part * (K / 2) + 32 * kb, kdesc(sb + M::KQ + kb * kBlock), ID_2,
+                                               part + kb);
+                    mma_commit(bars + BAR_D);
+                }
+                __syncwarp();
+            } else {
+                const int c = t & (V / 8 - 1);
+                const uint32_t dst = sb + M::VAL + 16 * c;
+                constexpr int pieces = V == 128 ? 4 : 3, step = (GROUP - 32) >> pieces;
+                if (vec) {
+#pragma unroll 4
+                    for (int r = (t - 32) >> pieces; r < T; r += step) cp_async16(dst + 2 * V * r, v + r * a.sv.token + 8 * c, true);
+                } else {
+#pragma unroll 1
+                    for (int r = (t - 32) >> pieces; r < T; r += step) copy_piece(dst + 2 * V * r, v + r * a.sv.token + 8 * c, true);
+                }
+            }
+            cp_async_wait();
+            ok = mbar_wait_warp(bars + BAR_D, phase, abort_flag) && ok;
+            tc_fence_after();
+            named_bar(NB_A, GROUP);  // v is there
+            const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
+            const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sm + M::VAL) + t;
+            if (column)
+#pragma unroll 1
+                for (int c = 0; c < TP / 16; ++c) {
+                    uint32_t ks[16], hi[8], lo[8];
+                    float b[16], bg[16], y[16];
+                    tmem_ld16(lanes + kD1 + 16 * c, ks);
+                    lds16f(s_b + 16 * c, b);
+                    lds16f(s_bg + 16 * c, bg);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        if (gone >> j & 1 || 16 * c + j >= T) y[j] = 0.f;
+                        y[j] = fmaf(-bg[j], __uint_as_float(ks[j]), b[j] * __bfloat162float(vs[(16 * c + j) * V]));
+                    if (16 * c + 16 > T || dead) {  // past the last node v was not written
+                        const uint32_t gone = (s_absent[c >> 1] | s_bad[c >> 1]) >> (16 * (c & 1));
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (gone >> j & 1 || 16 * c + j >= T) y[j] = 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split_pair(y[2 * i], y[2 * i + 1], hi[i], lo[i]);
+                    tmem_st8x2(lanes + 8 * c, hi, lanes + kRlo + 8 * c, lo);
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) split_pair(y[2 * i], y[2 * i + 1], hi[i], lo[i]);
-                tmem_st8x2(lanes + 8 * c, hi, lanes + kRlo + 8 * c, lo);
-            }
-    }
-    tc_fence_before();
-    ok = __syncthreads_and(ok) != 0;
-    tc_fence_after();
-    if (ok) {
-        if (t == 0) {
-            const uint64_t hi = sdesc_sw128(sb + M::PW, 16, 2048), lo = sdesc_sw128(sb + M::PW + 1024, 16, 2048);
-            mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem, hi, ID_1, 0);
-            mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem + kRlo, hi, ID_1, 1);
-            mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem, lo, ID_1, 1);
-            mma_commit(bars + BAR_O);
         }
-        __syncwarp();
-        ok = mbar_wait_warp(bars + BAR_O, 0, abort_flag);
+        if (more) ahead = look(head + gridDim.x);  // the products have read k and q
+        tc_fence_before();
+        ok = __syncthreads_and(ok) != 0;
         tc_fence_after();
-        // o by way of shared memory (the place of W, whose products are done), rows in 16-byte pieces
-        __nv_bfloat16 *s_o = reinterpret_cast<__nv_bfloat16 *>(sm);
-        if (column)
+        if (ok) {
+            if (t == 0) {
+                const uint64_t hi = sdesc_sw128(sb + M::PW, 16, 2048), lo = sdesc_sw128(sb + M::PW + 1024, 16, 2048);
+                mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem, hi, ID_1, 0);
+                mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem + kRlo, hi, ID_1, 1);
+                mma_chain_ta<TP / 16, 2>(tmem + kD2, tmem, lo, ID_1, 1);
+                mma_commit(bars + BAR_O);
+            }
+            __syncwarp();
+            ok = mbar_wait_warp(bars + BAR_O, phase, abort_flag);
+            tc_fence_after();
+            // o by way of shared memory (the place of W, whose products are done), rows in 16-byte pieces
+            __nv_bfloat16 *s_o = reinterpret_cast<__nv_bfloat16 *>(sm);
+            if (column)
 #pragma unroll 1
-            for (int c = t / GROUP; 16 * c < T; c += 2) {
-                uint32_t sq[16], d2[16];
-                float sg[16];
-                tmem_ld16x2(lanes + kD1 + TP + 16 * c, sq, lanes + kD2 + 16 * c, d2);
-                lds16f(s_sg + 16 * c, sg);
+                for (int c = t / GROUP; 16 * c < T; c += 2) {
+                    uint32_t sq[16], d2[16];
+                    float sg[16];
+                    tmem_ld16x2(lanes + kD1 + TP + 16 * c, sq, lanes + kD2 + 16 * c, d2);
+                    lds16f(s_sg + 16 * c, sg);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    s_o[(16 * c + i) * V + lane_row] =
-                        __float2bfloat16_rn(fmaf(sg[i], __uint_as_float(sq[i]), a.scale * __uint_as_float(d2[i])));
-            }
-        named_bar(NB_OUT, NT);
-        const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
-        if (dead) {
-            for (int i = t / GROUP; i < T && column; i += 2) {
-                if (s_absent[i >> 5] >> (i & 31) & 1) s_o[i * V + lane_row] = __float2bfloat16_rn(0.f);
-                if (s_bad[i >> 5] >> (i & 31) & 1) s_o[i * V + lane_row] = __float2bfloat16_rn(nan);
-            }
+                    for (int i = 0; i < 16; ++i)
+                        s_o[(16 * c + i) * V + lane_row] =
+                            __float2bfloat16_rn(fmaf(sg[i], __uint_as_float(sq[i]), a.scale * __uint_as_float(d2[i])));
+                }
             named_bar(NB_OUT, NT);
+            const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
+            if (dead) {
+                for (int i = t / GROUP; i < T && column; i += 2) {
+                    if (s_absent[i >> 5] >> (i & 31) & 1) s_o[i * V + lane_row] = __float2bfloat16_rn(0.f);
+                    if (s_bad[i >> 5] >> (i & 31) & 1) s_o[i * V + lane_row] = __float2bfloat16_rn(nan);
+                }
+                named_bar(NB_OUT, NT);
+            }
+            constexpr int pieces = V == 128 ? 4 : 3;
+            const int c = t & (V / 8 - 1);
+            for (int r = t >> pieces; r < T; r += NT >> pieces)
+                *reinterpret_cast<uint4 *>(o + r * o_tok + 8 * c) = *reinterpret_cast<const uint4 *>(s_o + r * V + 8 * c);
         }
-        constexpr int pieces = V == 128 ? 4 : 3;
-        const int c = t & (V / 8 - 1);
-        for (int r = t >> pieces; r < T; r += NT >> pieces)
-            *reinterpret_cast<uint4 *>(o + r * o_tok + 8 * c) = *reinterpret_cast<const uint4 *>(s_o + r * V + 8 * c);
+        fence_proxy_async_smem();  // the next state comes over what has been written here
+        tc_fence_before();
+        ok = __syncthreads_and(ok) != 0;
+        if (!ok) {  // a wait ran out (its limit is a second): no copy of a state is left in flight, and the rows show it
+            if (t == 0) mbar_drain(bars + BAR_S, phase);
+            if (t < V)
+                for (int i = 0; i < T; ++i) o[i * o_tok + t] = __float2bfloat16_rn(nan);
+        }
+        phase ^= 1;
     }
-    // A wait that ran out (its limit is a second): nothing in flight is left behind, and the row shows it.
-    ok = __syncthreads_and(ok) != 0;
-    if (!ok) {
-        if (t == 0) mbar_drain(bars + BAR_S, 0);
-        if (t < V)
-            for (int i = 0; i < T; ++i) o[i * o_tok + t] = __float2bfloat16_rn(nan);
-    }
-    tc_fence_before();
+    cp_async_wait();
     __syncthreads();
-    if (warp == SETUP) {
+    if (warp == SETUP && !first) {
         tc_fence_after();
-        tmem_dealloc(tmem, kCols);
+        tmem_dealloc(misc[0], kCols);
     }
 }
 
@@ -524,7 +550,8 @@ template <int K, int V, int TP> cudaError_t launch(const DecodeArgs &a, bool vec
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k_tree_tc<K, V, TP>, bytes, done);
     if (e != cudaSuccess) return e;
-    return launch_behind(k_tree_tc<K, V, TP>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)a.G), NT, bytes, st, a, vec);
+    const int heads = a.n_seqs * a.Hv;
+    return launch_behind(k_tree_tc<K, V, TP>, dim3((unsigned)(heads < 2 * kSMs ? heads : 2 * kSMs)), NT, bytes, st, a, vec, heads);
 }
 
 template <int K, int V> cudaError_t launch_nodes(const DecodeArgs &a, bool vec, cudaStream_t st) {

@@ -435,3 +435,46 @@ def test_tree_layouts_and_empty():
     check_o(o, tree_reference(x, parents, x["state"][x["idx"].long()]), bf16, BF16_TOL)
     e = make(2, 0, 1, 2, 64, 64, bf16)
     assert gdn.tree_gated_delta_rule(*args(e), torch.empty(2, 0, dtype=torch.int32, device="cuda"), e["state"].cuda()).numel() == 0
+
+
+@pytest.mark.parametrize("T", [5, 40])
+def test_tree_many_heads_with_idle_rows(T):
+    """More heads than the GPU takes at once, rows without a slot between the others: every CTA's next heads."""
+    x = make(30, T, 8, 32, 128, 128, bf16, seed=26)
+    parents = random_parents(30, T, 7)
+    idx = x["idx"].clone()
+    idx[3::4], idx[5] = -1, x["state"].shape[0]
+    o = gdn.tree_gated_delta_rule(*args(x), parents.cuda(), x["state"].cuda(), state_indices=idx.cuda())
+    some = [0, 1, 13, 28]
+    few = {n: (y[some] if isinstance(y, torch.Tensor) and n != "state" else y) for n, y in x.items()}
+    ref = tree_reference(few, parents[some], x["state"][x["idx"][some].long()])
+    check_o(o[some], ref, bf16, BF16_TOL)
+    assert (o[3::4] == 0).all() and o[5].isnan().all()
+    live = [b for b in range(30) if b % 4 != 3 and b != 5]
+    assert o[live].isfinite().all() and (o[live].float().abs().amax(dim=(1, 3)) > 0).all()
+
+
+def test_recurrent_many_heads_with_idle_rows():
+    x = make(50, 3, 8, 32, 128, 128, bf16, seed=27)
+    idx = x["idx"].clone()
+    idx[3::4], idx[5] = -1, x["state"].shape[0]
+    lists = torch.tensor([[2, 0, -1], [1, -1, 0], [0, 1, 2], [-1, -1, -1], [0, 3, 1]], dtype=torch.int32).repeat(10, 1)
+    state = x["state"].cuda()
+    o = gdn.recurrent_gated_delta_rule(*args(x), state, state_indices=idx.cuda(), token_indices=lists.cuda())
+    before = x["state"][x["idx"].long()]
+    for b in (0, 1, 2, 4, 17, 32, 49):
+        tokens = [t for t in lists[b].tolist()]
+        tokens = tokens[:tokens.index(-1)] if -1 in tokens else tokens
+        bad = 3 in tokens
+        if b == 4 or bad:
+            assert bad and o[b, 1:].isnan().all()
+            assert torch.equal(state[int(x["idx"][b])].cpu(), before[b])
+            continue
+        ref_o, ref_s = reference({n: (y[b:b + 1] if isinstance(y, torch.Tensor) and n != "state" else y) for n, y in x.items()},
+                                 before[b:b + 1], [tokens])
+        check_state(state[int(x["idx"][b])], ref_s[0])
+        check_o(o[b, :len(tokens)], ref_o[0], bf16)
+        assert (o[b, len(tokens):] == 0).all()
+    assert (o[3::4] == 0).all() and o[5].isnan().all()
+    for b in (3, 5, 7):
+        assert torch.equal(state[int(x["idx"][b])].cpu(), before[b])
