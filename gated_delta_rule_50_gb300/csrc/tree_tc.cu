@@ -17,6 +17,8 @@
 // S arrives by one bulk copy (a head's state is contiguous); its place in shared memory then holds L, P, W and o.
 // Two CTAs stay on each SM (109 KB, 256 TMEM columns each) and take head after head, so that one's copies run under
 // the other's arithmetic; k, q and the gates of a CTA's next head come while group B finishes W.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -32,8 +34,15 @@ constexpr int GROUP = 128, NT = 2 * GROUP, kSMs = 152;
 constexpr uint32_t kBlock = 16384;  // 128 rows of 64 bf16: one K block of [K; Q]
 constexpr uint32_t kCols = 256;     // TMEM: S^T hi, lo (K columns), later R^T hi, lo and D2 | G, later D1
 constexpr uint32_t kRlo = 32, kD2 = 64, kD1 = 128;
-enum { BAR_S = 0, BAR_G = 8, BAR_D = 16, BAR_O = 24 };  // mbarriers: the state, G, D1, D2
-enum { NB_STATE = 1, NB_B = 2, NB_FREE = 3, NB_A = 4, NB_DIAG = 5, NB_OUT = 6, NB_WALK = 7 };  // named barriers
+enum { BAR_S = 0, BAR_G = 8, BAR_D = 16, BAR_O = 24, BAR_K = 32, BAR_V = 40, BARS = 6 };  // state, G, D1, D2, k and q, v
+enum { NB_STATE = 1, NB_B = 2, NB_FREE = 3, NB_A = 4, NB_DIAG = 5, NB_INV = 6, NB_OUT = 7, NB_WALK = 8 };  // named barriers
+
+// q, k, v and o as [columns of all heads][token][batch]
+struct RowMaps {
+    CUtensorMap q, k, v, o;
+    bool mapped;  // the maps of q, k and v describe them (see rows_map); otherwise their rows are copied in pieces
+    bool rows16;  // pieces of 16 bytes are aligned
+};
 
 template <int K, int V, int TP> struct Map {
     // over the state once it is in TMEM: P in fp32, then row by row W (eight rows of hi, then of lo, in the place of
@@ -48,7 +57,7 @@ template <int K, int V, int TP> struct Map {
     // (a, parent), the same of the parent, beta, beta Gam, scale Gam: TP each
     static constexpr uint32_t VEC = TABLE + TP / 2 * LS * 4;
     static constexpr uint32_t BAR = VEC + 7 * TP * 4;
-    static constexpr uint32_t MISC = BAR + 32;
+    static constexpr uint32_t MISC = BAR + 8 * BARS;
     static constexpr uint32_t bytes = MISC + 32 + 1024;
 };
 
@@ -63,12 +72,22 @@ __device__ __forceinline__ uint64_t kdesc(uint32_t a) { return sdesc_sw128(a, 16
 __device__ __forceinline__ void bar_arrive(uint32_t id, uint32_t threads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// 16 bytes to shared memory, zeros where there is no source row
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16u : 0u) : "memory");
+// Rows of all tokens of batch row n, from column x on
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int n) {
+    tma_load_3d(dst, map, bar, x, 0, n);
 }
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-__device__ __forceinline__ void copy_piece(uint32_t dst, const __nv_bfloat16 *src, bool in) {  // any alignment
+__device__ __forceinline__ void store_rows(const CUtensorMap *map, uint32_t src, int x, int n) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(0), "r"(n), "r"(src)
+                 : "memory");
+}
+// 16 bytes of a row, 0 where there is no such row; asynchronously where they are aligned
+__device__ __forceinline__ void copy_piece(uint32_t dst, const __nv_bfloat16 *src, bool in, bool rows16) {
+    if (in && rows16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        return;
+    }
     uint32_t w[4] = {0, 0, 0, 0};
     if (in)
 #pragma unroll
@@ -76,6 +95,7 @@ __device__ __forceinline__ void copy_piece(uint32_t dst, const __nv_bfloat16 *sr
             w[i] = (uint32_t)__bfloat16_as_ushort(src[2 * i]) | (uint32_t)__bfloat16_as_ushort(src[2 * i + 1]) << 16;
     st_shared_v4(dst, w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Two fp32 products at once, on a pair of registers
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
     uint64_t p;
@@ -132,7 +152,7 @@ __device__ __forceinline__ void block_product(float (&c)[8], const Frag &a, uint
 }
 
 template <int K, int V, int TP>
-__global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ DecodeArgs a, bool vec, int heads) {
+__global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ DecodeArgs a, const __grid_constant__ RowMaps maps, int heads) {
     using M = Map<K, V, TP>;
     constexpr uint32_t ID_1 = idesc_bf16(128, TP, 0, 0), ID_2 = idesc_bf16(128, 2 * TP, 0, 0);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -141,6 +161,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
     const int t = threadIdx.x, warp = t >> 5, T = a.T, lane_row = t & (GROUP - 1);
     const float nan = __int_as_float(0x7fffffff);
     constexpr int SETUP = 7;  // the warp that sets up, copies the state and issues G
+    constexpr int INVERTERS = (TP + 31) / 32 * 32;  // threads of group A's warps 1 and 2 that invert, rounded up to warps
     const bool group_b = t >= GROUP, column = lane_row < V;  // the same for a whole warp
     const int64_t o_tok = (int64_t)a.Hv * V;
     int4 *s_up = reinterpret_cast<int4 *>(sm + M::VEC);  // e^g (its bits) and the parent, then the parent's
@@ -151,15 +172,15 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
     uint32_t *s_absent = misc + 2, *s_bad = misc + 4;  // nodes of each kind, a bit each
     if (warp == SETUP) {
         if (t == 32 * SETUP) {
-            for (int i = 0; i < 4; ++i) mbar_init(bars + 8 * i, 1);
+            for (int i = 0; i < BARS; ++i) mbar_init(bars + 8 * i, 1);
             misc[1] = 0;
             fence_mbar_init();
         }
         __syncwarp();
     }
     wait_for_previous();
-    // What a head's turn begins with: rows of k and q on the way to shared memory (group A, 16 bytes per thread and a
-    // multiple of eight rows at a time), gates and parent of this thread's node, the slot
+    // What a head's turn begins with: rows of k and q on the way to shared memory (one copy each per 64 columns; what
+    // is past the last node comes as 0), gates and parent of this thread's node, the slot
     struct Ahead {
         int64_t slot;
         float g, beta;
@@ -168,37 +189,36 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
     auto look = [&](int head) {
         const int n = head / a.Hv, h = head - n * a.Hv, hq = h / a.G;
         Ahead f = {a.state_indices ? a.state_indices[n] : n, 0.f, 0.f, -1};
-        if (!group_b) {
+        if (t < T) {
+            f.g = a.g[n * a.sg.batch + h * a.sg.head + t * a.sg.token];
+            f.beta = a.beta[n * a.sb.batch + h * a.sb.head + t * a.sb.token];
+            f.up = a.parents[(int64_t)n * T + t];
+        }
+        if (maps.mapped) {
+            if (t == 0) {
+                mbar_arrive_expect_tx(bars + BAR_K, 2 * TP * K * 2);
+                for (int kb = 0; kb < K / 64; ++kb) {
+                    load_rows(sb + M::KQ + kb * kBlock, &maps.k, bars + BAR_K, hq * (int)a.sk.head + 64 * kb, n);
+                    load_rows(sb + M::KQ + kb * kBlock + TP * 128, &maps.q, bars + BAR_K, hq * (int)a.sq.head + 64 * kb, n);
+                }
+            }
+        } else if (!group_b) {
             constexpr int PIECES = K / 8, ROWS = GROUP / PIECES;
             const int x = t % PIECES, r0 = t / PIECES;
             const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + n * a.sk.batch + hq * a.sk.head + 8 * x;
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + n * a.sq.batch + hq * a.sq.head + 8 * x;
             const uint32_t dst = sw128_addr(sb + M::KQ + (x >> 3) * kBlock, r0, x & 7);
-            if (t < T) {
-                f.g = a.g[n * a.sg.batch + h * a.sg.head + t * a.sg.token];
-                f.beta = a.beta[n * a.sb.batch + h * a.sb.head + t * a.sb.token];
-                f.up = a.parents[(int64_t)n * T + t];
-            }
-            if (vec) {
-#pragma unroll
-                for (int r = 0; r < TP; r += ROWS) {
-                    const bool in = r0 + r < T;
-                    cp_async16(dst + r * 128, in ? k + (r0 + r) * a.sk.token : k, in);
-                    cp_async16(dst + (TP + r) * 128, in ? q + (r0 + r) * a.sq.token : q, in);
-                }
-            } else {
 #pragma unroll 1
-                for (int r = 0; r < TP; r += ROWS) {
-                    copy_piece(dst + r * 128, k + (r0 + r) * a.sk.token, r0 + r < T);
-                    copy_piece(dst + (TP + r) * 128, q + (r0 + r) * a.sq.token, r0 + r < T);
-                }
+            for (int r = 0; r < TP; r += ROWS) {  // a multiple of eight rows at a time
+                copy_piece(dst + r * 128, k + (r0 + r) * a.sk.token, r0 + r < T, maps.rows16);
+                copy_piece(dst + (TP + r) * 128, q + (r0 + r) * a.sq.token, r0 + r < T, maps.rows16);
             }
         }
         return f;
     };
     Ahead ahead = look(blockIdx.x);
     bool ok = true, first = true;
-    uint32_t phase = 0;  // of every mbarrier: each is used once per head
+    uint32_t phase = 0, phase_k = 0;  // of the mbarriers: each is used once per head, that of k and q for idle ones too
     for (int head = blockIdx.x; head < heads; head += gridDim.x) {
         const int n = head / a.Hv, h = head - n * a.Hv;
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)n * T * a.Hv + h) * V;
@@ -209,7 +229,9 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
         if (slot < 0 || slot >= a.n_slots || !ok) {  // an idle row, no such slot, or a wait that ran out before
             if (t < V)
                 for (int i = 0; i < T; ++i) o[i * o_tok + t] = __float2bfloat16_rn(slot < 0 ? 0.f : nan);
-            cp_async_wait();
+            copies_done();
+            if (maps.mapped && t == 0) mbar_drain(bars + BAR_K, phase_k);  // their place is wanted again
+            phase_k ^= 1;
             if (more) ahead = look(head + gridDim.x);
             continue;
         }
@@ -229,7 +251,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             *reinterpret_cast<int2 *>(s_up + t) = make_int2(__float_as_int(expf(ga)), up);
             s_b[t] = be;
         }
-        cp_async_wait();
+        copies_done();
         fence_proxy_async_smem();
         tc_fence_before();
         __syncthreads();
@@ -237,6 +259,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
         const uint32_t tmem = misc[0], lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         if (group_b) {
             if (warp == SETUP) {
+                if (maps.mapped) ok = mbar_wait_warp(bars + BAR_K, phase_k, abort_flag);
                 if (t == 32 * SETUP) {
                     for (int kb = 0; kb < K / 64; ++kb)
                         mma_chain<4, 2, 2>(tmem + kD1, kdesc(sb + M::KQ + kb * kBlock), kdesc(sb + M::KQ + kb * kBlock), ID_1, kb);
@@ -278,7 +301,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                 s_bg[node] = kind ? 0.f : b * prod;
                 s_sg[node] = kind ? 0.f : a.scale * prod;
             }
-            ok = mbar_wait_warp(bars + BAR_G, phase, abort_flag);
+            ok = mbar_wait_warp(bars + BAR_G, phase, abort_flag) && ok;
             tc_fence_after();
             float x[TP];
 #pragma unroll
@@ -330,39 +353,11 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                         for (int i = 0; i < 8; ++i) diag[i * M::DS] = x[8 * c + i];
                     }
             }
-            // the inverses need the diagonal alone: the warps that make them go on while the others split L
-            constexpr int INV_WARP = (GROUP - TP) / 32;  // the first warp of the group with a column of an inverse
-            if ((warp & 3) >= INV_WARP) named_bar(NB_DIAG, GROUP);
-            else bar_arrive(NB_DIAG, GROUP);
+            bar_arrive(NB_DIAG, GROUP + INVERTERS);  // group A makes the inverses of the blocks on the diagonal
             if (has_row && !is_p)
 #pragma unroll
                 for (int c = 0; c < TP / 8; ++c) st_split_chunk(sb + M::LHI, sb + M::LLO, node, c, x + 8 * c);
-            if (row >= GROUP - TP) {  // a column of an inverse per thread: a finished y_i at once into all rows below it
-                const int u = row - (GROUP - TP), j0 = u & 15;
-                const float *diag = reinterpret_cast<const float *>(sm + M::DIAG) + (u & ~15) * M::DS;
-                float y[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = j == j0 ? 1.f : 0.f;
-#pragma unroll
-                for (int i = 0; i < 15; ++i) {
-                    float l[16];
-#pragma unroll
-                    for (int j = (i + 1) / 4 * 4; j < 16; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(diag + i * M::DS + j);
-                        l[j] = f.x, l[j + 1] = f.y, l[j + 2] = f.z, l[j + 3] = f.w;
-                    }
-#pragma unroll
-                    for (int j = i + 1; j < 16; ++j) y[j] = fmaf(-l[j], y[i], y[j]);
-                }
-                unsigned char *inv = sm + M::INV + (u >> 4) * 2 * M::INV_BLOCK + 2 * j0;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(y[j]);
-                    *reinterpret_cast<__nv_bfloat16 *>(inv + j * 48) = hi;
-                    *reinterpret_cast<__nv_bfloat16 *>(inv + M::INV_BLOCK + j * 48) = __float2bfloat16_rn(y[j] - __bfloat162float(hi));
-                }
-            }
-            named_bar(NB_B, GROUP);
+            named_bar(NB_INV, GROUP + INVERTERS);
             const int w = warp - 4, lane = t & 31;
             if (16 * w < TP) {  // rows 16 w .. 16 w + 15 of W: blocks beyond the w-th are 0
                 const int g = lane >> 2, q2 = lane & 3;
@@ -412,10 +407,6 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                 fence_proxy_async_smem();
             }
         } else {
-            // v has its place once the state has left it; until then its lines come as far as L2
-            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + n * a.sv.batch + h * a.sv.head;
-            for (int e = t; e < T * V / 64; e += GROUP)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(v + (e >> (V == 128)) * a.sv.token + (V == 128 ? e & 1 : 0) * 64));
             ok = mbar_wait_warp(bars + BAR_S, phase, abort_flag);
             if (column) {
                 const float *s = reinterpret_cast<const float *>(sm) + t;
@@ -436,6 +427,10 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             if (warp == 0) {
                 tc_fence_after();
                 if (t == 0) {
+                    if (maps.mapped) {  // v has its place now that the state has left it
+                        mbar_arrive_expect_tx(bars + BAR_V, TP * V * 2);
+                        load_rows(sb + M::VAL, &maps.v, bars + BAR_V, h * (int)a.sv.head, n);
+                    }
                     for (int part = 0; part < 2; ++part)
                         for (int kb = 0; kb < K / 64; ++kb)
                             mma_chain_ta<4, 2>(tmem + kD1, tmem + part * (K / 2) + 32 * kb, kdesc(sb + M::KQ + kb * kBlock), ID_2,
@@ -443,22 +438,48 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                     mma_commit(bars + BAR_D);
                 }
                 __syncwarp();
-            } else {
-                const int c = t & (V / 8 - 1);
-                const uint32_t dst = sb + M::VAL + 16 * c;
-                constexpr int pieces = V == 128 ? 4 : 3, step = (GROUP - 32) >> pieces;
-                if (vec) {
-#pragma unroll 4
-                    for (int r = (t - 32) >> pieces; r < T; r += step) cp_async16(dst + 2 * V * r, v + r * a.sv.token + 8 * c, true);
-                } else {
-#pragma unroll 1
-                    for (int r = (t - 32) >> pieces; r < T; r += step) copy_piece(dst + 2 * V * r, v + r * a.sv.token + 8 * c, true);
+            } else if (t < 32 + INVERTERS) {
+                named_bar(NB_DIAG, GROUP + INVERTERS);
+                if (t >= 32 && t < 32 + TP) {  // a column of an inverse per thread: a finished y_i at once into all rows below it
+                    const int u = t - 32, j0 = u & 15;
+                    const float *diag = reinterpret_cast<const float *>(sm + M::DIAG) + (u & ~15) * M::DS;
+                    float y[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[j] = j == j0 ? 1.f : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 15; ++i) {
+                        float l[16];
+#pragma unroll
+                        for (int j = (i + 1) / 4 * 4; j < 16; j += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(diag + i * M::DS + j);
+                            l[j] = f.x, l[j + 1] = f.y, l[j + 2] = f.z, l[j + 3] = f.w;
+                        }
+#pragma unroll
+                        for (int j = i + 1; j < 16; ++j) y[j] = fmaf(-l[j], y[i], y[j]);
+                    }
+                    unsigned char *inv = sm + M::INV + (u >> 4) * 2 * M::INV_BLOCK + 2 * j0;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(y[j]);
+                        *reinterpret_cast<__nv_bfloat16 *>(inv + j * 48) = hi;
+                        *reinterpret_cast<__nv_bfloat16 *>(inv + M::INV_BLOCK + j * 48) = __float2bfloat16_rn(y[j] - __bfloat162float(hi));
+                    }
                 }
+                bar_arrive(NB_INV, GROUP + INVERTERS);
             }
-            cp_async_wait();
             ok = mbar_wait_warp(bars + BAR_D, phase, abort_flag) && ok;
             tc_fence_after();
-            named_bar(NB_A, GROUP);  // v is there
+            if (maps.mapped) {
+                ok = mbar_wait_warp(bars + BAR_V, phase, abort_flag) && ok;
+            } else {
+                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + n * a.sv.batch + h * a.sv.head;
+                for (int e = t; e < TP * (V / 8); e += GROUP) {
+                    const int r = e / (V / 8), c = e % (V / 8);
+                    copy_piece(sb + M::VAL + 16 * e, v + r * a.sv.token + 8 * c, r < T, maps.rows16);
+                }
+                copies_done();
+                named_bar(NB_A, GROUP);
+            }
             const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
             const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sm + M::VAL) + t;
             if (column)
@@ -472,11 +493,11 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         y[j] = fmaf(-bg[j], __uint_as_float(ks[j]), b[j] * __bfloat162float(vs[(16 * c + j) * V]));
-                    if (16 * c + 16 > T || dead) {  // past the last node v was not written
+                    if (dead) {
                         const uint32_t gone = (s_absent[c >> 1] | s_bad[c >> 1]) >> (16 * (c & 1));
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if (gone >> j & 1 || 16 * c + j >= T) y[j] = 0.f;
+                            if (gone >> j & 1) y[j] = 0.f;
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) split_pair(y[2 * i], y[2 * i + 1], hi[i], lo[i]);
@@ -498,7 +519,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             __syncwarp();
             ok = mbar_wait_warp(bars + BAR_O, phase, abort_flag);
             tc_fence_after();
-            // o by way of shared memory (the place of W, whose products are done), rows in 16-byte pieces
+            // o by way of shared memory (the place of W, whose products are done), all rows in one copy
             __nv_bfloat16 *s_o = reinterpret_cast<__nv_bfloat16 *>(sm);
             if (column)
 #pragma unroll 1
@@ -512,6 +533,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                         s_o[(16 * c + i) * V + lane_row] =
                             __float2bfloat16_rn(fmaf(sg[i], __uint_as_float(sq[i]), a.scale * __uint_as_float(d2[i])));
                 }
+            fence_proxy_async_smem();
             named_bar(NB_OUT, NT);
             const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
             if (dead) {
@@ -519,12 +541,14 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                     if (s_absent[i >> 5] >> (i & 31) & 1) s_o[i * V + lane_row] = __float2bfloat16_rn(0.f);
                     if (s_bad[i >> 5] >> (i & 31) & 1) s_o[i * V + lane_row] = __float2bfloat16_rn(nan);
                 }
+                fence_proxy_async_smem();
                 named_bar(NB_OUT, NT);
             }
-            constexpr int pieces = V == 128 ? 4 : 3;
-            const int c = t & (V / 8 - 1);
-            for (int r = t >> pieces; r < T; r += NT >> pieces)
-                *reinterpret_cast<uint4 *>(o + r * o_tok + 8 * c) = *reinterpret_cast<const uint4 *>(s_o + r * V + 8 * c);
+            if (t == 0) {  // rows past the last node are not written
+                store_rows(&maps.o, sb, h * V, n);
+                bulk_commit();
+                bulk_wait_read_all();
+            }
         }
         fence_proxy_async_smem();  // the next state comes over what has been written here
         tc_fence_before();
@@ -534,9 +558,10 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             if (t < V)
                 for (int i = 0; i < T; ++i) o[i * o_tok + t] = __float2bfloat16_rn(nan);
         }
-        phase ^= 1;
+        phase ^= 1, phase_k ^= 1;
     }
-    cp_async_wait();
+    copies_done();
+    if (t == 0) bulk_wait_all();
     __syncthreads();
     if (warp == SETUP && !first) {
         tc_fence_after();
@@ -544,35 +569,69 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
     }
 }
 
-template <int K, int V, int TP> cudaError_t launch(const DecodeArgs &a, bool vec, cudaStream_t st) {
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+        const bool ok = e == cudaSuccess && found == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    return fn;
+}
+
+// A map of [B][T] rows that hold all heads, boxes of `columns` of all tokens (`rows`, zeros past the last).  False
+// where the layout is another: strides that are no multiples of 16 bytes, heads outside the tokens, rows that overlap.
+bool rows_map(CUtensorMap *m, const void *p, int width, int heads, int T, int B, const gdn_strides &s, int columns, int rows,
+              CUtensorMapSwizzle swizzle) {
+    const int64_t across = heads > 1 ? (heads - 1) * s.head + width : width;  // elements of a row
+    if ((heads > 1 && (s.head < width || s.head % 8)) || across > INT32_MAX) return false;
+    const int64_t batch = B > 1 ? s.batch : 0, token = T > 1 ? s.token : B > 1 ? batch : across;
+    if (token < across || token % 8 || token > (1ll << 38)) return false;
+    if (B > 1 && (batch < T * token || batch % token || batch > (1ll << 38))) return false;
+    const auto fn = encoder();
+    if (!fn || (reinterpret_cast<uintptr_t>(p) & 15)) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)across, (cuuint64_t)T, (cuuint64_t)B};
+    const cuuint64_t strides[2] = {(cuuint64_t)token * 2, (cuuint64_t)(B > 1 ? batch : T * token) * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)columns, (cuuint32_t)rows, 1}, step[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int K, int V, int TP> cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
     constexpr int bytes = (int)Map<K, V, TP>::bytes;
     static_assert(2 * (bytes + 1024) <= 233472, "two CTAs per SM");
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k_tree_tc<K, V, TP>, bytes, done);
     if (e != cudaSuccess) return e;
+    RowMaps maps;
+    const gdn_strides so = {(int64_t)a.T * a.Hv * V, (int64_t)a.Hv * V, V};
+    if (!rows_map(&maps.o, a.o, V, a.Hv, a.T, a.n_seqs, so, V, TP, CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
+    maps.mapped = rows_map(&maps.q, a.q, K, a.Hq, a.T, a.n_seqs, a.sq, 64, TP, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                  rows_map(&maps.k, a.k, K, a.Hq, a.T, a.n_seqs, a.sk, 64, TP, CU_TENSOR_MAP_SWIZZLE_128B) &&
+                  rows_map(&maps.v, a.v, V, a.Hv, a.T, a.n_seqs, a.sv, V, TP, CU_TENSOR_MAP_SWIZZLE_NONE);
+    const int64_t steps = a.sq.batch | a.sq.token | a.sq.head | a.sk.batch | a.sk.token | a.sk.head | a.sv.batch | a.sv.token |
+                          a.sv.head;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+    maps.rows16 = !(steps & 7) && !(at & 15);
     const int heads = a.n_seqs * a.Hv;
-    return launch_behind(k_tree_tc<K, V, TP>, dim3((unsigned)(heads < 2 * kSMs ? heads : 2 * kSMs)), NT, bytes, st, a, vec, heads);
+    return launch_behind(k_tree_tc<K, V, TP>, dim3((unsigned)(heads < 2 * kSMs ? heads : 2 * kSMs)), NT, bytes, st, a, maps, heads);
 }
 
-template <int K, int V> cudaError_t launch_nodes(const DecodeArgs &a, bool vec, cudaStream_t st) {
-    if (a.T <= 16) return launch<K, V, 16>(a, vec, st);
-    if (a.T <= 32) return launch<K, V, 32>(a, vec, st);
-    if (a.T <= 48) return launch<K, V, 48>(a, vec, st);
-    return launch<K, V, 64>(a, vec, st);
+template <int K, int V> cudaError_t launch_nodes(const DecodeArgs &a, cudaStream_t st) {
+    if (a.T <= 16) return launch<K, V, 16>(a, st);
+    if (a.T <= 32) return launch<K, V, 32>(a, st);
+    if (a.T <= 48) return launch<K, V, 48>(a, st);
+    return launch<K, V, 64>(a, st);
 }
-template <int K> cudaError_t launch_width(const DecodeArgs &a, bool vec, cudaStream_t st) {
-    return a.V == 128 ? launch_nodes<K, 128>(a, vec, st) : launch_nodes<K, 64>(a, vec, st);
+template <int K> cudaError_t launch_width(const DecodeArgs &a, cudaStream_t st) {
+    return a.V == 128 ? launch_nodes<K, 128>(a, st) : launch_nodes<K, 64>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_tc(const DecodeArgs &a, int K, cudaStream_t st) {
-    // 16-byte copies of the rows of q, k and v where every row begins on such a boundary
-    const int64_t s = a.sq.batch | a.sq.token | a.sq.head | a.sk.batch | a.sk.token | a.sk.head | a.sv.batch | a.sv.token |
-                      a.sv.head;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
-    const bool vec = !(s & 7) && !(at & 15);
-    return K == 128 ? launch_width<128>(a, vec, st) : launch_width<64>(a, vec, st);
+    return K == 128 ? launch_width<128>(a, st) : launch_width<64>(a, st);
 }
 
 }  // namespace gdn

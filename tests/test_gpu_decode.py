@@ -478,3 +478,41 @@ def test_recurrent_many_heads_with_idle_rows():
     assert (o[3::4] == 0).all() and o[5].isnan().all()
     for b in (3, 5, 7):
         assert torch.equal(state[int(x["idx"][b])].cpu(), before[b])
+
+
+@pytest.mark.parametrize("layout", ["heads outside", "padded rows", "tokens outside", "one shared row", "odd offset"])
+@pytest.mark.parametrize("op", ["tree", "recurrent"])
+def test_layouts(layout, op):
+    """Views that a tensor map can describe, that can only be copied in 16-byte pieces, and that cannot even be that."""
+    x = make(40, 6, 4, 8, 128, 128, bf16, seed=28, packed=False)
+
+    def view(t):
+        if layout == "heads outside":
+            return t.cuda().transpose(1, 2).contiguous().transpose(1, 2)
+        if layout == "tokens outside":
+            return t.cuda().transpose(0, 1).contiguous().transpose(0, 1)
+        if layout == "padded rows":
+            wide = torch.zeros(*t.shape[:2], t.shape[2] * t.shape[3] + 24, dtype=t.dtype, device="cuda")
+            v = wide[..., 8:8 + t.shape[2] * t.shape[3]].view(t.shape)
+        elif layout == "odd offset":
+            v = torch.zeros(t.numel() + 3, dtype=t.dtype, device="cuda")[3:].view(t.shape)
+        else:  # every batch row is the same memory
+            return t[:1].cuda().expand(t.shape)
+        v.copy_(t)
+        return v
+
+    if layout == "one shared row":
+        for n in ("q", "k", "v", "g", "beta"):
+            x[n] = x[n][:1].expand(x[n].shape).contiguous()
+    a = [view(x[n]) for n in ("q", "k", "v")] + [x["g"].cuda(), x["beta"].cuda()]
+    state, idx = x["state"].cuda(), x["idx"].cuda()
+    h0 = x["state"][x["idx"].long()]
+    if op == "tree":
+        parents = random_parents(40, 6, 8)
+        o = gdn.tree_gated_delta_rule(*a, parents.cuda(), state, state_indices=idx)
+        check_o(o, tree_reference(x, parents, h0), bf16, BF16_TOL)
+    else:
+        o = gdn.recurrent_gated_delta_rule(*a, state, state_indices=idx)
+        ref_o, ref_s = reference(x, h0)
+        check_o(o, ref_o, bf16)
+        check_state(state[idx.long()], ref_s)
