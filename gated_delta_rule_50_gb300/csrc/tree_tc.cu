@@ -114,13 +114,10 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 struct Frag {
     uint32_t hi[4], lo[4];
 };
-__device__ __forceinline__ Frag split_frag(const float (&c)[8], bool negate) {  // C of a product -> A of the next
+__device__ __forceinline__ Frag split_frag(const float (&c)[8]) {  // C of a product -> A of the next
     Frag f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) split_pair(c[2 * i], c[2 * i + 1], f.hi[i], f.lo[i]);
-    if (negate)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f.hi[i] ^= 0x80008000u, f.lo[i] ^= 0x80008000u;
     return f;
 }
 __device__ __forceinline__ void mma16816(float *c, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -382,8 +379,8 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                     if (b <= w) {
                         float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                         const uint32_t inv = sb + M::INV + b * 2 * M::INV_BLOCK + br * 48 + bh * 16;
-                        block_product(y, split_frag(c[b], false), inv, inv + M::INV_BLOCK);
-                        f = split_frag(y, false);
+                        block_product(y, split_frag(c[b]), inv, inv + M::INV_BLOCK);
+                        f = split_frag(y);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) f.hi[i] = f.lo[i] = 0u;
