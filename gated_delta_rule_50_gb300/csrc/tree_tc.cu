@@ -1,15 +1,15 @@
 // tree_tc.cu -- the drafted-tree operator on the tensor cores (bf16 io).  The mathematics is in tree.cu, here as
 //
-//   o_t = scale (Gam_t S^T q_t + sum_i W_ti R_i),  R_i = beta_i (v_i - Gam_i S^T k_i),  W = P (I + L)^-1
+//   o_t = scale Gam_t S^T q_t + sum_i W_ti R_i,  R_i = v_i - Gam_i S^T k_i,  W = scale P (I + L)^-1 diag(beta)
 //
-// because W needs no state: it is made while the state is on its way.  One CTA computes a (row, value head):
+// because W needs no state: it is made while the state is on its way.  With L = diag(beta) N the blocks of W are
+// W_b = (scale P_b - sum_{c > b} W_c N_cb) (I + L_bb)^-1 diag(beta_b).  One CTA computes a (row, value head):
 //
 //   all warps     rows of k and q into shared memory
-//   group B       G = [K; Q] K^T (lane r: row r of K K^T, then of Q K^T); the products of e^g down the tree; L and
-//                 P; W by blocks of 16 columns from the last on, W_b = (P_b - sum_{c > b} W_c L_cb) (I + L_bb)^-1,
-//                 16 rows per warp on fragments that stay in registers
+//   group B       G = [K; Q] K^T (lane r: row r of K K^T, then of Q K^T); the products of e^g down the tree; N and
+//                 P; W by blocks of 16 columns from the last on, 16 rows per warp on fragments that stay in registers
 //   group A       S^T from its bulk copy to TMEM; D1 = S^T [K; Q]^T (lane v: S^T k_t, then S^T q_t, of column v);
-//                 R^T to TMEM
+//                 (I + L_bb)^-1 diag(beta_b); R^T to TMEM
 //   all warps     D2 = R^T W^T (lane v: sum_i W_ti R_i of column v); o
 //
 // q and k are bf16 as given; S, R, L, P and W enter products as hi + lo bf16 pairs (16 bits; one bf16 rounding of
@@ -54,9 +54,9 @@ template <int K, int V, int TP> struct Map {
     // the products of e^g from node i to node t >= i: rows t and TP - 1 - t share one (see table_row); the stride
     // puts eight neighbouring rows on different banks
     static constexpr uint32_t TABLE = KQ + K / 64 * kBlock, LS = TP + 4;
-    // (a, parent), the same of the parent, beta, beta Gam, scale Gam: TP each
+    // (a, parent), the same of the parent, beta, Gam, scale Gam: TP each
     static constexpr uint32_t VEC = TABLE + TP / 2 * LS * 4;
-    static constexpr uint32_t BAR = VEC + 7 * TP * 4;
+    static constexpr uint32_t NEXT = VEC + 7 * TP * 4, BAR = NEXT + 3 * TP * 4;  // gates and parents of the next head
     static constexpr uint32_t MISC = BAR + 8 * BARS;
     static constexpr uint32_t bytes = MISC + 32 + 1024;
 };
@@ -95,6 +95,9 @@ __device__ __forceinline__ void copy_piece(uint32_t dst, const __nv_bfloat16 *sr
             w[i] = (uint32_t)__bfloat16_as_ushort(src[2 * i]) | (uint32_t)__bfloat16_as_ushort(src[2 * i + 1]) << 16;
     st_shared_v4(dst, w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ void copy_word(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Two fp32 products at once, on a pair of registers
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
@@ -110,6 +113,15 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+// split_pair with its two differences at once
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16(x0, x1);
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_of(x0, x1)), "l"(pair_of(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u))));
+    float d0, d1;
+    halves(d, d0, d1);
+    lo = pack_bf16(d0, d1);
+}
 // Fragments of 16 x 16 blocks: C as two 16 x 8 accumulators, A as hi and lo of four registers each.
 struct Frag {
     uint32_t hi[4], lo[4];
@@ -117,7 +129,7 @@ struct Frag {
 __device__ __forceinline__ Frag split_frag(const float (&c)[8]) {  // C of a product -> A of the next
     Frag f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split_pair(c[2 * i], c[2 * i + 1], f.hi[i], f.lo[i]);
+    for (int i = 0; i < 4; ++i) split2(c[2 * i], c[2 * i + 1], f.hi[i], f.lo[i]);
     return f;
 }
 __device__ __forceinline__ void mma16816(float *c, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -162,7 +174,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
     const bool group_b = t >= GROUP, column = lane_row < V;  // the same for a whole warp
     const int64_t o_tok = (int64_t)a.Hv * V;
     int4 *s_up = reinterpret_cast<int4 *>(sm + M::VEC);  // e^g (its bits) and the parent, then the parent's
-    float *s_b = reinterpret_cast<float *>(s_up + TP), *s_bg = s_b + TP, *s_sg = s_bg + TP;
+    float *s_b = reinterpret_cast<float *>(s_up + TP), *s_gam = s_b + TP, *s_sg = s_gam + TP;
     float *table = reinterpret_cast<float *>(sm + M::TABLE);
     uint32_t *misc = reinterpret_cast<uint32_t *>(sm + M::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
@@ -177,19 +189,17 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
     }
     wait_for_previous();
     // What a head's turn begins with: rows of k and q on the way to shared memory (one copy each per 64 columns; what
-    // is past the last node comes as 0), gates and parent of this thread's node, the slot
-    struct Ahead {
-        int64_t slot;
-        float g, beta;
-        int up;
-    };
-    auto look = [&](int head) {
+    // is past the last node comes as 0), gates and parent of this thread's node too (in registers the compiler would
+    // wait for them where it runs out of registers); returns the slot
+    float *next_g = reinterpret_cast<float *>(sm + M::NEXT), *next_b = next_g + TP;
+    int *next_up = reinterpret_cast<int *>(next_b + TP);
+    auto look = [&](int head) -> int {
         const int n = head / a.Hv, h = head - n * a.Hv, hq = h / a.G;
-        Ahead f = {a.state_indices ? a.state_indices[n] : n, 0.f, 0.f, -1};
+        const int slot = a.state_indices ? a.state_indices[n] : n;
         if (t < T) {
-            f.g = a.g[n * a.sg.batch + h * a.sg.head + t * a.sg.token];
-            f.beta = a.beta[n * a.sb.batch + h * a.sb.head + t * a.sb.token];
-            f.up = a.parents[(int64_t)n * T + t];
+            copy_word(next_g + t, a.g + n * a.sg.batch + h * a.sg.head + t * a.sg.token);
+            copy_word(next_b + t, a.beta + n * a.sb.batch + h * a.sb.head + t * a.sb.token);
+            copy_word(next_up + t, a.parents + (int64_t)n * T + t);
         }
         if (maps.mapped) {
             if (t == 0) {
@@ -211,17 +221,15 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                 copy_piece(dst + (TP + r) * 128, q + (r0 + r) * a.sq.token, r0 + r < T, maps.rows16);
             }
         }
-        return f;
+        return slot;
     };
-    Ahead ahead = look(blockIdx.x);
+    int next_slot = look(blockIdx.x);
     bool ok = true, first = true;
     uint32_t phase = 0, phase_k = 0;  // of the mbarriers: each is used once per head, that of k and q for idle ones too
     for (int head = blockIdx.x; head < heads; head += gridDim.x) {
         const int n = head / a.Hv, h = head - n * a.Hv;
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)n * T * a.Hv + h) * V;
-        const int64_t slot = ahead.slot;
-        const float ga = ahead.g, be = ahead.beta;
-        const int up = ahead.up;
+        const int slot = next_slot;
         const bool more = head + gridDim.x < heads;
         if (slot < 0 || slot >= a.n_slots || !ok) {  // an idle row, no such slot, or a wait that ran out before
             if (t < V)
@@ -229,7 +237,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             copies_done();
             if (maps.mapped && t == 0) mbar_drain(bars + BAR_K, phase_k);  // their place is wanted again
             phase_k ^= 1;
-            if (more) ahead = look(head + gridDim.x);
+            if (more) next_slot = look(head + gridDim.x);
             continue;
         }
         if (t == 32 * SETUP) {
@@ -244,11 +252,12 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
         }
         first = false;
         for (int e = t; e < TP / 2 * (int)M::LS / 4; e += NT) reinterpret_cast<float4 *>(table)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (t < TP) {
-            *reinterpret_cast<int2 *>(s_up + t) = make_int2(__float_as_int(expf(ga)), up);
-            s_b[t] = be;
-        }
         copies_done();
+        if (t < TP) {  // what this thread copied
+            const bool in = t < T;
+            *reinterpret_cast<int2 *>(s_up + t) = make_int2(__float_as_int(in ? expf(next_g[t]) : 0.f), in ? next_up[t] : -1);
+            s_b[t] = in ? next_b[t] : 0.f;
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncthreads();
@@ -295,7 +304,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                 }
                 const float b = kind ? 0.f : s_b[node];
                 s_b[node] = b;
-                s_bg[node] = kind ? 0.f : b * prod;
+                s_gam[node] = kind ? 0.f : prod;
                 s_sg[node] = kind ? 0.f : a.scale * prod;
             }
             ok = mbar_wait_warp(bars + BAR_G, phase, abort_flag) && ok;
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             named_bar(NB_B, GROUP);  // the products are there
             const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
             if (has_row) {
-                const float b = is_p ? 1.f : s_b[node];
+                const float b = is_p ? a.scale : 1.f;
                 const uint64_t bb = pair_of(b, b);
 #pragma unroll
                 for (int c = 0; c < TP / 4; ++c) {
@@ -347,7 +356,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                     if ((node >> 4) == (c >> 1)) {
                         float *diag = reinterpret_cast<float *>(sm + M::DIAG) + ((node & ~15) + 8 * (c & 1)) * M::DS + (node & 15);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) diag[i * M::DS] = x[8 * c + i];
+                        for (int i = 0; i < 8; ++i) diag[i * M::DS] = s_b[node] * x[8 * c + i];
                     }
             }
             bar_arrive(NB_DIAG, GROUP + INVERTERS);  // group A makes the inverses of the blocks on the diagonal
@@ -414,7 +423,8 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
 #pragma unroll
                     for (int i = 0; i < 32; ++i) y[i] = s[i * V];
                     s += 32 * V;
-                    split_pack16(y, hi, lo);
+    #pragma unroll
+                    for (int i = 0; i < 16; ++i) split2(y[2 * i], y[2 * i + 1], hi[i], lo[i]);
                     tmem_st16x2(lanes + 16 * c, hi, lanes + K / 2 + 16 * c, lo);
                 }
             }
@@ -442,7 +452,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                     const float *diag = reinterpret_cast<const float *>(sm + M::DIAG) + (u & ~15) * M::DS;
                     float y[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = j == j0 ? 1.f : 0.f;
+                    for (int j = 0; j < 16; ++j) y[j] = j == j0 ? s_b[u] : 0.f;
 #pragma unroll
                     for (int i = 0; i < 15; ++i) {
                         float l[16];
@@ -483,13 +493,12 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
 #pragma unroll 1
                 for (int c = 0; c < TP / 16; ++c) {
                     uint32_t ks[16], hi[8], lo[8];
-                    float b[16], bg[16], y[16];
+                    float gam[16], y[16];
                     tmem_ld16(lanes + kD1 + 16 * c, ks);
-                    lds16f(s_b + 16 * c, b);
-                    lds16f(s_bg + 16 * c, bg);
+                    lds16f(s_gam + 16 * c, gam);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        y[j] = fmaf(-bg[j], __uint_as_float(ks[j]), b[j] * __bfloat162float(vs[(16 * c + j) * V]));
+                        y[j] = fmaf(-gam[j], __uint_as_float(ks[j]), __bfloat162float(vs[(16 * c + j) * V]));
                     if (dead) {
                         const uint32_t gone = (s_absent[c >> 1] | s_bad[c >> 1]) >> (16 * (c & 1));
 #pragma unroll
@@ -497,11 +506,11 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                             if (gone >> j & 1) y[j] = 0.f;
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) split_pair(y[2 * i], y[2 * i + 1], hi[i], lo[i]);
+                    for (int i = 0; i < 8; ++i) split2(y[2 * i], y[2 * i + 1], hi[i], lo[i]);
                     tmem_st8x2(lanes + 8 * c, hi, lanes + kRlo + 8 * c, lo);
                 }
         }
-        if (more) ahead = look(head + gridDim.x);  // the products have read k and q
+        if (more) next_slot = look(head + gridDim.x);  // the products have read k and q
         tc_fence_before();
         ok = __syncthreads_and(ok) != 0;
         tc_fence_after();
@@ -528,7 +537,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         s_o[(16 * c + i) * V + lane_row] =
-                            __float2bfloat16_rn(fmaf(sg[i], __uint_as_float(sq[i]), a.scale * __uint_as_float(d2[i])));
+                            __float2bfloat16_rn(fmaf(sg[i], __uint_as_float(sq[i]), __uint_as_float(d2[i])));
                 }
             fence_proxy_async_smem();
             named_bar(NB_OUT, NT);
