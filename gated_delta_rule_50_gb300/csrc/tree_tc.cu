@@ -179,14 +179,12 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
     uint32_t *misc = reinterpret_cast<uint32_t *>(sm + M::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     uint32_t *s_absent = misc + 2, *s_bad = misc + 4;  // nodes of each kind, a bit each
-    if (warp == SETUP) {
-        if (t == 32 * SETUP) {
-            for (int i = 0; i < BARS; ++i) mbar_init(bars + 8 * i, 1);
-            misc[1] = 0;
-            fence_mbar_init();
-        }
-        __syncwarp();
+    if (t == 32 * SETUP) {
+        for (int i = 0; i < BARS; ++i) mbar_init(bars + 8 * i, 1);
+        misc[1] = 0;
+        fence_mbar_init();
     }
+    __syncthreads();  // thread 0 uses BAR_K at once
     wait_for_previous();
     // What a head's turn begins with: rows of k and q on the way to shared memory (one copy each per 64 columns; what
     // is past the last node comes as 0), gates and parent of this thread's node too (in registers the compiler would
@@ -423,7 +421,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
 #pragma unroll
                     for (int i = 0; i < 32; ++i) y[i] = s[i * V];
                     s += 32 * V;
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 16; ++i) split2(y[2 * i], y[2 * i + 1], hi[i], lo[i]);
                     tmem_st16x2(lanes + 16 * c, hi, lanes + K / 2 + 16 * c, lo);
                 }
