@@ -9,9 +9,10 @@
 // 128-byte line per row across the lanes).  The value columns are independent, so nothing crosses warps;
 // the four r lanes of a column group meet through shuffles.
 //
-// Up to about eight tokens the states' way through memory bounds the step (each is read and written once).  Two
-// kernels share the arithmetic: k_recurrent, a CTA per (row, head, part of the columns), for few heads, and
-// k_recurrent_flow, a CTA per SM that has the next states on the way in shared memory while it works, for many.
+// Up to about six tokens the states' way through memory bounds the step (each is read and written once): 64 rows of
+// 32 heads, 128 x 128, one bf16 token, take 45 us, 6.0 TB/s; one row 3.3 us, where reads, sums and writes wait for
+// each other.  Two kernels share the arithmetic: k_recurrent, a warp per CTA and 32 columns, and k_recurrent_flow for
+// lists of tokens on many heads (see launch()).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -60,9 +61,9 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// Up to kTok tokens for `cols` threads, one state column each
-template <int K, typename IO> struct Stage {
-    alignas(16) IO k[kTok<IO>][K], q[kTok<IO>][K], v[kTok<IO>][128];
+// Up to kTok tokens for COLS threads, one state column each
+template <int K, int COLS, typename IO> struct Stage {
+    alignas(16) IO k[kTok<IO>][K], q[kTok<IO>][K], v[kTok<IO>][COLS];
     float a[kTok<IO>], b[kTok<IO>];
     int tok[kTok<IO>];
 };
@@ -73,27 +74,31 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *x) {
                        __uint_as_float(u.y & 0xFFFF0000u));
 }
 
-// The threads of one head (tid = 0 .. cols - 1, columns col0 + tid) and their barrier
-template <int K, typename IO> struct Head {
+// The threads of one head (tid = 0 .. COLS - 1, columns col0 + tid) and, for more than a warp, their barrier
+template <int K, int COLS, typename IO> struct Head {
     static constexpr int NR = K / 4;
     const DecodeArgs &a;
-    Stage<K, IO> &s;
+    Stage<K, COLS, IO> &s;
     const Run u;
     const IO *q, *k, *v;
     const float *g, *beta;
     IO *o;  // row out_row of this head, this thread's column
-    int n, tid, cols, bar;
+    int n, tid, bar;
     bool rows16;  // rows of q, k and v begin on 16-byte boundaries
 
-    __device__ __forceinline__ Head(const DecodeArgs &a, Stage<K, IO> &s, const Run &u, int n, int h, int hq, int col0, int tid, int cols, int bar,
+    __device__ __forceinline__ Head(const DecodeArgs &a, Stage<K, COLS, IO> &s, const Run &u, int n, int h, int hq, int col0, int tid, int bar,
                                     bool rows16)
-        : a(a), s(s), u(u), n(n), tid(tid), cols(cols), bar(bar), rows16(rows16) {
+        : a(a), s(s), u(u), n(n), tid(tid), bar(bar), rows16(rows16) {
         q = static_cast<const IO *>(a.q) + u.b * a.sq.batch + hq * a.sq.head;
         k = static_cast<const IO *>(a.k) + u.b * a.sk.batch + hq * a.sk.head;
         v = static_cast<const IO *>(a.v) + u.b * a.sv.batch + h * a.sv.head + col0 + tid;
         g = a.g + u.b * a.sg.batch + h * a.sg.head;
         beta = a.beta + u.b * a.sb.batch + h * a.sb.head;
         o = a.o ? static_cast<IO *>(a.o) + (u.out_row * a.Hv + h) * a.V + col0 : nullptr;
+    }
+    __device__ __forceinline__ void sync() const {
+        if constexpr (COLS == 32) __syncwarp();
+        else named_bar(bar, COLS);
     }
     __device__ __forceinline__ int64_t o_tok() const { return (int64_t)a.Hv * a.V; }
     // o of tokens [from, len): 0, or NaN where an index was none
@@ -106,7 +111,7 @@ template <int K, typename IO> struct Head {
         int m = min(kTok<IO>, u.len - t0);
         if (a.token_indices) {
             if (tid < m) s.tok[tid] = a.token_indices[(int64_t)n * a.n_steps + t0 + tid];
-            named_bar(bar, cols);
+            sync();
             for (int t = 0; t < m; ++t) {
                 const int at = s.tok[t];
                 if (at >= 0 && at < a.T) continue;
@@ -118,19 +123,19 @@ template <int K, typename IO> struct Head {
         auto token = [&](int t) -> int64_t { return a.token_indices ? s.tok[t] : u.bos + t0 + t; };
         if (rows16) {
             constexpr int PIECE = 16 / (int)sizeof(IO), PIECES = K / PIECE;
-            for (int e = tid; e < m * PIECES; e += cols) {
+            for (int e = tid; e < m * PIECES; e += COLS) {
                 const int t = e / PIECES, x = e % PIECES * PIECE;
                 cp_async16(&s.k[t][x], k + token(t) * a.sk.token + x);
                 if (o) cp_async16(&s.q[t][x], q + token(t) * a.sq.token + x);
             }
-            const int pieces = cols / PIECE;
-            for (int e = tid; e < m * pieces; e += cols) {
+            constexpr int pieces = COLS / PIECE;
+            for (int e = tid; e < m * pieces; e += COLS) {
                 const int t = e / pieces, x = (e - t * pieces) * PIECE;
                 cp_async16(&s.v[t][x], v - tid + token(t) * a.sv.token + x);
             }
         } else {
 #pragma unroll 4
-            for (int e = tid; e < m * K; e += cols) {
+            for (int e = tid; e < m * K; e += COLS) {
                 const int t = e / K, x = e % K;
                 s.k[t][x] = k[token(t) * a.sk.token + x];
                 if (o) s.q[t][x] = q[token(t) * a.sq.token + x];
@@ -208,9 +213,9 @@ template <int K, typename IO> struct Head {
             advance(S, t0, m);
             t0 += m;
             if (!more || t0 >= u.len) break;
-            named_bar(bar, cols);
+            sync();
             m = stage(t0, more, bad);
-            named_bar(bar, cols);
+            sync();
             if (m == 0) break;
         }
         if (t0 < u.len) fill(t0, bad);
@@ -222,16 +227,21 @@ template <int K, typename IO> struct Head {
     }
 };
 
+// One warp, 32 columns of a state.  Warps of their own begin and end as they come, so that one's reads run under
+// another's arithmetic; a CTA of four for a whole state takes 3.9 us instead of 3.3 for one row of 32 heads (1 token),
+// 25.8 instead of 24.7 for 32 rows, 53 instead of 45 for 64.  16-byte copies of the tokens' rows, where they are
+// aligned, against reads of single elements: 3.3 and 3.6 us for that one row, 5.4 and 6.4 us for 37 rows of 8 fp32
+// heads, 64 x 64, 3 tokens.
 // grid (rows, q/k heads, value heads of one * parts of the columns)
-template <int K, typename IO> __global__ void __launch_bounds__(128) k_recurrent(const __grid_constant__ DecodeArgs a, bool rows16) {
+template <int K, typename IO> __global__ void __launch_bounds__(kTile) k_recurrent(const __grid_constant__ DecodeArgs a, bool rows16) {
     constexpr int NR = K / 4;
-    __shared__ Stage<K, IO> s;
-    const int tid = threadIdx.x, cols = blockDim.x;
-    const int n = blockIdx.x, hq = blockIdx.y, h = hq * a.G + blockIdx.z % a.G, col0 = blockIdx.z / a.G * cols;
+    __shared__ Stage<K, kTile, IO> s;
+    const int tid = threadIdx.x;
+    const int n = blockIdx.x, hq = blockIdx.y, h = hq * a.G + blockIdx.z % a.G, col0 = blockIdx.z / a.G * kTile;
     wait_for_previous();
     const Run u = run_of(a, n);
     if (!u.valid) return;
-    const Head<K, IO> head(a, s, u, n, h, hq, col0, tid, cols, 1, rows16);
+    const Head<K, kTile, IO> head(a, s, u, n, h, hq, col0, tid, 0, rows16);
     if (u.slot < 0 || u.slot >= a.n_slots) {
         head.fill(0, u.slot >= 0);
         return;
@@ -244,7 +254,7 @@ template <int K, typename IO> __global__ void __launch_bounds__(128) k_recurrent
     for (int i = 0; i < NR; ++i) S[i] = *reinterpret_cast<const float4 *>(src + (16 * (i >> 2) + (i & 3)) * a.V);
     bool more = true, bad = false;
     const int m = head.stage(0, more, bad);
-    named_bar(1, cols);
+    __syncwarp();
     if (!head.run(S, m, more, bad)) return;
     float *dst = head.out(h) + at;
 #pragma unroll
@@ -253,41 +263,37 @@ template <int K, typename IO> __global__ void __launch_bounds__(128) k_recurrent
 
 // Shared memory of k_recurrent_flow: a ring of slots, each a state and the first tokens of its row (k, q, v as they
 // are), what there is to know of the slots, a stage per group, barriers
-constexpr int kMaxSlots = 8;
+constexpr int kMaxSlots = 8, kGroup = 128;
 struct SlotInfo {
     float a[8], b[8];
     int m, more, bad;
 };
-struct Flow {
-    int groups, slots, state_bytes, slot_bytes, stage_bytes, bytes;
+template <typename IO> struct Flow {
+    static constexpr int K = 128, V = kGroup, groups = 2, state_bytes = K * V * 4;
+    static constexpr int slot_bytes = state_bytes + kTok<IO> * (2 * K + V) * (int)sizeof(IO);
+    static constexpr int stage_bytes = (int)sizeof(Stage<K, V, IO>);
+    static constexpr int rest = 128 + groups * stage_bytes + kMaxSlots * (int)sizeof(SlotInfo) + 256;
+    static constexpr int room = (232448 - rest) / slot_bytes;  // 227 KB
+    static constexpr int slots = room < kMaxSlots ? room : kMaxSlots, bytes = rest + slots * slot_bytes;
 };
-template <int K, typename IO> Flow flow_of(int V) {
-    Flow f;
-    f.groups = 256 / V;
-    f.state_bytes = K * V * 4;
-    f.slot_bytes = f.state_bytes + kTok<IO> * (2 * K + V) * (int)sizeof(IO);
-    f.stage_bytes = (int)sizeof(Stage<K, IO>);
-    const int rest = 128 + f.groups * f.stage_bytes + kMaxSlots * (int)sizeof(SlotInfo) + 256;
-    const int room = (232448 - rest) / f.slot_bytes;  // 227 KB
-    f.slots = room < kMaxSlots ? room : kMaxSlots;
-    f.bytes = rest + f.slots * f.slot_bytes;
-    return f;
-}
 
-// One CTA per SM: groups of V threads take the states of this CTA's heads in turn from the ring into registers, ask
-// at once for what comes next into the slot, run theirs and write it back from the registers.  What a fetch itself
-// depends on (slot, token numbers, gates) is read one round earlier, while the group waits for its state.
-template <int K, typename IO>
-__global__ void __launch_bounds__(256, 1) k_recurrent_flow(const __grid_constant__ DecodeArgs a, const __grid_constant__ Flow f, int heads) {
-    constexpr int NR = K / 4, AHEAD = kTok<IO>;
+// Lists of tokens (128 x 128 states).  There a warp on its own waits for its list, then for the rows that it names, and
+// only then works.  One CTA per SM: two groups of 128 threads take the states of this CTA's heads in turn from the ring
+// into registers, ask at once for what comes next into the slot, run theirs and write it back from the registers.  What
+// a fetch itself depends on (slot, list, gates) is read one round earlier, while the group waits for its state.
+// 96 rows of 64 heads, up to 6 tokens each: 137 us, 5.9 TB/s.
+template <typename IO>
+__global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_constant__ DecodeArgs a, int heads) {
+    using F = Flow<IO>;
+    constexpr int K = F::K, V = F::V, NR = K / 4, AHEAD = kTok<IO>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
-    unsigned char *stages = sm + f.slots * f.slot_bytes;
-    SlotInfo *info = reinterpret_cast<SlotInfo *>(stages + f.groups * f.stage_bytes);
+    unsigned char *stages = sm + F::slots * F::slot_bytes;
+    SlotInfo *info = reinterpret_cast<SlotInfo *>(stages + F::groups * F::stage_bytes);
     unsigned char *bars = reinterpret_cast<unsigned char *>(info + kMaxSlots);
     const uint32_t full = smem_u32(bars);
     volatile int *issued = reinterpret_cast<volatile int *>(bars + 64), *abort_flag = issued + 8;
-    const int group = threadIdx.x / a.V, tid = threadIdx.x - group * a.V, bar = 1 + group, lane = tid & 31;
+    const int group = threadIdx.x / V, tid = threadIdx.x - group * V, bar = 1 + group, lane = tid & 31;
 
     struct Ahead {  // of a head that is to be fetched; lane t has its t-th token
         Run u;
@@ -303,16 +309,13 @@ __global__ void __launch_bounds__(256, 1) k_recurrent_flow(const __grid_constant
         const bool live = x.u.valid && x.u.slot >= 0 && x.u.slot < a.n_slots;
         x.m = live ? min(AHEAD, x.u.len) : 0;
         x.more = 1, x.bad = 0;
-        x.tok = x.u.bos + lane;
-        if (a.token_indices) {
-            const int at = lane < x.m ? a.token_indices[(int64_t)n * a.n_steps + lane] : 0;
-            const uint32_t none = __ballot_sync(~0u, at < 0 || at >= a.T) & ((1u << x.m) - 1u);
-            if (none) {
-                x.m = __ffs(none) - 1;
-                x.more = 0, x.bad = __shfl_sync(~0u, at, x.m) >= 0;
-            }
-            x.tok = at;
+        const int at = lane < x.m ? a.token_indices[(int64_t)n * a.n_steps + lane] : 0;
+        const uint32_t none = __ballot_sync(~0u, at < 0 || at >= a.T) & ((1u << x.m) - 1u);
+        if (none) {
+            x.m = __ffs(none) - 1;
+            x.more = 0, x.bad = __shfl_sync(~0u, at, x.m) >= 0;
         }
+        x.tok = at;
         x.g = x.beta = 0.f;
         if (lane < x.m) {
             x.g = a.g[x.u.b * a.sg.batch + x.h * a.sg.head + x.tok * a.sg.token];
@@ -321,18 +324,18 @@ __global__ void __launch_bounds__(256, 1) k_recurrent_flow(const __grid_constant
         return x;
     };
     auto fetch = [&](int i, const Ahead &x) {  // a whole warp: the i-th head of this CTA into its slot
-        const int slot = i % f.slots, hq = x.h / a.G;
-        const uint32_t at = smem_u32(sm) + slot * f.slot_bytes, bar_f = full + 8 * slot;
+        const int slot = i % F::slots, hq = x.h / a.G;
+        const uint32_t at = smem_u32(sm) + slot * F::slot_bytes, bar_f = full + 8 * slot;
         const bool live = x.u.valid && x.u.slot >= 0 && x.u.slot < a.n_slots;
         if (lane < x.m) info[slot].a[lane] = expf(x.g), info[slot].b[lane] = x.beta;
         __syncwarp();
         if (lane == 0) {
             info[slot].m = x.m, info[slot].more = x.more, info[slot].bad = x.bad;
-            issued[slot] = i / f.slots + 1;
-            const uint32_t row = (uint32_t)((a.o ? 2 : 1) * K + a.V) * (uint32_t)sizeof(IO);
+            issued[slot] = i / F::slots + 1;
+            const uint32_t row = (uint32_t)((a.o ? 2 : 1) * K + V) * (uint32_t)sizeof(IO);
             if (live) {
-                mbar_arrive_expect_tx(bar_f, (uint32_t)f.state_bytes + x.m * row);
-                bulk_load(at, a.state + x.u.slot * a.slot_stride + (int64_t)x.h * K * a.V, (uint32_t)f.state_bytes, bar_f);
+                mbar_arrive_expect_tx(bar_f, (uint32_t)F::state_bytes + x.m * row);
+                bulk_load(at, a.state + x.u.slot * a.slot_stride + (int64_t)x.h * K * V, (uint32_t)F::state_bytes, bar_f);
             } else {
                 mbar_arrive(bar_f);
             }
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(256, 1) k_recurrent_flow(const __grid_constant
         if (lane < x.m) {
             const IO *k = static_cast<const IO *>(a.k) + x.u.b * a.sk.batch + hq * a.sk.head + x.tok * a.sk.token;
             const IO *v = static_cast<const IO *>(a.v) + x.u.b * a.sv.batch + x.h * a.sv.head + x.tok * a.sv.token;
-            const uint32_t kb = K * sizeof(IO), vb = a.V * sizeof(IO), to = at + f.state_bytes;
+            const uint32_t kb = K * sizeof(IO), vb = V * sizeof(IO), to = at + F::state_bytes;
             bulk_load(to + lane * kb, k, kb, bar_f);
             bulk_load(to + 2 * AHEAD * kb + lane * vb, v, vb, bar_f);
             if (a.o) {
@@ -352,54 +355,54 @@ __global__ void __launch_bounds__(256, 1) k_recurrent_flow(const __grid_constant
     };
     if (threadIdx.x < 32) {
         if (lane == 0) {
-            for (int i = 0; i < f.slots; ++i) mbar_init(full + 8 * i, 1), issued[i] = 0;
+            for (int i = 0; i < F::slots; ++i) mbar_init(full + 8 * i, 1), issued[i] = 0;
             *abort_flag = 0;
             fence_mbar_init();
         }
         __syncwarp();
         wait_for_previous();
-        for (int i = 0, item = blockIdx.x; i < f.slots && item < heads; ++i, item += gridDim.x) fetch(i, look(item));
+        for (int i = 0, item = blockIdx.x; i < F::slots && item < heads; ++i, item += gridDim.x) fetch(i, look(item));
     }
     if (threadIdx.x >= 32) wait_for_previous();
     __syncthreads();
-    const int c = tid & 7, r = lane >> 3, at = 4 * r * a.V + (tid & ~31) + 4 * c;
-    Stage<K, IO> &s = *reinterpret_cast<Stage<K, IO> *>(stages + group * f.stage_bytes);
+    const int c = tid & 7, r = lane >> 3, at = 4 * r * V + (tid & ~31) + 4 * c;
+    Stage<K, V, IO> &s = *reinterpret_cast<Stage<K, V, IO> *>(stages + group * F::stage_bytes);
     int i = group;
-    for (int item = blockIdx.x + group * gridDim.x; item < heads; item += f.groups * gridDim.x, i += f.groups) {
-        const int slot = i % f.slots, n = item / a.Hv, h = item - n * a.Hv;
-        const int next = item + f.slots * gridDim.x;
+    for (int item = blockIdx.x + group * gridDim.x; item < heads; item += F::groups * gridDim.x, i += F::groups) {
+        const int slot = i % F::slots, n = item / a.Hv, h = item - n * a.Hv;
+        const int next = item + F::slots * gridDim.x;
         Ahead ahead;
         if (tid < 32 && next < heads) ahead = look(next);
         const Run u = run_of(a, n);
-        const Head<K, IO> head(a, s, u, n, h, h / a.G, 0, tid, a.V, bar, true);
+        const Head<K, V, IO> head(a, s, u, n, h, h / a.G, 0, tid, bar, true);
         const bool live = u.valid && u.slot >= 0 && u.slot < a.n_slots;
-        named_bar(bar, a.V);  // the stage is free
-        const bool ok = mbar_wait_warp(full + 8 * slot, (i / f.slots) & 1, abort_flag);
-        const unsigned char *from = sm + slot * f.slot_bytes;
+        named_bar(bar, V);  // the stage is free
+        const bool ok = mbar_wait_warp(full + 8 * slot, (i / F::slots) & 1, abort_flag);
+        const unsigned char *from = sm + slot * F::slot_bytes;
         const int m = info[slot].m;
         const bool more = info[slot].more, bad = info[slot].bad;
         float4 S[NR];
         const float *src = reinterpret_cast<const float *>(from) + at;
 #pragma unroll
-        for (int j = 0; j < NR; ++j) S[j] = *reinterpret_cast<const float4 *>(src + (16 * (j >> 2) + (j & 3)) * a.V);
-        const uint4 *raw = reinterpret_cast<const uint4 *>(from + f.state_bytes);
+        for (int j = 0; j < NR; ++j) S[j] = *reinterpret_cast<const float4 *>(src + (16 * (j >> 2) + (j & 3)) * V);
+        const uint4 *raw = reinterpret_cast<const uint4 *>(from + F::state_bytes);
         constexpr int ROW = K * (int)sizeof(IO) / 16;
         uint4 *sk = reinterpret_cast<uint4 *>(s.k), *sq = reinterpret_cast<uint4 *>(s.q);
-        for (int e = tid; e < m * ROW; e += a.V) {
+        for (int e = tid; e < m * ROW; e += V) {
             sk[e] = raw[e];
             if (a.o) sq[e] = raw[AHEAD * ROW + e];
         }
         const IO *raw_v = reinterpret_cast<const IO *>(raw + 2 * AHEAD * ROW) + tid;
-        for (int t = 0; t < m; ++t) s.v[t][tid] = raw_v[t * a.V];
+        for (int t = 0; t < m; ++t) s.v[t][tid] = raw_v[t * V];
         if (tid < m) s.a[tid] = info[slot].a[tid], s.b[tid] = info[slot].b[tid];
-        if (!named_bar_and(bar, a.V, ok)) {  // a copy did not arrive in a second: none is left in flight
+        if (!named_bar_and(bar, V, ok)) {  // a copy did not arrive in a second: none is left in flight
             if (tid == 0)
-                for (int j = 0; j < f.slots; ++j)
+                for (int j = 0; j < F::slots; ++j)
                     if (issued[j]) mbar_drain(full + 8 * j, (issued[j] - 1) & 1);
             if (u.valid) head.fill(0, true);
             return;
         }
-        if (tid < 32 && next < heads) fetch(i + f.slots, ahead);
+        if (tid < 32 && next < heads) fetch(i + F::slots, ahead);
         if (!live) {
             if (u.valid) head.fill(0, u.slot >= 0);
             continue;
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(256, 1) k_recurrent_flow(const __grid_constant
         if (!head.run(S, m, more, bad)) continue;
         float *dst = head.out(h) + at;
 #pragma unroll
-        for (int j = 0; j < NR; ++j) *reinterpret_cast<float4 *>(dst + (16 * (j >> 2) + (j & 3)) * a.V) = S[j];
+        for (int j = 0; j < NR; ++j) *reinterpret_cast<float4 *>(dst + (16 * (j >> 2) + (j & 3)) * V) = S[j];
     }
 }
 
@@ -419,16 +422,18 @@ template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
                          (a.o ? reinterpret_cast<uintptr_t>(a.q) : 0);
     const bool rows16 = !((strides * (int64_t)sizeof(IO)) & 15) && !(at & 15);
-    if (heads >= 2 * kSMs && rows16) {  // several states for every SM
-        const Flow f = flow_of<K, IO>(a.V);
-        static std::atomic<uint64_t> done{0};
-        const cudaError_t e = allow_smem(k_recurrent_flow<K, IO>, 232448, done);
-        if (e != cudaSuccess) return e;
-        return launch_behind(k_recurrent_flow<K, IO>, dim3(kSMs), 256, f.bytes, st, a, f, (int)heads);
-    } else {  // a warp per CTA where that spreads the heads over more SMs
-        const int cols = heads * (a.V / kTile) <= 4 * kSMs ? kTile : a.V;
-        return launch_behind(k_recurrent<K, IO>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)(a.G * (a.V / cols))), cols, 0, st, a, rows16);
-    }
+    // The ring pays for lists of tokens from about twelve states per SM on: 53.2 us against 53.6 of single warps at 2048
+    // heads, 136 against 152 at 6144 (6 tokens at most; 2 tokens: 130 against 128), but 32.2 against 30.2 at 1024.
+    // Without lists warps are faster at every size (64 rows of 32 heads, 1 token: 45 against 46 us; 16 rows: 13.4
+    // against 14.2), for narrow heads too (96 rows of 64 heads, 64 x 64, lists: 23 against 35).
+    if constexpr (K == 128)
+        if (a.token_indices && a.V == kGroup && heads >= 12 * kSMs && rows16) {
+            static std::atomic<uint64_t> done{0};
+            const cudaError_t e = allow_smem(k_recurrent_flow<IO>, Flow<IO>::bytes, done);
+            if (e != cudaSuccess) return e;
+            return launch_behind(k_recurrent_flow<IO>, dim3(kSMs), 2 * kGroup, Flow<IO>::bytes, st, a, (int)heads);
+        }
+    return launch_behind(k_recurrent<K, IO>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)(a.G * (a.V / kTile))), kTile, 0, st, a, rows16);
 }
 
 }  // namespace

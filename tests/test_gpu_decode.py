@@ -480,6 +480,38 @@ def test_recurrent_many_heads_with_idle_rows():
         assert torch.equal(state[int(x["idx"][b])].cpu(), before[b])
 
 
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("with_q", [True, False])
+def test_recurrent_token_lists_many_heads(with_q, dtype):
+    """Lists on more heads than the GPU takes at once, some longer than what is fetched ahead, an empty and an idle row
+    and one whose list holds an index that is none."""
+    x = make(30, 12, 16, 64, 128, 128, dtype, seed=29, slots=31)
+    gen = torch.Generator().manual_seed(3)
+    idxs, lists = torch.full((30, 11), -1, dtype=torch.int32), []
+    for b in range(30):
+        n = int(torch.randint(0, 12, (1,), generator=gen))
+        lists.append(torch.randint(0, 12, (n,), generator=gen).tolist())
+        idxs[b, :n] = torch.tensor(lists[b], dtype=torch.int32)
+    lists[4], idxs[4, 0] = [], -1
+    idxs[9, :3], lists[9] = torch.tensor([3, 12, 1], dtype=torch.int32), [3]
+    idx = x["idx"].clone()
+    idx[20], lists[20] = -1, []
+    state, a = x["state"].cuda(), args(x)
+    o = gdn.recurrent_gated_delta_rule(a[0] if with_q else None, *a[1:], state, state_indices=idx.cuda(),
+                                       token_indices=idxs.cuda())
+    h0 = x["state"][x["idx"].long()]
+    ref_o, ref_s = reference(x, h0, lists)
+    ref_s[9] = h0[9]
+    check_state(state[x["idx"].long().cuda()], ref_s)
+    if not with_q:
+        assert o is None
+        return
+    for b, t in enumerate(lists):
+        if t:
+            check_o(o[b, :len(t)], ref_o[b], dtype)
+        assert o[b, len(t):].isnan().all() if b == 9 else (o[b, len(t):] == 0).all()
+
+
 @pytest.mark.parametrize("layout", ["heads outside", "padded rows", "tokens outside", "one shared row", "odd offset"])
 @pytest.mark.parametrize("op", ["tree", "recurrent"])
 def test_layouts(layout, op):
