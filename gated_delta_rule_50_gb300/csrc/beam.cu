@@ -324,25 +324,26 @@ __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
     const uint32_t by_n = (1u << 20) / (uint32_t)n + 1, by_chunks = (1u << 20) / (uint32_t)a.n_chunks + 1;
     wait_for_previous();
     const uint64_t *keys = a.keys + (int64_t)b * total;
-    if (tid < W) s_score[tid] = a.scores[b * W + tid], s_done[tid] = a.finished && a.finished[b * W + tid];
     if (tid == 0) s_count = 0;
     const bool few = total <= kPickKeys * kThreads;
     uint64_t held[kPickKeys];
-    if (few) {
+    if (few) {  // all reads before anything waits for one
 #pragma unroll
         for (int i = 0; i < kPickKeys; ++i) held[i] = tid + i * kThreads < total ? __ldcg(keys + tid + i * kThreads) : 0;
     }
-    __syncthreads();
-    for (int w = tid >> 5; w < W; w += kThreads / 32) {
+    const int mine_w = kThreads - 1 - tid;  // not the warps that begin with the beams' sums
+    const float score = mine_w < W ? a.scores[b * W + mine_w] : 0.f;
+    const uint8_t done = mine_w < W && a.finished ? a.finished[b * W + mine_w] : 0;
+    for (int w = tid >> 5; w < W; w += kThreads / 32) {  // what a finished beam left there is not used
         float m = -INFINITY, s = 0.f;
-        if (!s_done[w])
-            for (int i = lane; i < a.n_chunks; i += 32) {
-                const float2 st = __ldcg(a.stats + (int64_t)(b * W + w) * a.n_chunks + i);
-                join(m, s, st.x, st.y);
-            }
+        for (int i = lane; i < a.n_chunks; i += 32) {
+            const float2 st = __ldcg(a.stats + (int64_t)(b * W + w) * a.n_chunks + i);
+            join(m, s, st.x, st.y);
+        }
         join_warp(m, s);
         if (lane == 0) s_norm[w] = normaliser(m, s);
     }
+    if (mine_w < W) s_score[mine_w] = score, s_done[mine_w] = done != 0;
     __syncthreads();
 
     // key j of a list, as a key of its score and its place in the search
