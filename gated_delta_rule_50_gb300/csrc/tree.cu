@@ -10,8 +10,10 @@
 //
 // One CTA computes a (row, value head), two threads per value column.  Both have the state in registers as in
 // decode.cu and take S^T k_t and S^T q_t of every other node; then one makes the column's corrections d, and both
-// the outputs, with L and P read as broadcast vectors.  Bound by fp32 multiply-adds: 4 T K V of them for the state,
-// T^2 (K + V) for the rest.
+// the outputs, with L and P read as broadcast vectors.  Bound by fp32 multiply-adds (2 T K V of them for the state,
+// T^2 (K + V) for the rest) and the shared-memory reads that feed them: 64 rows of 32 heads, 64 nodes, 128 x 128, take
+// 811 us, 7.9 T multiply-adds a second; 16 rows of 32 heads 34 us with 7 nodes and 96 with 32.  One thread per column
+// and rows staged element by element took 1265 us.
 #include "common.cuh"
 #include "decode.h"
 
@@ -244,9 +246,11 @@ template <int K, int TP> cudaError_t launch(const DecodeArgs &a, cudaStream_t st
     const int64_t steps = a.sq.batch | a.sq.token | a.sq.head | a.sk.batch | a.sk.token | a.sk.head | a.sv.batch | a.sv.token |
                           a.sv.head;
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
-    const bool rows16 = !(steps & 3) && !(at & 15);
+    const bool rows16 = !(steps & 3) && !(at & 15);  // 16 rows of 32 heads, 48 nodes: 142 us, 147 with pieces of 4 bytes
     return launch_behind(k_tree<K, TP>, dim3((unsigned)(a.n_seqs * a.Hv)), 2 * a.V, (size_t)tree_floats<K, TP>(a.T, a.V) * 4, st, a, rows16);
 }
+// The triangles' loops end at the width: 16 rows of 32 heads with 7, 16, 32 and 48 nodes take 34, 54, 96 and 142 us
+// and with 64 as the only width 45, 72, 109 and 148.
 template <int K> cudaError_t launch_nodes(const DecodeArgs &a, cudaStream_t st) {
     if (a.T <= 16) return launch<K, 16>(a, st);
     if (a.T <= 32) return launch<K, 32>(a, st);

@@ -15,8 +15,13 @@
 // q and k are bf16 as given; S, R, L, P and W enter products as hi + lo bf16 pairs (16 bits; one bf16 rounding of
 // them would cost as much as the rounding of o) and are kept in fp32 between them.
 // S arrives by one bulk copy (a head's state is contiguous); its place in shared memory then holds L, P, W and o.
-// Two CTAs stay on each SM (109 KB, 256 TMEM columns each) and take head after head, so that one's copies run under
+// Two CTAs stay on each SM (108 KB, 256 TMEM columns each) and take head after head, so that one's copies run under
 // the other's arithmetic; k, q and the gates of a CTA's next head come while group B finishes W.
+//
+// The states' way from memory is the floor.  64 rows of 64 heads, 64 nodes, 128 x 128, take 104 us where that is 66:
+// a head's steps wait for each other (state, products, inverses, W, products, o), and two heads per SM do not fill
+// the gaps (tensor pipe 18 %, instruction issue 36 %).  Before: CTAs that ended with their head 122 us, W by
+// substitution on CUDA cores behind the state 247.  16 rows of 32 heads, 33 nodes: 15.4 us; one row, 7 nodes: 4.6 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -40,7 +45,9 @@ enum { NB_STATE = 1, NB_B = 2, NB_FREE = 3, NB_A = 4, NB_DIAG = 5, NB_INV = 6, N
 // q, k, v and o as [columns of all heads][token][batch]
 struct RowMaps {
     CUtensorMap q, k, v, o;
-    bool mapped;  // the maps of q, k and v describe them (see rows_map); otherwise their rows are copied in pieces
+    // the maps of q, k and v describe them (see rows_map); otherwise their rows are copied in pieces, by all threads:
+    // 104 us with maps, 122 without for 64 rows of 64 heads, 64 nodes, 4.6 and 5.0 for one row, 7 nodes
+    bool mapped;
     bool rows16;  // pieces of 16 bytes are aligned
 };
 
@@ -622,6 +629,8 @@ template <int K, int V, int TP> cudaError_t launch(const DecodeArgs &a, cudaStre
     return launch_behind(k_tree_tc<K, V, TP>, dim3((unsigned)(heads < 2 * kSMs ? heads : 2 * kSMs)), NT, bytes, st, a, maps, heads);
 }
 
+// Products, tables and W are as wide as the nodes, rounded up to blocks of 16: 16 rows of 32 heads with 16, 32 and 48
+// nodes take 11.3, 13.5 and 15.7 us and with 64 as the only width 16.2, 16.7 and 17.4; one row of 7 nodes 4.6 and 6.6.
 template <int K, int V> cudaError_t launch_nodes(const DecodeArgs &a, cudaStream_t st) {
     if (a.T <= 16) return launch<K, V, 16>(a, st);
     if (a.T <= 32) return launch<K, V, 32>(a, st);

@@ -287,6 +287,9 @@ const char *gdn_version(void);
  *   - a state index of n_slots or more, a token index of T or more, or a
  *     parent that is not an earlier node makes the row's outputs from there on
  *     NaN and leaves its slot as it was.
+ * Hv is at most 16383, n_seqs * Hv at most (2^31 - 1) / 2 and, for
+ * gdn_reorder_states, B at most 65535 (GDN_ERR_UNSUPPORTED otherwise); o and the
+ * states begin on 16-byte boundaries.
  */
 typedef struct {
     int64_t batch, token, head; /* in elements; the innermost dimension is contiguous */
@@ -310,8 +313,8 @@ typedef struct {
  * The recurrence itself, token by token:
  *     S_t = exp(g_t) S_{t-1} + k_t (beta_t (v_t - exp(g_t) S_{t-1}^T k_t))^T,  o_t = scale S_t^T q_t
  * for every row (sequence) over its T tokens, in fp32.  It reads and writes
- * each state once; meant for one to about sixteen tokens (above that gdn_fwd
- * is faster) and right for any number.
+ * each state once; meant for few tokens (gdn_fwd takes them by the chunk) and
+ * right for any number.
  *   state     [n_slots, Hv, K, V] fp32, updated in place at the row's slot.  The
  *             slots of one call must differ from each other.
  *   out_state nullable [n_seqs, Hv, K, V] fp32 contiguous: row n's new state goes
