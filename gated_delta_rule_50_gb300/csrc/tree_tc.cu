@@ -14,8 +14,9 @@
 //
 // q and k are bf16 as given; S, R, L, P and W enter products as hi + lo bf16 pairs (16 bits; one bf16 rounding of
 // them would cost as much as the rounding of o) and are kept in fp32 between them.
-// S arrives by one bulk copy (a head's state is contiguous); its place in shared memory then holds L, P, W and o.
-// Two CTAs stay on each SM (108 KB, 256 TMEM columns each) and take head after head, so that one's copies run under
+// S arrives by one bulk copy (a head's state is contiguous); its place in shared memory then holds L, P, W and o, or,
+// where these have a place of their own, the next head's state.
+// Two CTAs stay on each SM (up to 110 KB, 256 TMEM columns each) and take head after head, so that one's copies run under
 // the other's arithmetic; k, q and the gates of a CTA's next head come while group B finishes W.
 //
 // The states' way from memory is the floor.  64 rows of 64 heads, 64 nodes, 128 x 128, take 104 us where that is 66:
@@ -36,7 +37,6 @@ namespace {
 using namespace tc;
 
 constexpr int GROUP = 128, NT = 2 * GROUP, kSMs = 152;
-constexpr uint32_t kBlock = 16384;  // 128 rows of 64 bf16: one K block of [K; Q]
 constexpr uint32_t kCols = 256;     // TMEM: S^T hi, lo (K columns), later R^T hi, lo and D2 | G, later D1
 constexpr uint32_t kRlo = 32, kD2 = 64, kD1 = 128;
 enum { BAR_S = 0, BAR_G = 8, BAR_D = 16, BAR_O = 24, BAR_K = 32, BAR_V = 40, BARS = 6 };  // state, G, D1, D2, k and q, v
@@ -51,20 +51,27 @@ struct RowMaps {
     bool rows16;  // pieces of 16 bytes are aligned
 };
 
-template <int K, int V, int TP> struct Map {
-    // over the state once it is in TMEM: P in fp32, then row by row W (eight rows of hi, then of lo, in the place of
-    // eight of P), then o; L hi and lo; the blocks of L on the diagonal in fp32, by columns; their inverses; v
-    static constexpr uint32_t PW = 0, LHI = TP * 256, LLO = LHI + TP * 128, DIAG = LLO + TP * 128, DS = 20;
-    static constexpr uint32_t INV = DIAG + TP * DS * 4, INV_BLOCK = 16 * 48;  // hi, then lo; rows of 48 bytes
-    static constexpr uint32_t VAL = INV + TP / 16 * 2 * INV_BLOCK, scratch = VAL + TP * V * 2, state = K * V * 4;
-    static constexpr uint32_t KQ = ((scratch > state ? scratch : state) + 1023) / 1024 * 1024;
+template <int K, int V, int TP, bool APART> struct Map {
+    // [K; Q] in blocks of 64 columns (as the 128 rows of an operand a block goes on into what follows, for rows of the
+    // product that nobody reads), then the state
+    static constexpr uint32_t KQ = 0, KQ_BLOCK = 2 * TP * 128, STATE = K / 64 * KQ_BLOCK, state = K * V * 4;
+    // scratch: P in fp32, then row by row W (eight rows of hi, then of lo, in the place of eight of P), then o; L hi and
+    // lo (halves of the same rows where 32 columns do); the blocks of L on the diagonal in fp32, by columns; their
+    // inverses as hi, then lo, in rows of 48 bytes; v
+    static constexpr uint32_t L_BYTES = TP * (TP <= 32 ? 128 : 256), DS = 20, DIAG_BYTES = TP * DS * 4, INV_BLOCK = 16 * 48;
+    static constexpr uint32_t INV_BYTES = TP / 16 * 2 * INV_BLOCK, scratch = TP * 256 + L_BYTES + DIAG_BYTES + INV_BYTES + TP * V * 2;
     // the products of e^g from node i to node t >= i: rows t and TP - 1 - t share one (see table_row); the stride
     // puts eight neighbouring rows on different banks
-    static constexpr uint32_t TABLE = KQ + K / 64 * kBlock, LS = TP + 4;
-    // (a, parent), the same of the parent, beta, Gam, scale Gam: TP each
-    static constexpr uint32_t VEC = TABLE + TP / 2 * LS * 4;
-    static constexpr uint32_t NEXT = VEC + 7 * TP * 4, BAR = NEXT + 3 * TP * 4;  // gates and parents of the next head
-    static constexpr uint32_t MISC = BAR + 8 * BARS;
+    static constexpr uint32_t LS = TP + 4, TABLE_BYTES = TP / 2 * LS * 4;
+    // (a, parent), the same of the parent, beta, Gam, scale Gam: TP each; gates and parents of the next head
+    static constexpr uint32_t rest = TABLE_BYTES + 10 * TP * 4 + 8 * BARS + 32 + 1024;
+    // APART: the scratch has a place of its own, and the next head's state comes while this one's products run.
+    // Otherwise it lies over the state, once that is in TMEM.
+    static constexpr uint32_t PW = STATE + (APART ? state : 0), LHI = PW + TP * 256, LLO = TP <= 32 ? LHI : LHI + TP * 128;
+    static constexpr int L_LO = TP <= 32 ? 4 : 0;  // first 16-byte piece of lo in its rows
+    static constexpr uint32_t DIAG = LHI + L_BYTES, INV = DIAG + DIAG_BYTES, VAL = INV + INV_BYTES;
+    static constexpr uint32_t END = PW + scratch, TABLE = ((END > STATE + state ? END : STATE + state) + 15) / 16 * 16;
+    static constexpr uint32_t VEC = TABLE + TABLE_BYTES, NEXT = VEC + 7 * TP * 4, BAR = NEXT + 3 * TP * 4, MISC = BAR + 8 * BARS;
     static constexpr uint32_t bytes = MISC + 32 + 1024;
 };
 
@@ -167,9 +174,9 @@ __device__ __forceinline__ void block_product(float (&c)[8], const Frag &a, uint
     for (int i = 0; i < 8; ++i) c[i] += x[i];
 }
 
-template <int K, int V, int TP>
+template <int K, int V, int TP, bool APART>
 __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ DecodeArgs a, const __grid_constant__ RowMaps maps, int heads) {
-    using M = Map<K, V, TP>;
+    using M = Map<K, V, TP, APART>;
     constexpr uint32_t ID_1 = idesc_bf16(128, TP, 0, 0), ID_2 = idesc_bf16(128, 2 * TP, 0, 0);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_align1024(smem_raw);
@@ -210,8 +217,8 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             if (t == 0) {
                 mbar_arrive_expect_tx(bars + BAR_K, 2 * TP * K * 2);
                 for (int kb = 0; kb < K / 64; ++kb) {
-                    load_rows(sb + M::KQ + kb * kBlock, &maps.k, bars + BAR_K, hq * (int)a.sk.head + 64 * kb, n);
-                    load_rows(sb + M::KQ + kb * kBlock + TP * 128, &maps.q, bars + BAR_K, hq * (int)a.sq.head + 64 * kb, n);
+                    load_rows(sb + M::KQ + kb * M::KQ_BLOCK, &maps.k, bars + BAR_K, hq * (int)a.sk.head + 64 * kb, n);
+                    load_rows(sb + M::KQ + kb * M::KQ_BLOCK + TP * 128, &maps.q, bars + BAR_K, hq * (int)a.sq.head + 64 * kb, n);
                 }
             }
         } else if (!group_b) {
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             const int x = t % PIECES, r0 = t / PIECES;
             const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + n * a.sk.batch + hq * a.sk.head + 8 * x;
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + n * a.sq.batch + hq * a.sq.head + 8 * x;
-            const uint32_t dst = sw128_addr(sb + M::KQ + (x >> 3) * kBlock, r0, x & 7);
+            const uint32_t dst = sw128_addr(sb + M::KQ + (x >> 3) * M::KQ_BLOCK, r0, x & 7);
 #pragma unroll 1
             for (int r = 0; r < TP; r += ROWS) {  // a multiple of eight rows at a time
                 copy_piece(dst + r * 128, k + (r0 + r) * a.sk.token, r0 + r < T, maps.rows16);
@@ -228,14 +235,21 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
         }
         return slot;
     };
+    auto load_state = [&](int slot, int h) {  // one thread
+        mbar_arrive_expect_tx(bars + BAR_S, M::state);
+        bulk_load(sb + M::STATE, a.state + slot * a.slot_stride + (int64_t)h * K * V, M::state, bars + BAR_S);
+    };
     int next_slot = look(blockIdx.x);
-    bool ok = true, first = true;
+    bool ok = true, first = true, coming = false, asked = false;  // the next head's state is on its way; by this thread
     uint32_t phase = 0, phase_k = 0;  // of the mbarriers: each is used once per head, that of k and q for idle ones too
     for (int head = blockIdx.x; head < heads; head += gridDim.x) {
         const int n = head / a.Hv, h = head - n * a.Hv;
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)n * T * a.Hv + h) * V;
         const int slot = next_slot;
-        const bool more = head + gridDim.x < heads;
+        const bool more = head + gridDim.x < heads, here = coming;
+        int ahead = -1;  // the slot whose state is asked for before this head is done
+        if (APART && more) ahead = a.state_indices ? a.state_indices[(head + gridDim.x) / a.Hv] : (head + gridDim.x) / a.Hv;
+        coming = asked = false;
         if (slot < 0 || slot >= a.n_slots || !ok) {  // an idle row, no such slot, or a wait that ran out before
             if (t < V)
                 for (int i = 0; i < T; ++i) o[i * o_tok + t] = __float2bfloat16_rn(slot < 0 ? 0.f : nan);
@@ -246,9 +260,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             continue;
         }
         if (t == 32 * SETUP) {
-            const uint32_t bytes = (uint32_t)(K * V * 4);
-            mbar_arrive_expect_tx(bars + BAR_S, bytes);
-            bulk_load(sb, a.state + slot * a.slot_stride + (int64_t)h * K * V, bytes, bars + BAR_S);
+            if (!here) load_state(slot, h);
             for (int i = 2; i < 6; ++i) misc[i] = 0;
         }
         if (warp == SETUP && first) {
@@ -273,7 +285,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                 if (maps.mapped) ok = mbar_wait_warp(bars + BAR_K, phase_k, abort_flag);
                 if (t == 32 * SETUP) {
                     for (int kb = 0; kb < K / 64; ++kb)
-                        mma_chain<4, 2, 2>(tmem + kD1, kdesc(sb + M::KQ + kb * kBlock), kdesc(sb + M::KQ + kb * kBlock), ID_1, kb);
+                        mma_chain<4, 2, 2>(tmem + kD1, kdesc(sb + M::KQ + kb * M::KQ_BLOCK), kdesc(sb + M::KQ + kb * M::KQ_BLOCK), ID_1, kb);
                     mma_commit(bars + BAR_G);
                 }
                 __syncwarp();
@@ -367,7 +379,13 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             bar_arrive(NB_DIAG, GROUP + INVERTERS);  // group A makes the inverses of the blocks on the diagonal
             if (has_row && !is_p)
 #pragma unroll
-                for (int c = 0; c < TP / 8; ++c) st_split_chunk(sb + M::LHI, sb + M::LLO, node, c, x + 8 * c);
+                for (int c = 0; c < TP / 8; ++c) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) split_pair(x[8 * c + 2 * i], x[8 * c + 2 * i + 1], hi[i], lo[i]);
+                    st_shared_v4(sw128_addr(sb + M::LHI, node, c), hi[0], hi[1], hi[2], hi[3]);
+                    st_shared_v4(sw128_addr(sb + M::LLO, node, c + M::L_LO), lo[0], lo[1], lo[2], lo[3]);
+                }
             named_bar(NB_INV, GROUP + INVERTERS);
             const int w = warp - 4, lane = t & 31;
             if (16 * w < TP) {  // rows 16 w .. 16 w + 15 of W: blocks beyond the w-th are 0
@@ -412,7 +430,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
 #pragma unroll
                         for (int e = 0; e < b; ++e)
                             block_product(c[e], f, sw128_addr(sb + M::LHI, 16 * b + br, 2 * e + bh),
-                                          sw128_addr(sb + M::LLO, 16 * b + br, 2 * e + bh));
+                                          sw128_addr(sb + M::LLO, 16 * b + br, M::L_LO + 2 * e + bh));
                     }
                 }
                 fence_proxy_async_smem();
@@ -420,7 +438,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
         } else {
             ok = mbar_wait_warp(bars + BAR_S, phase, abort_flag);
             if (column) {
-                const float *s = reinterpret_cast<const float *>(sm) + t;
+                const float *s = reinterpret_cast<const float *>(sm + M::STATE) + t;
 #pragma unroll 1
                 for (int c = 0; c < K / 32; ++c) {
                     float y[32];
@@ -445,9 +463,11 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                     }
                     for (int part = 0; part < 2; ++part)
                         for (int kb = 0; kb < K / 64; ++kb)
-                            mma_chain_ta<4, 2>(tmem + kD1, tmem + part * (K / 2) + 32 * kb, kdesc(sb + M::KQ + kb * kBlock), ID_2,
+                            mma_chain_ta<4, 2>(tmem + kD1, tmem + part * (K / 2) + 32 * kb, kdesc(sb + M::KQ + kb * M::KQ_BLOCK), ID_2,
                                                part + kb);
                     mma_commit(bars + BAR_D);
+                    asked = ahead >= 0 && ahead < a.n_slots && ok;  // this warp has seen the state arrive, all have taken it
+                    if (asked) load_state(ahead, (head + gridDim.x) % a.Hv);
                 }
                 __syncwarp();
             } else if (t < 32 + INVERTERS) {
@@ -516,6 +536,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                 }
         }
         if (more) next_slot = look(head + gridDim.x);  // the products have read k and q
+        coming = ahead >= 0 && ahead < a.n_slots;
         tc_fence_before();
         ok = __syncthreads_and(ok) != 0;
         tc_fence_after();
@@ -531,7 +552,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
             ok = mbar_wait_warp(bars + BAR_O, phase, abort_flag);
             tc_fence_after();
             // o by way of shared memory (the place of W, whose products are done), all rows in one copy
-            __nv_bfloat16 *s_o = reinterpret_cast<__nv_bfloat16 *>(sm);
+            __nv_bfloat16 *s_o = reinterpret_cast<__nv_bfloat16 *>(sm + M::PW);
             if (column)
 #pragma unroll 1
                 for (int c = t / GROUP; 16 * c < T; c += 2) {
@@ -556,7 +577,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                 named_bar(NB_OUT, NT);
             }
             if (t == 0) {  // rows past the last node are not written
-                store_rows(&maps.o, sb, h * V, n);
+                store_rows(&maps.o, sb + M::PW, h * V, n);
                 bulk_commit();
                 bulk_wait_read_all();
             }
@@ -566,6 +587,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
         ok = __syncthreads_and(ok) != 0;
         if (!ok) {  // a wait ran out (its limit is a second): no copy of a state is left in flight, and the rows show it
             if (t == 0) mbar_drain(bars + BAR_S, phase);
+            if (asked) mbar_drain(bars + BAR_S, phase ^ 1);
             if (t < V)
                 for (int i = 0; i < T; ++i) o[i * o_tok + t] = __float2bfloat16_rn(nan);
         }
@@ -609,11 +631,11 @@ bool rows_map(CUtensorMap *m, const void *p, int width, int heads, int T, int B,
               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int K, int V, int TP> cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
-    constexpr int bytes = (int)Map<K, V, TP>::bytes;
+template <int K, int V, int TP, bool APART = false> cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
+    constexpr int bytes = (int)Map<K, V, TP, APART>::bytes;
     static_assert(2 * (bytes + 1024) <= 233472, "two CTAs per SM");
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(k_tree_tc<K, V, TP>, bytes, done);
+    const cudaError_t e = allow_smem(k_tree_tc<K, V, TP, APART>, bytes, done);
     if (e != cudaSuccess) return e;
     RowMaps maps;
     const gdn_strides so = {(int64_t)a.T * a.Hv * V, (int64_t)a.Hv * V, V};
@@ -626,12 +648,18 @@ template <int K, int V, int TP> cudaError_t launch(const DecodeArgs &a, cudaStre
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
     maps.rows16 = !(steps & 7) && !(at & 15);
     const int heads = a.n_seqs * a.Hv;
-    return launch_behind(k_tree_tc<K, V, TP>, dim3((unsigned)(heads < 2 * kSMs ? heads : 2 * kSMs)), NT, bytes, st, a, maps, heads);
+    return launch_behind(k_tree_tc<K, V, TP, APART>, dim3((unsigned)(heads < 2 * kSMs ? heads : 2 * kSMs)), NT, bytes, st, a, maps, heads);
 }
 
 // Products, tables and W are as wide as the nodes, rounded up to blocks of 16: 16 rows of 32 heads with 16, 32 and 48
 // nodes take 11.3, 13.5 and 15.7 us and with 64 as the only width 16.2, 16.7 and 17.4; one row of 7 nodes 4.6 and 6.6.
 template <int K, int V> cudaError_t launch_nodes(const DecodeArgs &a, cudaStream_t st) {
+    // The scratch apart from the state, and the state asked for ahead, from more than two turns of the CTAs on: 64 rows
+    // of 64 heads with 16 nodes 60.7 us against 72.5, with 32 74.1 against 82.4; 768 heads with 7 nodes 15.8 and 16.0,
+    // but 512 11.5 and 10.9.  Narrower states lose by it at every size (64 x 64, 64 rows of 64 heads, 32 nodes: 65.8
+    // and 61.3 us), and with more nodes two CTAs do not fit on an SM.
+    if constexpr (K == 128 && V == 128)
+        if (a.T <= 32 && (int64_t)a.n_seqs * a.Hv >= 4 * kSMs) return a.T <= 16 ? launch<K, V, 16, true>(a, st) : launch<K, V, 32, true>(a, st);
     if (a.T <= 16) return launch<K, V, 16>(a, st);
     if (a.T <= 32) return launch<K, V, 32>(a, st);
     if (a.T <= 48) return launch<K, V, 48>(a, st);

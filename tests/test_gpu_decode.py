@@ -454,6 +454,11 @@ def test_tree_many_heads_with_idle_rows(T):
     assert o[live].isfinite().all() and (o[live].float().abs().amax(dim=(1, 3)) > 0).all()
 
 
+def test_tree_many_heads_ahead():
+    """The widest trees whose next state is asked for while a head's products run."""
+    test_tree_many_heads_with_idle_rows(32)
+
+
 def test_recurrent_many_heads_with_idle_rows():
     x = make(50, 3, 8, 32, 128, 128, bf16, seed=27)
     idx = x["idx"].clone()
