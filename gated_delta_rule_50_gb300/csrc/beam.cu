@@ -15,9 +15,10 @@
 // factor of 2^kSlack, so that the sums are hardly ever rescaled.
 //
 // The logits' way through memory is the floor, two bytes or four each.  64 searches of 8 beams over 131072 bf16
-// logits (a seventh of them finished, 114 MB) take 30 us: about 18 of streaming at 6.4 TB/s, the rest the first
+// logits (a seventh of them finished, 114 MB) take 30 us: about 18 of streaming, the rest the first
 // reads, the selection at the end of every CTA (all come to it together) and the joining kernel.  One search of 4
 // beams over 32000 takes 8.5 us, 8 of 5 over 50021 masked fp32 logits 14.5: two kernels of dependent steps.
+// Asking for a row's next 16 to 128 KB ahead in L2 made none of them faster.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -214,8 +215,11 @@ template <typename IO, bool MASK> struct Row {
     }
 };
 
-template <typename IO, bool MASK> __global__ void __launch_bounds__(kThreads, 6) k_beam_scan(const BeamArgs a) {
-    constexpr int N = Pack<IO>::N, STEP = kThreads * N;
+// Eight CTAs per SM with three vectors on the way per thread, or six with four where a mask takes registers too: 512
+// rows of 131072 bf16 logits in two chunks each take 31.7 us, in six CTAs per SM 37.7, because 1024 do not fit at once
+// (30.3 and 29.5 where a seventh of the rows is finished); masked with eight 16.4 instead of 14.4 for 40 rows of 50021.
+template <typename IO, bool MASK> __global__ void __launch_bounds__(kThreads, MASK ? 6 : 8) k_beam_scan(const BeamArgs a) {
+    constexpr int N = Pack<IO>::N, STEP = kThreads * N, DEEP = MASK ? 4 : 3;
     extern __shared__ uint64_t s_got[];  // n times the elements per thread
     __shared__ Nth sh;
     __shared__ float2 s_stat[kThreads / 32];
@@ -259,13 +263,14 @@ template <typename IO, bool MASK> __global__ void __launch_bounds__(kThreads, 6)
     int at = begin;
     if (at < 0) take(x.edge(at), at), at += STEP;
     const int whole = min(end, a.vocab - N + 1);
-    for (; at + 3 * STEP < whole; at += 4 * STEP) {
-        uint4 u[4];
+    for (; at + (DEEP - 1) * STEP < whole; at += DEEP * STEP) {
+        uint4 u[DEEP];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = x.inside(at + j * STEP);
+        for (int j = 0; j < DEEP; ++j) u[j] = x.inside(at + j * STEP);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) take(u[j], at + j * STEP);
+        for (int j = 0; j < DEEP; ++j) take(u[j], at + j * STEP);
     }
+#pragma unroll 1  // its code, unrolled, costs one search of 4 beams 0.7 us
     for (; at < whole; at += STEP) take(x.inside(at), at);
     if (at < end) take(x.edge(at), at);
     float s, s_odd, ms = best == -INFINITY ? -INFINITY : m;
@@ -449,9 +454,8 @@ template <typename IO> cudaError_t launch(const BeamArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Elements of a row that one CTA takes: enough CTAs for six on every SM where the rows allow it (as many as fit; 64
-// searches of 8 beams over 131072 take 31 us with four or six wanted, 35 with eight and 34 to 41 with more: each CTA
-// selects), a vector per thread at least, and no more than the keys in shared memory allow.  Equal chunks: up to seven
+// Elements of a row that one CTA takes: enough CTAs for six on every SM where the rows allow it (64 searches of 8
+// beams over 131072 take 31 us with four or six wanted, 35 with eight and 34 to 41 with more: each CTA selects), a vector per thread at least, and no more than the keys in shared memory allow.  Equal chunks: up to seven
 // elements are added for a row that begins inside a vector.
 int beam_chunk(int64_t rows, int64_t vocab, int64_t n, gdn_dtype io) {
     const int64_t wanted = 152 * 6, least = kThreads * (io == GDN_BF16 ? 8 : 4), per = kMaxGot / n < 512 ? kMaxGot / n : 512;
