@@ -278,10 +278,19 @@ template <typename IO> struct Flow {
 };
 
 // Lists of tokens (128 x 128 states).  There a warp on its own waits for its list, then for the rows that it names, and
-// only then works.  One CTA per SM: two groups of 128 threads take the states of this CTA's heads in turn from the ring
-// into registers, ask at once for what comes next into the slot, run theirs and write it back from the registers.  What
-// a fetch itself depends on (slot, list, gates) is read one round earlier, while the group waits for its state.
-// 96 rows of 64 heads, up to 6 tokens each: 137 us, 5.9 TB/s.
+// only then works.  One CTA per SM: two groups of 128 threads take this CTA's heads in order, whichever is free, each
+// from the ring into registers, ask at once for what comes next into the slot, run theirs and write it back from the
+// registers.  What a fetch itself depends on (slot, list, gates) is read while the group waits for its state.
+//
+// A slot's turns: its i-th use is asked for (`armed` ends its i-th phase, after `full` has been armed for its own), then
+// arrives (`full` ends its i-th phase), then is taken and asked for again.  A phase is waited for by its parity, which
+// says nothing while an earlier phase of the same slot is open: hence `armed` first, which the group that took the
+// slot's previous use may be late with, since that can be the other group.  Late by a copy, not by a list: between
+// taking a head and asking for the next one into its slot a group waits for nothing else, so that the limits of the
+// waits hold whatever the lengths of the lists.  The parity of `armed` always tells: the slot's use before this one was
+// taken by this group, which waited for its `armed`, or by the other one, which took it after asking for it or waits
+// for a head that this group asked for.
+// 96 rows of 64 heads, up to 6 tokens each: 134 us, 6.0 TB/s.
 template <typename IO>
 __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_constant__ DecodeArgs a, int heads) {
     using F = Flow<IO>;
@@ -291,8 +300,10 @@ __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_c
     unsigned char *stages = sm + F::slots * F::slot_bytes;
     SlotInfo *info = reinterpret_cast<SlotInfo *>(stages + F::groups * F::stage_bytes);
     unsigned char *bars = reinterpret_cast<unsigned char *>(info + kMaxSlots);
-    const uint32_t full = smem_u32(bars);
-    volatile int *issued = reinterpret_cast<volatile int *>(bars + 64), *abort_flag = issued + 8;
+    static_assert(F::groups == 2 && 8 * kMaxSlots <= 64, "see above; the places of the barriers");
+    const uint32_t full = smem_u32(bars), armed = full + 64;
+    volatile int *issued = reinterpret_cast<volatile int *>(bars + 128), *abort_flag = issued + kMaxSlots;
+    int *counter = reinterpret_cast<int *>(bars + 128) + kMaxSlots + 1, *taken = counter + 1;  // taken: one per group
     const int group = threadIdx.x / V, tid = threadIdx.x - group * V, bar = 1 + group, lane = tid & 31;
 
     struct Ahead {  // of a head that is to be fetched; lane t has its t-th token
@@ -339,6 +350,7 @@ __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_c
             } else {
                 mbar_arrive(bar_f);
             }
+            mbar_arrive(armed + 8 * slot);
         }
         __syncwarp();
         if (lane < x.m) {
@@ -355,8 +367,8 @@ __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_c
     };
     if (threadIdx.x < 32) {
         if (lane == 0) {
-            for (int i = 0; i < F::slots; ++i) mbar_init(full + 8 * i, 1), issued[i] = 0;
-            *abort_flag = 0;
+            for (int i = 0; i < F::slots; ++i) mbar_init(full + 8 * i, 1), mbar_init(armed + 8 * i, 1), issued[i] = 0;
+            *abort_flag = 0, *counter = 0;
             fence_mbar_init();
         }
         __syncwarp();
@@ -367,51 +379,64 @@ __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_c
     __syncthreads();
     const int c = tid & 7, r = lane >> 3, at = 4 * r * V + (tid & ~31) + 4 * c;
     Stage<K, V, IO> &s = *reinterpret_cast<Stage<K, V, IO> *>(stages + group * F::stage_bytes);
-    int i = group;
-    for (int item = blockIdx.x + group * gridDim.x; item < heads; item += F::groups * gridDim.x, i += F::groups) {
+    bool alive = true;  // no wait of this group has run out
+    for (;;) {
+        if (tid == 0) taken[group] = atomicAdd(counter, 1);
+        named_bar(bar, V);  // the stage is free too
+        const int i = taken[group], item = blockIdx.x + i * (int)gridDim.x;
+        if (item >= heads) break;
         const int slot = i % F::slots, n = item / a.Hv, h = item - n * a.Hv;
         const int next = item + F::slots * gridDim.x;
-        Ahead ahead;
-        if (tid < 32 && next < heads) ahead = look(next);
         const Run u = run_of(a, n);
         const Head<K, V, IO> head(a, s, u, n, h, h / a.G, 0, tid, bar, true);
         const bool live = u.valid && u.slot >= 0 && u.slot < a.n_slots;
-        named_bar(bar, V);  // the stage is free
-        const bool ok = mbar_wait_warp(full + 8 * slot, (i / F::slots) & 1, abort_flag);
-        const unsigned char *from = sm + slot * F::slot_bytes;
-        const int m = info[slot].m;
-        const bool more = info[slot].more, bad = info[slot].bad;
+        int m = 0;
+        bool more = false, bad = false;
         float4 S[NR];
-        const float *src = reinterpret_cast<const float *>(from) + at;
+        if (alive) {
+            Ahead ahead;
+            if (tid < 32 && next < heads) ahead = look(next);
+            const uint32_t parity = (i / F::slots) & 1;
+            const bool ok = mbar_wait_warp(armed + 8 * slot, parity, abort_flag) && mbar_wait_warp(full + 8 * slot, parity, abort_flag);
+            const unsigned char *from = sm + slot * F::slot_bytes;
+            m = ok ? info[slot].m : 0;
+            more = info[slot].more, bad = info[slot].bad;
+            const float *src = reinterpret_cast<const float *>(from) + at;
 #pragma unroll
-        for (int j = 0; j < NR; ++j) S[j] = *reinterpret_cast<const float4 *>(src + (16 * (j >> 2) + (j & 3)) * V);
-        const uint4 *raw = reinterpret_cast<const uint4 *>(from + F::state_bytes);
-        constexpr int ROW = K * (int)sizeof(IO) / 16;
-        uint4 *sk = reinterpret_cast<uint4 *>(s.k), *sq = reinterpret_cast<uint4 *>(s.q);
-        for (int e = tid; e < m * ROW; e += V) {
-            sk[e] = raw[e];
-            if (a.o) sq[e] = raw[AHEAD * ROW + e];
+            for (int j = 0; j < NR; ++j) S[j] = *reinterpret_cast<const float4 *>(src + (16 * (j >> 2) + (j & 3)) * V);
+            const uint4 *raw = reinterpret_cast<const uint4 *>(from + F::state_bytes);
+            constexpr int ROW = K * (int)sizeof(IO) / 16;
+            uint4 *sk = reinterpret_cast<uint4 *>(s.k), *sq = reinterpret_cast<uint4 *>(s.q);
+            for (int e = tid; e < m * ROW; e += V) {
+                sk[e] = raw[e];
+                if (a.o) sq[e] = raw[AHEAD * ROW + e];
+            }
+            const IO *raw_v = reinterpret_cast<const IO *>(raw + 2 * AHEAD * ROW) + tid;
+            for (int t = 0; t < m; ++t) s.v[t][tid] = raw_v[t * V];
+            if (tid < m) s.a[tid] = info[slot].a[tid], s.b[tid] = info[slot].b[tid];
+            alive = named_bar_and(bar, V, ok);
+            if (alive && tid < 32 && next < heads) fetch(i + F::slots, ahead);
         }
-        const IO *raw_v = reinterpret_cast<const IO *>(raw + 2 * AHEAD * ROW) + tid;
-        for (int t = 0; t < m; ++t) s.v[t][tid] = raw_v[t * V];
-        if (tid < m) s.a[tid] = info[slot].a[tid], s.b[tid] = info[slot].b[tid];
-        if (!named_bar_and(bar, V, ok)) {  // a copy did not arrive in a second: none is left in flight
-            if (tid == 0)
-                for (int j = 0; j < F::slots; ++j)
-                    if (issued[j]) mbar_drain(full + 8 * j, (issued[j] - 1) & 1);
-            if (u.valid) head.fill(0, true);
-            return;
-        }
-        if (tid < 32 && next < heads) fetch(i + F::slots, ahead);
         if (!live) {
             if (u.valid) head.fill(0, u.slot >= 0);
             continue;
         }
-        if (!head.run(S, m, more, bad)) continue;
+        if (!alive) {  // a copy did not arrive in a second: this head and all that follow show it
+            head.fill(0, true);
+            const float nan = __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int j = 0; j < NR; ++j) S[j] = make_float4(nan, nan, nan, nan);
+        } else if (!head.run(S, m, more, bad)) {
+            continue;
+        }
         float *dst = head.out(h) + at;
 #pragma unroll
         for (int j = 0; j < NR; ++j) *reinterpret_cast<float4 *>(dst + (16 * (j >> 2) + (j & 3)) * V) = S[j];
     }
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag)  // no copy is left in flight
+        for (int j = 0; j < F::slots; ++j)
+            if (issued[j]) mbar_drain(full + 8 * j, (issued[j] - 1) & 1);
 }
 
 template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {

@@ -287,6 +287,8 @@ const char *gdn_version(void);
  *   - a state index of n_slots or more, a token index of T or more, or a
  *     parent that is not an earlier node makes the row's outputs from there on
  *     NaN and leaves its slot as it was.
+ * The kernels' waits for their own copies are bounded (a second).  Where one ran
+ * out, the rows that it concerns have NaN for outputs and for new states.
  * Hv is at most 16383, n_seqs * Hv at most (2^31 - 1) / 2 and, for
  * gdn_reorder_states, B at most 65535 (GDN_ERR_UNSUPPORTED otherwise); o and the
  * states begin on 16-byte boundaries.
