@@ -10,14 +10,16 @@
 // scores and selects in the same way.
 // No result depends on the order in which threads arrive: places of collected keys do, their ranks do not.
 //
-// The sum is one of 2^(c x - m) with c = log2 e in fp32: one multiply-add and one exp2 per logit, and the same c
-// and m turn the sum back (in pairs of fp32, once per beam).  m follows the maximum only where that has grown by a
-// factor of 2^kSlack, so that the sums are hardly ever rescaled.
+// The sum is one of 2^(c (x - m)) with c = log2 e: a subtraction, a product and an exp2 per logit.  m is itself one of the
+// logits, so that x - m is exact near 0 whatever the logits' size (c x - c m in one multiply-add is not: past 3e9, as
+// where forbidden tokens hold -1e30, the rounding of c m alone is hundreds).  m follows the maximum only where that has
+// grown by kSlack, so that the sums are hardly ever rescaled.  The normaliser is kept as a pair, its rounding beside it:
+// where it is large, that is more than the scores' differences.
 //
 // The logits' way through memory is the floor, two bytes or four each.  64 searches of 8 beams over 131072 bf16
-// logits (a seventh of them finished, 114 MB) take 30 us: about 18 of streaming, the rest the first
+// logits (a seventh of them finished, 114 MB) take 31 us: about 18 of streaming, the rest the first
 // reads, the selection at the end of every CTA (all come to it together) and the joining kernel.  One search of 4
-// beams over 32000 takes 8.5 us, 8 of 5 over 50021 masked fp32 logits 14.5: two kernels of dependent steps.
+// beams over 32000 takes 8.5 us, 8 of 5 over 50021 masked fp32 logits 14.6: two kernels of dependent steps.
 // Asking for a row's next 16 to 128 KB ahead in L2 made none of them faster.
 #include <cuda_bf16.h>
 
@@ -31,7 +33,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxGot = 8192;  // n times the elements per thread, at most: keys in shared memory
 constexpr int kPickKeys = 8;   // keys per thread that k_beam_pick holds in registers
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 40.f;
+constexpr float kSlack = 28.f;
 
 __device__ __forceinline__ uint32_t ordered(float x) {  // larger for larger x; +0 and -0 alike
     const uint32_t u = __float_as_uint(x + 0.f);
@@ -52,33 +54,35 @@ __device__ __forceinline__ float exp2_of(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// A sum of 2^(c x - m) and its m; an empty one is (-inf, 0).  A logit of NaN or +inf leaves s = NaN.
+// A sum of 2^(c (x - m)) and its m; an empty one is (-inf, 0).  A logit of NaN or +inf leaves s = NaN.
 __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
     const float top = fmaxf(m, m2);
-    s = (m == -INFINITY ? s : s * exp2f(m - top)) + (m2 == -INFINITY ? s2 : s2 * exp2f(m2 - top));
+    s = (m == -INFINITY ? s : s * exp2f(kLog2e * (m - top))) + (m2 == -INFINITY ? s2 : s2 * exp2f(kLog2e * (m2 - top)));
     m = top;
 }
 __device__ __forceinline__ void join_warp(float &m, float &s) {
     float top = m;
 #pragma unroll
     for (int step = 16; step; step >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, step));
-    if (m != -INFINITY) s *= exp2f(m - top);
+    if (m != -INFINITY) s *= exp2f(kLog2e * (m - top));
 #pragma unroll
     for (int step = 16; step; step >>= 1) s += __shfl_xor_sync(~0u, s, step);
     m = top;
 }
 
-// The logarithm of the sum, (m + log2 s) / c: the exponent of s apart and the rest carried along, so that the
-// rounding is that of the result.
-__device__ __forceinline__ float normaliser(float m, float s) {
-    if (!(s > 0.f)) return s == 0.f ? -INFINITY : s;
-    const float e = (float)((int)(__float_as_uint(s) >> 23) - 127);  // s is at least 1, up to rounding, and no infinity
+// The logarithm of the sum, m + ln s, as a rounded value and what the rounding left.  ln s = (e + f) ln 2 with the
+// exponent e of s apart, so that log2f sees a number near 1.
+__device__ __forceinline__ float2 normaliser(float m, float s) {
+    if (!(s > 0.f)) return make_float2(s == 0.f ? -INFINITY : s, 0.f);
+    // s is at least 1, up to rounding, and at most 2^61: the elements of a row times 2^(c kSlack)
+    const float e = (float)((int)(__float_as_uint(s) >> 23) - 127);
     const float f = log2f(__uint_as_float((__float_as_uint(s) & 0x007FFFFFu) | 0x3F800000u));
-    const float a = m + e, v = a - m, rest = (m - (a - v)) + (e - v) + f;  // a + rest = m + log2 s
-    constexpr double inv = 1.0 / (double)kLog2e;
-    constexpr float hi = (float)inv, lo = (float)(inv - (double)hi);
-    const float p = a * hi;
-    return p + (fmaf(a, hi, -p) + fmaf(a, lo, rest * hi));
+    constexpr double ln2 = 0.69314718055994530942;
+    constexpr float hi = (float)ln2, lo = (float)(ln2 - (double)hi);
+    const float p = e * hi, rest = fmaf(e, hi, -p) + fmaf(e, lo, f * hi);  // p + rest = ln s
+    const float a = m + p, v = a - m, r = (m - (a - v)) + (p - v) + rest;  // a + r = m + ln s
+    const float sum = a + r;
+    return make_float2(sum, r - (sum - a));
 }
 
 struct Nth {  // shared memory of nth_largest
@@ -125,14 +129,14 @@ __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
 __device__ __forceinline__ void halves(uint64_t p, float &lo, float &hi) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 
@@ -216,8 +220,8 @@ template <typename IO, bool MASK> struct Row {
 };
 
 // Eight CTAs per SM with three vectors on the way per thread, or six with four where a mask takes registers too: 512
-// rows of 131072 bf16 logits in two chunks each take 31.7 us, in six CTAs per SM 37.7, because 1024 do not fit at once
-// (30.3 and 29.5 where a seventh of the rows is finished); masked with eight 16.4 instead of 14.4 for 40 rows of 50021.
+// rows of 131072 bf16 logits in two chunks each take 32 us (31.7 before x - m was formed first), in six CTAs per SM
+// 37.7, because 1024 do not fit at once; masked with eight 16.4 instead of 14.4 for 40 rows of 50021.
 template <typename IO, bool MASK> __global__ void __launch_bounds__(kThreads, MASK ? 6 : 8) k_beam_scan(const BeamArgs a) {
     constexpr int N = Pack<IO>::N, STEP = kThreads * N, DEEP = MASK ? 4 : 3;
     extern __shared__ uint64_t s_got[];  // n times the elements per thread
@@ -238,24 +242,24 @@ template <typename IO, bool MASK> __global__ void __launch_bounds__(kThreads, MA
     const int first = chunk * a.chunk - shift, begin = first + tid * N;
     const int end = min(first + a.chunk, a.vocab);
 
-    float best = -INFINITY, m = 0.f;  // m: at most c * best, 0 before there is one
+    float best = -INFINITY, m = 0.f;  // m: at most best, 0 before there is one
     uint64_t sum = 0, neg_m = 0;      // pairs: the even and the odd elements' sums; -m twice
     const uint64_t c2 = pair_of(kLog2e, kLog2e);
     int best_at = begin;
     auto take = [&](const uint4 &u, int at) {
         const float top = Pack<IO>::max(u);
         if (top > best) {
-            if (best == -INFINITY || fmaf(top, kLog2e, -m) > kSlack) {
-                const float f = best == -INFINITY ? 1.f : exp2_of(fmaf(top, -kLog2e, m));
-                sum = fma2(sum, pair_of(f, f), 0);
-                m = kLog2e * top, neg_m = pair_of(-m, -m);
+            if (best == -INFINITY || top - m > kSlack) {
+                const float f = best == -INFINITY ? 1.f : exp2_of(kLog2e * (m - top));
+                sum = mul2(sum, pair_of(f, f));
+                m = top, neg_m = pair_of(-m, -m);
             }
             best = top, best_at = at;
         }
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
             float e0, e1;
-            halves(fma2(pair_of(Pack<IO>::get(u, i), Pack<IO>::get(u, i + 1)), c2, neg_m), e0, e1);
+            halves(mul2(add2(pair_of(Pack<IO>::get(u, i), Pack<IO>::get(u, i + 1)), neg_m), c2), e0, e1);
             sum = add2(sum, pair_of(exp2_of(e0), exp2_of(e1)));
         }
     };
@@ -325,7 +329,8 @@ template <typename IO, bool MASK> __global__ void __launch_bounds__(kThreads, MA
 __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
     extern __shared__ uint64_t s_got[];
     __shared__ Nth sh;
-    __shared__ float s_norm[GDN_BEAM_MAX], s_score[GDN_BEAM_MAX];
+    __shared__ float2 s_norm[GDN_BEAM_MAX];
+    __shared__ float s_score[GDN_BEAM_MAX];
     __shared__ uint8_t s_done[GDN_BEAM_MAX];
     __shared__ int s_count;
     const int tid = threadIdx.x, lane = tid & 31, n = a.n, W = a.W, b = blockIdx.x;
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(kThreads) k_beam_pick(const BeamArgs a) {
     auto entry = [&](int w, int list, int j, uint64_t key) -> uint64_t {
         if (s_done[w]) return j == 0 && list == w * a.n_chunks ? make_key(s_score[w], (uint32_t)w * a.vocab) : 0;
         if (!key) return 0;
-        return make_key(s_score[w] + (key_value(key) - s_norm[w]), (uint32_t)w * a.vocab + key_index(key));
+        return make_key(s_score[w] + ((key_value(key) - s_norm[w].x) - s_norm[w].y), (uint32_t)w * a.vocab + key_index(key));
     };
     auto read = [&](int list, int j) { return entry(list / a.n_chunks, list, j, __ldcg(keys + (int64_t)list * n + j)); };
     uint64_t mine = 0;
