@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <limits>
 #include <sstream>
 #include <string>
 #include <vector>
@@ -80,14 +81,19 @@ void shaped(const Tensor &t, const char *name, at::IntArrayRef shape, at::Device
     if (t.sizes() != shape) value_error(std::string(name) + " must have shape " + text_of(shape) + ", got " + text_of(t.sizes()));
     on_device(t, name, dev);
 }
-// Device indices as contiguous int32
+// Device indices as contiguous int32.  What needs more bits stays out of range, above or below: no slot, token or node
+// has such a number (see reorder for pools of more than 2^31 slots).
 Tensor ints(const Tensor &t, const char *name, at::IntArrayRef shape, at::Device dev) {
     if (!t.defined()) return t;
     shaped(t, name, shape, dev);
     if (t.scalar_type() == at::kInt) return t.contiguous();
     if (!at::isIntegralType(t.scalar_type(), false))
         type_error(std::string(name) + " must hold integers, got " + toString(t.scalar_type()));
-    return t.to(at::kInt).contiguous();
+    if (t.element_size() < 4) return t.to(at::kInt).contiguous();
+    Tensor wide = t.to(at::kLong);
+    constexpr int64_t least = std::numeric_limits<int32_t>::min(), most = std::numeric_limits<int32_t>::max();
+    if (t.scalar_type() == at::kUInt64) wide = wide.masked_fill(wide.lt(0), most);  // past 2^63
+    return wide.clamp(at::Scalar(least), at::Scalar(most)).to(at::kInt).contiguous();
 }
 bool slots_contiguous(const Tensor &t) {  // every t[i]
     int64_t expected = 1;
@@ -302,7 +308,7 @@ PyObject *reorder(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         const int64_t B = parents.size(0), W = parents.size(1);
         if (W < 1 || W > GDN_BEAM_MAX) value_error("beams must be 1 to " + std::to_string(GDN_BEAM_MAX));
         parents = ints(parents, "parents", {B, W}, dev);
-        const Tensor indices = ints(optional(a[2], "state_indices"), "state_indices", {B, W}, dev);
+        const Tensor given = optional(a[2], "state_indices"), indices = ints(given, "state_indices", {B, W}, dev);
         std::vector<gdn_state_view> views;
         views.reserve(states.size());
         int64_t slots = 0;
@@ -315,6 +321,8 @@ PyObject *reorder(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
             const int64_t size = (int64_t)s.element_size();
             views.push_back({s.data_ptr(), s.stride(0) * size, slots ? s.numel() / slots * size : 0});
         }
+        if (slots > std::numeric_limits<int32_t>::max() && given.defined() && given.scalar_type() != at::kInt)
+            value_error("a pool of more than 2^31 - 1 slots takes int32 state_indices");
         const c10::cuda::CUDAGuard guard(dev);
         check(gdn_reorder_states(views.data(), (int64_t)views.size(), slots, B, W, ptr<int32_t>(parents), ptr<int32_t>(indices),
                                  stream_of(dev)),

@@ -9,9 +9,10 @@
     reorder_states(states, parents, ...)                                         # the states follow it
 
 The calls go through an extension module (``csrc/binding.cpp``) onto the decoding entry points of
-``include/gdn.h``, which also says what happens to indices that are out of range.  Nothing here synchronises or
-copies to the host, so the calls can be captured in a CUDA graph.  There is no CPU path and no backward: training
-runs through ``chunk_gated_delta_rule``.
+``include/gdn.h``, which also says what happens to indices that are out of range (whatever integers hold them: they
+are read as int32, and what does not fit stays out of range).  Nothing here synchronises or copies to the host, so
+the calls can be captured in a CUDA graph.  There is no CPU path and no backward: training runs through
+``chunk_gated_delta_rule``.
 """
 from __future__ import annotations
 
