@@ -198,6 +198,7 @@ PyObject *recurrent(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const c10::cuda::CUDAGuard guard(d.dev);
         Tensor o;
         if (d.q.defined()) o = d.out(p.B, steps);
+        if (cu.defined() && o.defined()) o.zero_();  // the kernel writes the sequences' rows alone
         check(gdn_recurrent(&p, ptr(d.q), ptr(d.k), ptr(d.v), ptr<float>(d.g), ptr<float>(d.beta), ptr<float>(d.state),
                             ptr<float>(out_state), ptr(o), stream_of(d.dev)),
               "gdn_recurrent");

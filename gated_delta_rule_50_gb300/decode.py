@@ -60,7 +60,9 @@ def recurrent_gated_delta_rule(q: Optional[torch.Tensor], k: torch.Tensor, v: to
 
     state_indices [B]  the slot of each row (default: row n has slot n); negative: an idle row, o = 0.  The
                        slots of one call must differ unless ``out_state`` is given.
-    cu_seqlens [N+1]   B = 1: N sequences packed one after the other, one slot each.
+    cu_seqlens [N+1]   B = 1: N sequences packed one after the other, one slot each.  Tokens outside every sequence
+                       have o = 0; so have those of a sequence whose offsets fall or leave the T tokens, unless
+                       another claims them, and its slot stays as it was.
     token_indices [B,P]  run row n through its tokens token_indices[n, 0], [n, 1], ... up to the first negative
                        entry: the accepted path of a drafted tree, or rows of different lengths.  o is [B,P,Hv,V].
     out_state [B,Hv,K,V]  (or [N,...]) gets the new states, row by row, and ``state`` is only read: rows may then

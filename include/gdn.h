@@ -329,7 +329,8 @@ typedef struct {
  *   o         [B, T, Hv, V] contiguous, or [B, n_steps, Hv, V] with token_indices
  *             (0 past a row's end).  q and o may both be NULL: only the states
  *             move.  With cu_seqlens, rows of o outside every sequence are not
- *             written.
+ *             written; a sequence whose offsets fall or leave 0 .. T is skipped,
+ *             its rows and its slot too.
  */
 gdn_status gdn_recurrent(const gdn_decode_problem *p, const void *q, const void *k, const void *v,
                          const float *g, const float *beta, float *state, float *out_state, void *o,
