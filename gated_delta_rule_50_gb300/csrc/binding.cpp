@@ -9,11 +9,13 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <initializer_list>
 #include <limits>
 #include <sstream>
 #include <string>
@@ -115,6 +117,22 @@ void check(gdn_status s, const char *where) {
 }
 gdn_strides strides_of(const Tensor &t) { return {t.stride(0), t.stride(1), t.stride(2)}; }
 
+// Nothing here has a derivative, in either direction: what would drop one is refused
+void no_derivative(std::initializer_list<const Tensor *> tensors) {
+    const bool backward = at::GradMode::is_enabled(), forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    for (const Tensor *t : tensors) {
+        if (!t->defined()) continue;
+        if (backward && t->requires_grad())
+            value_error("the decoding operators have no backward: call them under torch.no_grad(), or train through "
+                        "chunk_gated_delta_rule");
+        if (forward && t->_fw_grad(0).defined()) value_error("the decoding operators take no forward-mode tangents");
+    }
+}
+// A new version of a tensor that a kernel writes in place, as autograd counts them
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // What the two state operators share: checks, the layouts that the kernels read, the problem
 struct Decode {
     Tensor q, k, v, g, beta, state;
@@ -135,10 +153,7 @@ struct Decode {
         shaped(beta, "beta", {p.B, p.T, p.Hv}, dev);
         if (v.scalar_type() != k.scalar_type() || (q.defined() && q.scalar_type() != k.scalar_type()))
             type_error("q, k and v must have one dtype");
-        if (at::GradMode::is_enabled() && (k.requires_grad() || v.requires_grad() || g.requires_grad() || beta.requires_grad() ||
-                                           state.requires_grad() || (q.defined() && q.requires_grad())))
-            value_error("the decoding operators have no backward: call them under torch.no_grad(), or train through "
-                        "chunk_gated_delta_rule");
+        no_derivative({&q, &k, &v, &g, &beta, &state});
         if (state.dim() != 4 || state.size(1) != p.Hv || state.size(2) != p.K || state.size(3) != p.V)
             value_error("state must have shape (slots, " + std::to_string(p.Hv) + ", " + std::to_string(p.K) + ", " +
                         std::to_string(p.V) + "), got " + text_of(state.sizes()));
@@ -194,6 +209,7 @@ PyObject *recurrent(PyObject *, PyObject *const *a, Py_ssize_t n) {
             shaped(out_state, "out_state", {p.n_seqs, p.Hv, p.K, p.V}, d.dev);
             if (out_state.scalar_type() != at::kFloat || !out_state.is_contiguous())
                 value_error("out_state must be contiguous float32");
+            no_derivative({&out_state});
         }
         const c10::cuda::CUDAGuard guard(d.dev);
         Tensor o;
@@ -202,6 +218,7 @@ PyObject *recurrent(PyObject *, PyObject *const *a, Py_ssize_t n) {
         check(gdn_recurrent(&p, ptr(d.q), ptr(d.k), ptr(d.v), ptr<float>(d.g), ptr<float>(d.beta), ptr<float>(d.state),
                             ptr<float>(out_state), ptr(o), stream_of(d.dev)),
               "gdn_recurrent");
+        written(out_state.defined() ? out_state : d.state);
         if (!o.defined()) Py_RETURN_NONE;
         return THPVariable_Wrap(o);
     });
@@ -243,6 +260,7 @@ PyObject *beam(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         if (p.n < 1 || p.n > GDN_BEAM_MAX || p.W < 1 || p.W > GDN_BEAM_MAX)
             value_error("beams and candidates must be 1 to " + std::to_string(GDN_BEAM_MAX));
         shaped(scores, "scores", {p.B, p.W}, dev);
+        no_derivative({&logits, &scores});
         if (scores.scalar_type() != at::kFloat) type_error(std::string("scores must be float32, got ") + toString(scores.scalar_type()));
         logits = inner_contiguous(logits);
         p.logits_batch = logits.stride(0), p.logits_beam = logits.stride(1);
@@ -318,6 +336,7 @@ PyObject *reorder(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
             if (views.empty()) slots = s.size(0);
             if (s.size(0) != slots) value_error("all states must have the same number of slots");
             on_device(s, "states", dev);
+            no_derivative({&s});
             if (!slots_contiguous(s)) value_error("every slot of a state must be contiguous");
             const int64_t size = (int64_t)s.element_size();
             views.push_back({s.data_ptr(), s.stride(0) * size, slots ? s.numel() / slots * size : 0});
@@ -328,6 +347,7 @@ PyObject *reorder(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         check(gdn_reorder_states(views.data(), (int64_t)views.size(), slots, B, W, ptr<int32_t>(parents), ptr<int32_t>(indices),
                                  stream_of(dev)),
               "gdn_reorder_states");
+        for (const Tensor &s : states) written(s);
         Py_RETURN_NONE;
     });
 }

@@ -11,8 +11,9 @@
 The calls go through an extension module (``csrc/binding.cpp``) onto the decoding entry points of
 ``include/gdn.h``, which also says what happens to indices that are out of range (whatever integers hold them: they
 are read as int32, and what does not fit stays out of range).  Nothing here synchronises or copies to the host, so
-the calls can be captured in a CUDA graph.  There is no CPU path and no backward: training runs through
-``chunk_gated_delta_rule``.
+the calls can be captured in a CUDA graph.  There is no CPU path and no derivative: training runs through
+``chunk_gated_delta_rule``, and inputs that require a gradient or carry a tangent are refused (under
+``torch.no_grad()`` the former are taken).
 """
 from __future__ import annotations
 
