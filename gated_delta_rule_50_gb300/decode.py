@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import importlib.machinery
 import importlib.util
+import threading
 from typing import Optional, Sequence, Union
 
 import torch
@@ -33,18 +34,21 @@ TREE_MAX = 64
 BEAM_MAX = 64
 
 _native = None
+_lock = threading.Lock()
 
 
 def load_binding():
     """Builds (if needed) and loads the extension module; raises if either fails."""
     global _native
-    if _native is None:
-        load_library()
-        loader = importlib.machinery.ExtensionFileLoader("_gdn_decode", _build.BINDING)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_gdn_decode", loader))
-        loader.exec_module(module)
-        module.set_error(GdnError)
-        _native = module
+    with _lock:
+        if _native is None:
+            path = _build.build_binding()
+            load_library()
+            loader = importlib.machinery.ExtensionFileLoader("_gdn_decode", path)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_gdn_decode", loader))
+            loader.exec_module(module)
+            module.set_error(GdnError)
+            _native = module
     return _native
 
 
