@@ -6,6 +6,9 @@
 //     o_t = scale (Gam_t S^T q_t + sum_{i in anc(t)} P_ti d_i),                  P_ti = D_ti (q_t . k_i)
 // which is the recurrence along every path at once: no node needs a state of its own.  D is built by products
 // down the tree (D_ti = e^{g_t} D_parent(t),i), so a gate of -inf stays 0 and nothing is a difference of sums.
+// The fast sums run over all nodes, with zeros in L and P where i is not above t, and 0 times a NaN is one.  Such a sum
+// cannot be finite again, so it is enough to look at the results: where one is not, the sums are taken again over the
+// paths alone (from node to parent), and a NaN or an infinity reaches what its path reaches and nothing else.
 // This file holds the CUDA-core kernel, for fp32 io; tree_tc.cu has the tensor-core kernel for bf16.
 //
 // One CTA computes a (row, value head), two threads per value column.  Both have the state in registers as in
@@ -177,7 +180,7 @@ template <int K, int TP> __global__ void __launch_bounds__(256) k_tree(const __g
         s_d[t * V + col] = (bad | absent) >> t & 1 ? 0.f : R;
     }
     __syncthreads();
-    float x[TP];
+    float x[TP], zeros = 0.f;
 #pragma unroll
     for (int t = 0; t < TP; ++t) x[t] = t < T ? s_d[t * V + col] : 0.f;
     if (!half) {
@@ -206,13 +209,36 @@ template <int K, int TP> __global__ void __launch_bounds__(256) k_tree(const __g
             for (int j = 0; j < 4; ++j) x[t + j] = acc[j];
         }
 #pragma unroll
-        for (int t = 0; t < TP; ++t)
-            if (t < T) s_d[t * V + col] = x[t];
+        for (int t = 0; t < TP; ++t) zeros = fmaf(x[t], 0.f, zeros);
+        if (zeros == 0.f) {
+#pragma unroll
+            for (int t = 0; t < TP; ++t)
+                if (t < T) s_d[t * V + col] = x[t];
+        } else {
+            for (int t = 0; t < T; ++t) {
+                if ((bad | absent) >> t & 1) continue;
+                float d = s_d[t * V + col];
+                for (int p = s_par[t]; p >= 0; p = s_par[p]) d = fmaf(-s_l[t * LS + p], s_d[p * V + col], d);
+                s_d[t * V + col] = d;
+            }
+        }
     }
     __syncthreads();
     if (half)
 #pragma unroll
-        for (int t = 0; t < TP; ++t) x[t] = t < T ? s_d[t * V + col] : 0.f;
+        for (int t = 0; t < TP; ++t) {
+            x[t] = t < T ? s_d[t * V + col] : 0.f;
+            zeros = fmaf(x[t], 0.f, zeros);
+        }
+    if (zeros != 0.f) {
+        for (int t = half; t < T; t += 2) {
+            float acc = s_y[t * V + col];
+            if (!((bad | absent) >> t & 1))
+                for (int p = t; p >= 0; p = s_par[p]) acc = fmaf(s_p[t * LS + p], s_d[p * V + col], acc);
+            o[t * o_tok + col] = bad >> t & 1 ? nan : absent >> t & 1 ? 0.f : a.scale * acc;
+        }
+        return;
+    }
 #pragma unroll
     for (int t = 0; t < TP; t += 4) {
         if (t % 16 == 0 && t >= T) break;

@@ -14,15 +14,16 @@
 //
 // q and k are bf16 as given; S, R, L, P and W enter products as hi + lo bf16 pairs (16 bits; one bf16 rounding of
 // them would cost as much as the rounding of o) and are kept in fp32 between them.
+// A head with an output that is not finite is done again along its paths (along_paths; tree.cu says why).
 // S arrives by one bulk copy (a head's state is contiguous); its place in shared memory then holds L, P, W and o, or,
 // where these have a place of their own, the next head's state.
 // Two CTAs stay on each SM (up to 110 KB, 256 TMEM columns each) and take head after head, so that one's copies run under
 // the other's arithmetic; k, q and the gates of a CTA's next head come while group B finishes W.
 //
-// The states' way from memory is the floor.  64 rows of 64 heads, 64 nodes, 128 x 128, take 104 us where that is 66:
+// The states' way from memory is the floor.  64 rows of 64 heads, 64 nodes, 128 x 128, take 106 us where that is 66:
 // a head's steps wait for each other (state, products, inverses, W, products, o), and two heads per SM do not fill
 // the gaps (tensor pipe 18 %, instruction issue 36 %).  Before: CTAs that ended with their head 122 us, W by
-// substitution on CUDA cores behind the state 247.  16 rows of 32 heads, 33 nodes: 15.4 us; one row, 7 nodes: 4.6 us.
+// substitution on CUDA cores behind the state 247.  16 rows of 32 heads, 33 nodes: 15.5 us; one row, 7 nodes: 4.7 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -73,6 +74,7 @@ template <int K, int V, int TP, bool APART> struct Map {
     static constexpr uint32_t END = PW + scratch, TABLE = ((END > STATE + state ? END : STATE + state) + 15) / 16 * 16;
     static constexpr uint32_t VEC = TABLE + TABLE_BYTES, NEXT = VEC + 7 * TP * 4, BAR = NEXT + 3 * TP * 4, MISC = BAR + 8 * BARS;
     static constexpr uint32_t bytes = MISC + 32 + 1024;
+    static_assert(TP * TP * 8 <= scratch, "L and P of along_paths");
 };
 
 // Where row t of the table begins: the first half of the rows at 0, with entries up to t at most; the others
@@ -127,6 +129,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
 // split_pair with its two differences at once
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16(x0, x1);
@@ -174,6 +181,56 @@ __device__ __forceinline__ void block_product(float (&c)[8], const Frag &a, uint
     for (int i = 0; i < 8; ++i) c[i] += x[i];
 }
 
+// All outputs of a head, each sum over the nodes of a path alone, from the inputs in memory and what the head has left
+// in shared memory: the products of e^g, beta (0 for nodes of no use), Gam, parents.  All threads; L and P in `scratch`.
+// 0.06, 0.3 and 0.7 ms for 7, 33 and 64 nodes.  Looking for what is not finite costs 2 % of the heads' time elsewhere (64
+// rows of 64 heads, 64 nodes: 103.4 -> 105.7 us); keeping it out of every operand as it came up took 128 us.
+template <int K, int V, int TP>
+__device__ __noinline__ void along_paths(const DecodeArgs &a, int head, int64_t slot, const float *table, const int4 *s_up, const float *s_b,
+                                         const float *s_gam, uint64_t absent, uint64_t bad, float *scratch) {
+    const int n = head / a.Hv, h = head - n * a.Hv, hq = h / a.G, T = a.T, tid = threadIdx.x;
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + n * a.sq.batch + hq * a.sq.head;
+    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + n * a.sk.batch + hq * a.sk.head;
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + n * a.sv.batch + h * a.sv.head + tid;
+    const float *S = a.state + slot * a.slot_stride + (int64_t)h * K * V + tid;
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)n * T * a.Hv + h) * V + tid;
+    const uint64_t none = absent | bad;
+    float2 *lp = reinterpret_cast<float2 *>(scratch);  // (L, P) of node t and i <= t, t TP + i
+    for (int e = tid; e < T * TP; e += NT) {
+        const int t = e / TP, i = e % TP;
+        if (i > t || (none >> t & 1)) continue;
+        float kk = 0.f, qk = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < K; ++j) {
+            const float x = __bfloat162float(k[i * a.sk.token + j]);
+            kk = fmaf(__bfloat162float(k[t * a.sk.token + j]), x, kk);
+            qk = fmaf(__bfloat162float(q[t * a.sq.token + j]), x, qk);
+        }
+        const float D = table[table_row<TP>(t) + i];
+        lp[e] = make_float2(s_b[t] * D * kk, D * qk);
+    }
+    __syncthreads();
+    if (tid < V) {
+        float d[TP];
+        for (int t = 0; t < T; ++t) {
+            float ks = 0.f, qs = 0.f;
+            if (!(none >> t & 1)) {
+#pragma unroll 4
+                for (int j = 0; j < K; ++j) {
+                    ks = fmaf(__bfloat162float(k[t * a.sk.token + j]), S[j * V], ks);
+                    qs = fmaf(__bfloat162float(q[t * a.sq.token + j]), S[j * V], qs);
+                }
+                float x = s_b[t] * (__bfloat162float(v[t * a.sv.token]) - s_gam[t] * ks), y = s_gam[t] * qs;
+                for (int p = s_up[t].y; p >= 0; p = s_up[p].y) x = fmaf(-lp[t * TP + p].x, d[p], x);
+                d[t] = x;
+                for (int p = t; p >= 0; p = s_up[p].y) y = fmaf(lp[t * TP + p].y, d[p], y);
+                qs = a.scale * y;
+            }
+            o[(int64_t)t * a.Hv * V] = __float2bfloat16_rn(bad >> t & 1 ? __int_as_float(0x7fffffff) : qs);
+        }
+    }
+}
+
 template <int K, int V, int TP, bool APART>
 __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ DecodeArgs a, const __grid_constant__ RowMaps maps, int heads) {
     using M = Map<K, V, TP, APART>;
@@ -192,7 +249,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
     float *table = reinterpret_cast<float *>(sm + M::TABLE);
     uint32_t *misc = reinterpret_cast<uint32_t *>(sm + M::MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
-    uint32_t *s_absent = misc + 2, *s_bad = misc + 4;  // nodes of each kind, a bit each
+    uint32_t *s_absent = misc + 2, *s_bad = misc + 4, *s_found = misc + 6;  // nodes of each kind, a bit each; an output is not finite
     if (t == 32 * SETUP) {
         for (int i = 0; i < BARS; ++i) mbar_init(bars + 8 * i, 1);
         misc[1] = 0;
@@ -261,7 +318,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
         }
         if (t == 32 * SETUP) {
             if (!here) load_state(slot, h);
-            for (int i = 2; i < 6; ++i) misc[i] = 0;
+            for (int i = 2; i < 7; ++i) misc[i] = 0;
         }
         if (warp == SETUP && first) {
             __syncwarp();
@@ -560,15 +617,30 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                     float sg[16];
                     tmem_ld16x2(lanes + kD1 + TP + 16 * c, sq, lanes + kD2 + 16 * c, d2);
                     lds16f(s_sg + 16 * c, sg);
+                    uint64_t zeros = 0;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s_o[(16 * c + i) * V + lane_row] =
-                            __float2bfloat16_rn(fmaf(sg[i], __uint_as_float(sq[i]), __uint_as_float(d2[i])));
+                    for (int i = 0; i < 16; i += 2) {
+                        const float y0 = fmaf(sg[i], __uint_as_float(sq[i]), __uint_as_float(d2[i]));
+                        const float y1 = fmaf(sg[i + 1], __uint_as_float(sq[i + 1]), __uint_as_float(d2[i + 1]));
+                        s_o[(16 * c + i) * V + lane_row] = __float2bfloat16_rn(y0);
+                        s_o[(16 * c + i + 1) * V + lane_row] = __float2bfloat16_rn(y1);
+                        zeros = fma2(pair_of(y0, y1), 0, zeros);
+                    }
+                    float z0, z1;
+                    halves(zeros, z0, z1);
+                    if (z0 + z1 != 0.f) {  // whatever nodes hold that give no output, it is none of this
+                        const uint32_t none = (s_absent[c >> 1] | s_bad[c >> 1]) >> (16 * (c & 1));
+                        for (int i = 0; i < 16; ++i)
+                            if (!(none >> i & 1) && !(fabsf(__bfloat162float(s_o[(16 * c + i) * V + lane_row])) < INFINITY)) *s_found = 1;
+                    }
                 }
             fence_proxy_async_smem();
             named_bar(NB_OUT, NT);
-            const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1];
-            if (dead) {
+            const bool dead = s_absent[0] | s_absent[1] | s_bad[0] | s_bad[1], again = *s_found;
+            if (again) {
+                along_paths<K, V, TP>(a, head, slot, table, s_up, s_b, s_gam, s_absent[0] | (uint64_t)s_absent[1] << 32,
+                                      s_bad[0] | (uint64_t)s_bad[1] << 32, reinterpret_cast<float *>(sm + M::PW));
+            } else if (dead) {
                 for (int i = t / GROUP; i < T && column; i += 2) {
                     if (s_absent[i >> 5] >> (i & 31) & 1) s_o[i * V + lane_row] = __float2bfloat16_rn(0.f);
                     if (s_bad[i >> 5] >> (i & 31) & 1) s_o[i * V + lane_row] = __float2bfloat16_rn(nan);
@@ -576,7 +648,7 @@ __global__ void __launch_bounds__(NT, 2) k_tree_tc(const __grid_constant__ Decod
                 fence_proxy_async_smem();
                 named_bar(NB_OUT, NT);
             }
-            if (t == 0) {  // rows past the last node are not written
+            if (t == 0 && !again) {  // rows past the last node are not written
                 store_rows(&maps.o, sb + M::PW, h * V, n);
                 bulk_commit();
                 bulk_wait_read_all();

@@ -343,6 +343,8 @@ gdn_status gdn_recurrent(const gdn_decode_problem *p, const void *q, const void 
  * and the state itself stays as it was.  parents [B, T] (device, contiguous):
  * an earlier node of the row, or -1 for a child of the state; below -1 the
  * node is absent, and with it what hangs under it (o = 0).  T <= GDN_TREE_MAX.
+ * What is not finite in a node reaches its own outputs and those of the nodes
+ * under it, none of the others (fp32 and bf16).
  * After acceptance, gdn_recurrent with token_indices = the accepted path moves
  * the state.  cu_seqlens and token_indices must be NULL.
  */
