@@ -27,7 +27,7 @@ namespace {
 
 using at::Tensor;
 
-PyObject *g_error = nullptr;  // the package's GdnError
+PyObject *g_error = nullptr, *g_no_memory = nullptr;  // the package's GdnError, torch.OutOfMemoryError
 
 struct Raise {
     PyObject *type;
@@ -50,6 +50,8 @@ template <typename F> PyObject *guarded(F f) {
             PyErr_SetObject(g_error, e);
             Py_DECREF(e);
         }
+    } catch (const c10::OutOfMemoryError &e) {
+        PyErr_SetString(g_no_memory, e.what_without_backtrace());
     } catch (const c10::Error &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
     } catch (const std::exception &e) {
@@ -352,10 +354,12 @@ PyObject *reorder(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     });
 }
 
-PyObject *set_error(PyObject *, PyObject *type) {
-    Py_INCREF(type);
-    Py_XDECREF(g_error);
-    g_error = type;
+// (GdnError, torch.OutOfMemoryError)
+PyObject *set_errors(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    if (!arguments(n_args, 2)) return nullptr;
+    Py_INCREF(a[0]), Py_INCREF(a[1]);
+    Py_XDECREF(g_error), Py_XDECREF(g_no_memory);
+    g_error = a[0], g_no_memory = a[1];
     Py_RETURN_NONE;
 }
 
@@ -364,7 +368,7 @@ PyMethodDef methods[] = {
     {"tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree)), METH_FASTCALL, nullptr},
     {"beam", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(beam)), METH_FASTCALL, nullptr},
     {"reorder", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(reorder)), METH_FASTCALL, nullptr},
-    {"set_error", set_error, METH_O, nullptr},
+    {"set_errors", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(set_errors)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdn_decode", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -47,7 +47,7 @@ def load_binding():
             loader = importlib.machinery.ExtensionFileLoader("_gdn_decode", path)
             module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_gdn_decode", loader))
             loader.exec_module(module)
-            module.set_error(GdnError)
+            module.set_errors(GdnError, torch.OutOfMemoryError)
             _native = module
     return _native
 
