@@ -9,9 +9,10 @@
 // 128-byte line per row across the lanes).  The value columns are independent, so nothing crosses warps;
 // the four r lanes of a column group meet through shuffles.
 //
-// Up to about six tokens the states' way through memory bounds the step (each is read and written once): 64 rows of
-// 32 heads, 128 x 128, one bf16 token, take 45 us, 6.0 TB/s; one row 3.3 us, where reads, sums and writes wait for
-// each other.  Two kernels share the arithmetic: k_recurrent, a warp per CTA and 32 columns, and k_recurrent_flow for
+// For one token the states' way through memory bounds the step (each is read and written once): 64 rows of 32 heads,
+// 128 x 128, bf16, take 45 us, 6.0 TB/s; one row 3.0 us, where reads, sums and writes wait for each other.  More tokens
+// on the same states take 53 us (3) and 74 us (6), where memory would take 41 and 42: each costs three multiply-adds per
+// element of the state and two reads of k, with seven or eight warps on an SM.  Two kernels share the arithmetic: k_recurrent, a warp per CTA and 32 columns, and k_recurrent_flow for
 // lists of tokens on many heads (see launch()).
 #include <cuda_bf16.h>
 
@@ -447,10 +448,11 @@ template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
                          (a.o ? reinterpret_cast<uintptr_t>(a.q) : 0);
     const bool rows16 = !((strides * (int64_t)sizeof(IO)) & 15) && !(at & 15);
-    // The ring pays for lists of tokens from about twelve states per SM on: 53.2 us against 53.6 of single warps at 2048
-    // heads, 136 against 152 at 6144 (6 tokens at most; 2 tokens: 130 against 128), but 32.2 against 30.2 at 1024.
-    // Without lists warps are faster at every size (64 rows of 32 heads, 1 token: 45 against 46 us; 16 rows: 13.4
-    // against 14.2), for narrow heads too (96 rows of 64 heads, 64 x 64, lists: 23 against 35).
+    // The ring pays for lists of tokens from about twelve states per SM on: 52.4 us against 52.8 of single warps at 2048
+    // heads, 92 against 99 at 4096, 134 against 148 at 6144 (6 tokens at most; fp32: 148 against 156; 2 tokens: 129.5
+    // against 126.4), but 31.8 against 30.0 at 1024.  Without lists warps are faster at every size (64 rows of 32 heads
+    // with 1, 3 and 6 tokens: 44.7, 53.2 and 73.8 us against 46.0, 53.6 and 75.8; 16 rows: 13.4 against 14.2), for narrow
+    // heads too (96 rows of 64 heads, 64 x 64, lists: 23 against 35).
     if constexpr (K == 128)
         if (a.token_indices && a.V == kGroup && heads >= 12 * kSMs && rows16) {
             static std::atomic<uint64_t> done{0};

@@ -13,10 +13,12 @@
 //
 // One CTA computes a (row, value head), two threads per value column.  Both have the state in registers as in
 // decode.cu and take S^T k_t and S^T q_t of every other node; then one makes the column's corrections d, and both
-// the outputs, with L and P read as broadcast vectors.  Bound by fp32 multiply-adds (2 T K V of them for the state,
-// T^2 (K + V) for the rest) and the shared-memory reads that feed them: 64 rows of 32 heads, 64 nodes, 128 x 128, take
-// 811 us, 7.9 T multiply-adds a second; 16 rows of 32 heads 34 us with 7 nodes and 96 with 32.  One thread per column
-// and rows staged element by element took 1265 us.
+// the outputs, with L and P read as broadcast vectors.  64 rows of 32 heads, 64 nodes, 128 x 128, take 830 us; 16 rows of
+// 32 heads 35 us with 7 nodes, 98 with 32.  Neither memory (5 %) nor the multiply-adds (2 T K V for the state, T^2 (K + V)
+// for the rest: 7.7 T a second, a fifth of what the SMs could) bound it, but the chain: an SM holds one such CTA, whose
+// loads, products, substitution and outputs follow each other (1.5 instructions a cycle, barriers first among the stalls).
+// One thread per column and rows staged element by element took 1265 us, but 98 instead of 114 for 16 rows of 32 heads
+// with 33 nodes.
 #include "common.cuh"
 #include "decode.h"
 
@@ -275,8 +277,8 @@ template <int K, int TP> cudaError_t launch(const DecodeArgs &a, cudaStream_t st
     const bool rows16 = !(steps & 3) && !(at & 15);  // 16 rows of 32 heads, 48 nodes: 142 us, 147 with pieces of 4 bytes
     return launch_behind(k_tree<K, TP>, dim3((unsigned)(a.n_seqs * a.Hv)), 2 * a.V, (size_t)tree_floats<K, TP>(a.T, a.V) * 4, st, a, rows16);
 }
-// The triangles' loops end at the width: 16 rows of 32 heads with 7, 16, 32 and 48 nodes take 34, 54, 96 and 142 us
-// and with 64 as the only width 45, 72, 109 and 148.
+// The triangles' loops end at the width: 16 rows of 32 heads with 7, 16, 32 and 48 nodes take 35, 55, 98 and 144 us
+// and with 64 as the only width 47, 74, 111 and 151.
 template <int K> cudaError_t launch_nodes(const DecodeArgs &a, cudaStream_t st) {
     if (a.T <= 16) return launch<K, 16>(a, st);
     if (a.T <= 32) return launch<K, 32>(a, st);

@@ -724,11 +724,11 @@ template <int K, int V, int TP, bool APART = false> cudaError_t launch(const Dec
 }
 
 // Products, tables and W are as wide as the nodes, rounded up to blocks of 16: 16 rows of 32 heads with 16, 32 and 48
-// nodes take 11.3, 13.5 and 15.7 us and with 64 as the only width 16.2, 16.7 and 17.4; one row of 7 nodes 4.6 and 6.6.
+// nodes take 11.5, 13.9 and 16.0 us and with 64 as the only width 16.2, 17.0 and 17.6; one row of 7 nodes 4.8 and 6.7.
 template <int K, int V> cudaError_t launch_nodes(const DecodeArgs &a, cudaStream_t st) {
     // The scratch apart from the state, and the state asked for ahead, from more than two turns of the CTAs on: 64 rows
-    // of 64 heads with 16 nodes 60.7 us against 72.5, with 32 74.1 against 82.4; 768 heads with 7 nodes 15.8 and 16.0,
-    // but 512 11.5 and 10.9.  Narrower states lose by it at every size (64 x 64, 64 rows of 64 heads, 32 nodes: 65.8
+    // of 64 heads with 16 nodes 62.2 us against 73.6, with 32 75.3 against 83.7; 768 heads with 7 nodes 16.4 and 16.5,
+    // but 512 12.0 and 11.0.  Narrower states lose by it at every size (64 x 64, 64 rows of 64 heads, 32 nodes: 65.8
     // and 61.3 us), and with more nodes two CTAs do not fit on an SM.
     if constexpr (K == 128 && V == 128)
         if (a.T <= 32 && (int64_t)a.n_seqs * a.Hv >= 4 * kSMs) return a.T <= 16 ? launch<K, V, 16, true>(a, st) : launch<K, V, 32, true>(a, st);
