@@ -21,6 +21,13 @@ the decoding calls that follow a prefill (``decode.py``):
     o = tree_gated_delta_rule(q, k, v, g, beta, parents, state, ...)    # drafted tokens, state kept
     scores, tokens, parents = beam_search_step(logits, scores, ...)
     reorder_states(states, parents, ...)
+    tokens, logprobs = sample_tokens(logits, random, temperature, top_k, top_p, min_p, mask)
+
+linear attention with a decay for each head (``linear.py``; its step is in ``decode.py``):
+
+    o, final_state = chunk_linear_attention(q, k, v, g, scale=None, initial_state=None,
+        output_final_state=False, cu_seqlens=None)
+    o = recurrent_linear_attention(q, k, v, g, state, ...)              # state pool moved in place
 
 plus the save-for-backward pair that training through ``chunk_gated_delta_rule`` uses (the forward
 keeps its operand images and chunk-entry states; the backward skips its recompute passes):
@@ -42,7 +49,9 @@ from . import build as _build
 __all__ = ["chunk_gated_delta_rule", "chunk_gated_delta_rule_fwd", "chunk_gated_delta_rule_bwd",
            "chunk_gated_delta_rule_fwd_saved", "chunk_gated_delta_rule_bwd_saved", "SavedForward",
            "cp_plan", "cp_trigger", "GdnError", "load_library", "library_path", "workspace_bytes", "CHUNK",
-           "recurrent_gated_delta_rule", "tree_gated_delta_rule", "beam_search_step", "reorder_states"]
+           "recurrent_gated_delta_rule", "tree_gated_delta_rule", "beam_search_step", "reorder_states",
+           "sample_tokens", "recurrent_linear_attention", "chunk_linear_attention", "chunk_linear_attention_fwd",
+           "chunk_linear_attention_bwd"]
 
 CHUNK = 64
 GDN_F32, GDN_BF16 = 0, 1
@@ -372,5 +381,6 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None,
     return o, (ht if output_final_state else None)
 
 
-from .decode import (beam_search_step, recurrent_gated_delta_rule, reorder_states,  # noqa: E402
-                     tree_gated_delta_rule)
+from .decode import (beam_search_step, recurrent_gated_delta_rule, recurrent_linear_attention,  # noqa: E402
+                     reorder_states, sample_tokens, tree_gated_delta_rule)
+from .linear import (chunk_linear_attention, chunk_linear_attention_bwd, chunk_linear_attention_fwd)  # noqa: E402

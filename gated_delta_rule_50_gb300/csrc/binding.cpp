@@ -1,4 +1,5 @@
-// binding.cpp -- the Python side of the decoding entry points of include/gdn.h, as an extension module.
+// binding.cpp -- the Python side of the decoding entry points of include/gdn.h and of those of linear attention, as an
+// extension module.
 //
 // A decoding call works for a few microseconds on the GPU, and marshalling it through ctypes took three times as
 // long: reading some forty properties of the tensors one Python attribute at a time.  Here they are read from the
@@ -14,11 +15,13 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 #include <limits>
 #include <sstream>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "gdn.h"
@@ -126,8 +129,17 @@ void no_derivative(std::initializer_list<const Tensor *> tensors) {
         if (!t->defined()) continue;
         if (backward && t->requires_grad())
             value_error("the decoding operators have no backward: call them under torch.no_grad(), or train through "
-                        "chunk_gated_delta_rule");
+                        "chunk_gated_delta_rule or chunk_linear_attention");
         if (forward && t->_fw_grad(0).defined()) value_error("the decoding operators take no forward-mode tangents");
+    }
+}
+// The calls below the autograd function of linear attention: a derivative is not dropped either
+void below_autograd(std::initializer_list<const Tensor *> tensors) {
+    const bool backward = at::GradMode::is_enabled(), forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    for (const Tensor *t : tensors) {
+        if (!t->defined()) continue;
+        if (backward && t->requires_grad()) value_error("chunk_linear_attention_fwd and _bwd have no derivative: call chunk_linear_attention");
+        if (forward && t->_fw_grad(0).defined()) value_error("linear attention takes no forward-mode tangents");
     }
 }
 // A new version of a tensor that a kernel writes in place, as autograd counts them
@@ -141,8 +153,10 @@ struct Decode {
     gdn_decode_problem p{};
     at::Device dev = at::kCPU;
 
-    Decode(PyObject *const *a) {
-        q = optional(a[0], "q"), k = tensor(a[1], "k"), v = tensor(a[2], "v"), g = tensor(a[3], "g"), beta = tensor(a[4], "beta");
+    // a: q, k, v, g, beta, state, scale; without the delta rule beta is None and g, which may be, has one value per head
+    Decode(PyObject *const *a, bool delta = true) {
+        q = optional(a[0], "q"), k = tensor(a[1], "k"), v = tensor(a[2], "v");
+        g = delta ? tensor(a[3], "g") : optional(a[3], "g"), beta = delta ? tensor(a[4], "beta") : Tensor();
         state = tensor(a[5], "state");
         on_cuda(k, "k");
         dev = k.device();
@@ -151,8 +165,12 @@ struct Decode {
         p.io_dtype = io_dtype(k, "io");
         if (q.defined()) shaped(q, "q", k.sizes(), dev);
         shaped(v, "v", {p.B, p.T, p.Hv, p.V}, dev);
-        shaped(g, "g", {p.B, p.T, p.Hv}, dev);
-        shaped(beta, "beta", {p.B, p.T, p.Hv}, dev);
+        if (delta) {
+            shaped(g, "g", {p.B, p.T, p.Hv}, dev);
+            shaped(beta, "beta", {p.B, p.T, p.Hv}, dev);
+        } else if (g.defined()) {
+            shaped(g, "g", {p.Hv}, dev);
+        }
         if (v.scalar_type() != k.scalar_type() || (q.defined() && q.scalar_type() != k.scalar_type()))
             type_error("q, k and v must have one dtype");
         no_derivative({&q, &k, &v, &g, &beta, &state});
@@ -164,9 +182,14 @@ struct Decode {
         if (!slots_contiguous(state)) value_error("every slot of state must be contiguous");
         k = inner_contiguous(k), v = inner_contiguous(v);
         if (q.defined()) q = inner_contiguous(q), p.q = strides_of(q);
-        if (g.scalar_type() != at::kFloat) g = g.to(at::kFloat);
-        if (beta.scalar_type() != at::kFloat) beta = beta.to(at::kFloat);
-        p.k = strides_of(k), p.v = strides_of(v), p.g = strides_of(g), p.beta = strides_of(beta);
+        if (g.defined() && g.scalar_type() != at::kFloat) g = g.to(at::kFloat);
+        p.k = strides_of(k), p.v = strides_of(v);
+        if (delta) {
+            if (beta.scalar_type() != at::kFloat) beta = beta.to(at::kFloat);
+            p.g = strides_of(g), p.beta = strides_of(beta);
+        } else if (g.defined()) {
+            g = g.contiguous();
+        }
         p.scale = a[6] == Py_None ? (float)std::pow((double)p.K, -0.5) : (float)PyFloat_AsDouble(a[6]);
         if (PyErr_Occurred()) throw std::runtime_error("scale");
         p.n_slots = state.size(0), p.slot_stride = state.stride(0);
@@ -184,10 +207,10 @@ bool arguments(Py_ssize_t got, Py_ssize_t wanted) {
 }
 
 // (q, k, v, g, beta, state, scale, state_indices, cu_seqlens, token_indices, out_state) -> o or None
-PyObject *recurrent(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *step(PyObject *const *a, Py_ssize_t n, bool delta) {
     if (!arguments(n, 11)) return nullptr;
     return guarded([&]() -> PyObject * {
-        Decode d(a);
+        Decode d(a, delta);
         gdn_decode_problem &p = d.p;
         Tensor cu = optional(a[8], "cu_seqlens"), list = optional(a[9], "token_indices"), out_state = optional(a[10], "out_state");
         int64_t steps = p.T;
@@ -217,14 +240,22 @@ PyObject *recurrent(PyObject *, PyObject *const *a, Py_ssize_t n) {
         Tensor o;
         if (d.q.defined()) o = d.out(p.B, steps);
         if (cu.defined() && o.defined()) o.zero_();  // the kernel writes the sequences' rows alone
-        check(gdn_recurrent(&p, ptr(d.q), ptr(d.k), ptr(d.v), ptr<float>(d.g), ptr<float>(d.beta), ptr<float>(d.state),
-                            ptr<float>(out_state), ptr(o), stream_of(d.dev)),
-              "gdn_recurrent");
+        if (delta)
+            check(gdn_recurrent(&p, ptr(d.q), ptr(d.k), ptr(d.v), ptr<float>(d.g), ptr<float>(d.beta), ptr<float>(d.state),
+                                ptr<float>(out_state), ptr(o), stream_of(d.dev)),
+                  "gdn_recurrent");
+        else
+            check(gdn_linear_recurrent(&p, ptr(d.q), ptr(d.k), ptr(d.v), ptr<float>(d.g), ptr<float>(d.state),
+                                       ptr<float>(out_state), ptr(o), stream_of(d.dev)),
+                  "gdn_linear_recurrent");
         written(out_state.defined() ? out_state : d.state);
         if (!o.defined()) Py_RETURN_NONE;
         return THPVariable_Wrap(o);
     });
 }
+
+PyObject *recurrent(PyObject *, PyObject *const *a, Py_ssize_t n) { return step(a, n, true); }
+PyObject *linear_recurrent(PyObject *, PyObject *const *a, Py_ssize_t n) { return step(a, n, false); }
 
 // (q, k, v, g, beta, state, scale, state_indices, parents) -> o
 PyObject *tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -354,6 +385,183 @@ PyObject *reorder(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     });
 }
 
+// What the forward and the backward of linear attention share: checks, layouts, the problem
+struct Linear {
+    Tensor q, k, v, g, h0, cu;
+    gdn_linear_problem p{};
+    at::Device dev = at::kCPU;
+
+    // a: q, k, v, g, scale, initial_state, cu_seqlens
+    Linear(PyObject *const *a) {
+        q = tensor(a[0], "q"), k = tensor(a[1], "k"), v = tensor(a[2], "v"), g = optional(a[3], "g");
+        h0 = optional(a[5], "initial_state"), cu = optional(a[6], "cu_seqlens");
+        below_autograd({&q, &k, &v, &g, &h0});
+        on_cuda(q, "q");
+        dev = q.device();
+        if (q.dim() != 4 || v.dim() != 4) value_error("q and v must have four dimensions: [B, T, heads, width]");
+        p.B = q.size(0), p.T = q.size(1), p.Hq = q.size(2), p.K = q.size(3), p.Hv = v.size(2), p.V = v.size(3);
+        p.io_dtype = io_dtype(q, "io");
+        shaped(k, "k", q.sizes(), dev);
+        shaped(v, "v", {p.B, p.T, p.Hv, p.V}, dev);
+        if (k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type()) type_error("q, k and v must have one dtype");
+        q = inner_contiguous(q), k = inner_contiguous(k), v = inner_contiguous(v);
+        p.q = strides_of(q), p.k = strides_of(k), p.v = strides_of(v);
+        if (g.defined()) {
+            shaped(g, "g", {p.Hv}, dev);
+            if (c10::isComplexType(g.scalar_type())) type_error("g must hold real numbers");
+            if (g.scalar_type() != at::kFloat) g = g.to(at::kFloat);
+            g = g.contiguous();
+        }
+        p.scale = a[4] == Py_None ? (float)std::pow((double)p.K, -0.5) : (float)PyFloat_AsDouble(a[4]);
+        if (PyErr_Occurred()) throw std::runtime_error("scale");
+        p.n_seqs = p.B;
+        if (cu.defined()) {
+            if (p.B != 1) value_error("cu_seqlens needs B = 1");
+            if (cu.dim() != 1 || cu.size(0) < 1) value_error("cu_seqlens must have one dimension and at least one entry");
+            cu = ints(cu, "cu_seqlens", cu.sizes(), dev);
+            p.n_seqs = cu.size(0) - 1;
+            p.cu_seqlens = ptr<int32_t>(cu);
+        }
+        h0 = state(h0, "initial_state");
+    }
+    Tensor state(const Tensor &t, const char *name) const {
+        if (!t.defined()) return t;
+        shaped(t, name, {p.n_seqs, p.Hv, p.K, p.V}, dev);
+        if (t.scalar_type() != at::kFloat) type_error(std::string(name) + " must be float32, got " + toString(t.scalar_type()));
+        return t.contiguous();
+    }
+    Tensor new_state() const { return at::detail::empty_cuda({p.n_seqs, p.Hv, p.K, p.V}, at::kFloat, dev, std::nullopt); }
+    Tensor workspace(size_t bytes, const char *where) const {
+        if (bytes == 0) throw Failed{GDN_ERR_UNSUPPORTED, where};
+        return at::detail::empty_cuda({(int64_t)bytes}, at::kByte, dev, std::nullopt);
+    }
+};
+
+// (q, k, v, g, scale, initial_state, cu_seqlens, output_final_state) -> (o, final_state or None)
+PyObject *linear_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 8)) return nullptr;
+    return guarded([&]() -> PyObject * {
+        Linear x(a);
+        const int wanted = PyObject_IsTrue(a[7]);
+        if (wanted < 0) throw std::runtime_error("output_final_state");
+        const c10::cuda::CUDAGuard guard(x.dev);
+        const Tensor ws = x.workspace(gdn_linear_fwd_workspace_bytes(&x.p), "gdn_linear_fwd");
+        const Tensor o = at::detail::empty_cuda({x.p.B, x.p.T, x.p.Hv, x.p.V}, x.q.scalar_type(), x.dev, std::nullopt);
+        const Tensor end = wanted ? x.new_state() : Tensor();
+        check(gdn_linear_fwd(&x.p, ptr(x.q), ptr(x.k), ptr(x.v), ptr<float>(x.g), ptr<float>(x.h0), ptr(o), ptr<float>(end),
+                             ptr(ws), ws.nbytes(), stream_of(x.dev)),
+              "gdn_linear_fwd");
+        PyObject *first = THPVariable_Wrap(o), *second = Py_None;
+        if (wanted) second = THPVariable_Wrap(end);
+        else Py_INCREF(Py_None);
+        return Py_BuildValue("(NN)", first, second);
+    });
+}
+
+// (q, k, v, g, scale, initial_state, cu_seqlens, do, dht, wanted) -> (dq, dk, dv, dh0), None for each whose bit of `wanted` is 0
+PyObject *linear_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 10)) return nullptr;
+    return guarded([&]() -> PyObject * {
+        Linear x(a);
+        Tensor d_o = tensor(a[7], "do");
+        shaped(d_o, "do", {x.p.B, x.p.T, x.p.Hv, x.p.V}, x.dev);
+        if (d_o.scalar_type() != x.q.scalar_type()) type_error("do must have the dtype of q, k and v");
+        d_o = inner_contiguous(d_o);
+        x.p.d_o = strides_of(d_o);
+        const Tensor dht = x.state(optional(a[8], "dht"), "dht");
+        below_autograd({&d_o, &dht});
+        const long wanted = PyLong_AsLong(a[9]);
+        if (PyErr_Occurred()) throw std::runtime_error("wanted");
+        const c10::cuda::CUDAGuard guard(x.dev);
+        const Tensor ws = x.workspace(gdn_linear_bwd_workspace_bytes(&x.p), "gdn_linear_bwd");
+        Tensor out[4];
+        for (int i = 0; i < 3; ++i)
+            if (wanted >> i & 1)
+                out[i] = at::detail::empty_cuda(i < 2 ? x.q.sizes() : x.v.sizes(), x.q.scalar_type(), x.dev, std::nullopt);
+        if (wanted >> 3 & 1) out[3] = x.new_state();
+        check(gdn_linear_bwd(&x.p, ptr(x.q), ptr(x.k), ptr(x.v), ptr<float>(x.g), ptr<float>(x.h0), ptr(d_o), ptr<float>(dht),
+                             ptr(out[0]), ptr(out[1]), ptr(out[2]), ptr<float>(out[3]), ptr(ws), ws.nbytes(), stream_of(x.dev)),
+              "gdn_linear_bwd");
+        PyObject *r[4];
+        for (int i = 0; i < 4; ++i) {
+            r[i] = out[i].defined() ? THPVariable_Wrap(out[i]) : Py_None;
+            if (!out[i].defined()) Py_INCREF(Py_None);
+        }
+        return Py_BuildValue("(NNNN)", r[0], r[1], r[2], r[3]);
+    });
+}
+
+// A parameter of every row: a number, or a tensor of one for each row
+template <typename T> Tensor per_row(PyObject *o, const char *name, T none, T *one, int64_t B, at::Device dev) {
+    *one = none;
+    if (o == Py_None) return Tensor();
+    if (!THPVariable_Check(o)) {
+        if constexpr (std::is_same_v<T, float>) {
+            *one = (float)PyFloat_AsDouble(o);
+        } else {
+            const long long k = PyLong_AsLongLong(o);
+            *one = (T)std::min<long long>(std::max<long long>(k, std::numeric_limits<T>::min()), std::numeric_limits<T>::max());
+        }
+        if (PyErr_Occurred()) throw std::runtime_error(name);
+        return Tensor();
+    }
+    const Tensor t = THPVariable_Unpack(o);
+    if constexpr (std::is_same_v<T, float>) {
+        shaped(t, name, {B}, dev);
+        if (!at::isFloatingType(t.scalar_type())) type_error(std::string(name) + " must hold floating-point numbers, got " + toString(t.scalar_type()));
+        return t.to(at::kFloat).contiguous();
+    } else {
+        return ints(t, name, {B}, dev);
+    }
+}
+
+// (logits, random, temperature, top_k, top_p, min_p, mask) -> (tokens, logprobs)
+PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 7)) return nullptr;
+    return guarded([&]() -> PyObject * {
+        Tensor logits = tensor(a[0], "logits"), u = tensor(a[1], "random"), mask = optional(a[6], "mask");
+        on_cuda(logits, "logits");
+        const at::Device dev = logits.device();
+        if (logits.dim() != 2) value_error("logits must have two dimensions: [B, vocab]");
+        gdn_sample_problem p{};
+        p.B = logits.size(0), p.vocab = logits.size(1);
+        p.logits_dtype = io_dtype(logits, "logits");
+        if (p.vocab < 1 || p.vocab > GDN_SAMPLE_VOCAB_MAX)
+            value_error("the vocabulary must have 1 to " + std::to_string(GDN_SAMPLE_VOCAB_MAX) + " tokens");
+        shaped(u, "random", {p.B}, dev);
+        if (u.scalar_type() != at::kFloat) type_error(std::string("random must be float32, got ") + toString(u.scalar_type()));
+        no_derivative({&logits, &u});
+        logits = inner_contiguous(logits), u = u.contiguous();
+        p.logits_row = logits.stride(0);
+        const Tensor heat = per_row<float>(a[2], "temperature", 1.f, &p.temperature, p.B, dev);
+        const Tensor top_k = per_row<int32_t>(a[3], "top_k", 0, &p.top_k, p.B, dev);
+        const Tensor top_p = per_row<float>(a[4], "top_p", 1.f, &p.top_p, p.B, dev);
+        const Tensor min_p = per_row<float>(a[5], "min_p", 0.f, &p.min_p, p.B, dev);
+        no_derivative({&heat, &top_p, &min_p});
+        p.temperatures = ptr<float>(heat), p.top_ks = ptr<int32_t>(top_k), p.top_ps = ptr<float>(top_p), p.min_ps = ptr<float>(min_p);
+        if (mask.defined()) {
+            if (mask.scalar_type() != at::kBool) type_error(std::string("mask must be bool, got ") + toString(mask.scalar_type()));
+            on_device(mask, "mask", dev);
+            if (mask.sizes() != logits.sizes()) {
+                try {
+                    mask = mask.expand(logits.sizes());
+                } catch (const c10::Error &) {
+                    value_error("mask must be broadcastable to " + text_of(logits.sizes()) + ", got " + text_of(mask.sizes()));
+                }
+            }
+            mask = inner_contiguous(mask);
+            p.mask_row = mask.stride(0);
+        }
+        const c10::cuda::CUDAGuard guard(dev);
+        const Tensor tokens = at::detail::empty_cuda({p.B}, at::kInt, dev, std::nullopt);
+        const Tensor logprobs = at::detail::empty_cuda({p.B}, at::kFloat, dev, std::nullopt);
+        check(gdn_sample(&p, ptr(logits), ptr<float>(u), ptr<uint8_t>(mask), ptr<int32_t>(tokens), ptr<float>(logprobs), stream_of(dev)),
+              "gdn_sample");
+        PyObject *t = THPVariable_Wrap(tokens), *l = THPVariable_Wrap(logprobs);
+        return Py_BuildValue("(NN)", t, l);
+    });
+}
+
 // (GdnError, torch.OutOfMemoryError)
 PyObject *set_errors(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     if (!arguments(n_args, 2)) return nullptr;
@@ -368,6 +576,10 @@ PyMethodDef methods[] = {
     {"tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(tree)), METH_FASTCALL, nullptr},
     {"beam", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(beam)), METH_FASTCALL, nullptr},
     {"reorder", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(reorder)), METH_FASTCALL, nullptr},
+    {"linear_recurrent", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_recurrent)), METH_FASTCALL, nullptr},
+    {"linear_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_fwd)), METH_FASTCALL, nullptr},
+    {"linear_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_bwd)), METH_FASTCALL, nullptr},
+    {"sample", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sample)), METH_FASTCALL, nullptr},
     {"set_errors", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(set_errors)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdn_decode", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -2,7 +2,8 @@
 //
 // Per row and value head, with a = e^g:  d = beta (v - a S^T k),  S' = a S + k d^T,  o = scale S'^T q.
 // Both products are taken from the state before the update, o = scale (a S^T q + (q.k) d), so one pass over
-// the state's registers serves k and q and a second one updates it.
+// the state's registers serves k and q and a second one updates it.  Linear attention (DELTA false) is the same without the
+// correction, d = v, and with one a per head.
 //
 // A warp holds a [K][32] tile of the state in registers: lane = (r, c) with c = 0..7 has the four columns
 // 4c .. 4c+3 of the rows 16 i + 4 r + j (K values of 32 bits per lane, K/4 accesses of 16 bytes, each a full
@@ -76,7 +77,7 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *x) {
 }
 
 // The threads of one head (tid = 0 .. COLS - 1, columns col0 + tid) and, for more than a warp, their barrier
-template <int K, int COLS, typename IO> struct Head {
+template <int K, int COLS, typename IO, bool DELTA> struct Head {
     static constexpr int NR = K / 4;
     const DecodeArgs &a;
     Stage<K, COLS, IO> &s;
@@ -93,8 +94,8 @@ template <int K, int COLS, typename IO> struct Head {
         q = static_cast<const IO *>(a.q) + u.b * a.sq.batch + hq * a.sq.head;
         k = static_cast<const IO *>(a.k) + u.b * a.sk.batch + hq * a.sk.head;
         v = static_cast<const IO *>(a.v) + u.b * a.sv.batch + h * a.sv.head + col0 + tid;
-        g = a.g + u.b * a.sg.batch + h * a.sg.head;
-        beta = a.beta + u.b * a.sb.batch + h * a.sb.head;
+        g = a.g ? a.g + u.b * a.sg.batch + h * a.sg.head : nullptr;
+        beta = DELTA ? a.beta + u.b * a.sb.batch + h * a.sb.head : nullptr;
         o = a.o ? static_cast<IO *>(a.o) + (u.out_row * a.Hv + h) * a.V + col0 : nullptr;
     }
     __device__ __forceinline__ void sync() const {
@@ -144,7 +145,10 @@ template <int K, int COLS, typename IO> struct Head {
 #pragma unroll 4
             for (int t = 0; t < m; ++t) s.v[t][tid] = v[token(t) * a.sv.token];
         }
-        if (tid < m) s.a[tid] = expf(g[token(tid) * a.sg.token]), s.b[tid] = beta[token(tid) * a.sb.token];
+        if (tid < m) {
+            s.a[tid] = DELTA || g ? expf(g[token(tid) * a.sg.token]) : 1.f;
+            if constexpr (DELTA) s.b[tid] = beta[token(tid) * a.sb.token];
+        }
         asm volatile("cp.async.wait_all;" ::: "memory");
         return m;
     }
@@ -160,7 +164,7 @@ template <int K, int COLS, typename IO> struct Head {
                 const float4 kk = load4(s.k[t] + 16 * i + 4 * r);
                 const float kj[4] = {kk.x, kk.y, kk.z, kk.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; DELTA && j < 4; ++j) {
                     const float4 x = S[4 * i + j];
                     ks[0] = fmaf(kj[j], x.x, ks[0]);
                     ks[1] = fmaf(kj[j], x.y, ks[1]);
@@ -182,7 +186,8 @@ template <int K, int COLS, typename IO> struct Head {
                 }
             }
             const float al = s.a[t];
-            const float d = s.b[t] * (to_f<IO>(s.v[t][col]) - al * reduce_columns(ks, r));
+            float d = to_f<IO>(s.v[t][col]);
+            if constexpr (DELTA) d = s.b[t] * (d - al * reduce_columns(ks, r));
             if (o) {
                 qk += __shfl_xor_sync(~0u, qk, 8);
                 qk += __shfl_xor_sync(~0u, qk, 16);
@@ -234,7 +239,7 @@ template <int K, int COLS, typename IO> struct Head {
 // aligned, against reads of single elements: 3.3 and 3.6 us for that one row, 5.4 and 6.4 us for 37 rows of 8 fp32
 // heads, 64 x 64, 3 tokens.
 // grid (rows, q/k heads, value heads of one * parts of the columns)
-template <int K, typename IO> __global__ void __launch_bounds__(kTile) k_recurrent(const __grid_constant__ DecodeArgs a, bool rows16) {
+template <int K, typename IO, bool DELTA> __global__ void __launch_bounds__(kTile) k_recurrent(const __grid_constant__ DecodeArgs a, bool rows16) {
     constexpr int NR = K / 4;
     __shared__ Stage<K, kTile, IO> s;
     const int tid = threadIdx.x;
@@ -242,7 +247,7 @@ template <int K, typename IO> __global__ void __launch_bounds__(kTile) k_recurre
     wait_for_previous();
     const Run u = run_of(a, n);
     if (!u.valid) return;
-    const Head<K, kTile, IO> head(a, s, u, n, h, hq, col0, tid, 0, rows16);
+    const Head<K, kTile, IO, DELTA> head(a, s, u, n, h, hq, col0, tid, 0, rows16);
     if (u.slot < 0 || u.slot >= a.n_slots) {
         head.fill(0, u.slot >= 0);
         return;
@@ -292,7 +297,7 @@ template <typename IO> struct Flow {
 // taken by this group, which waited for its `armed`, or by the other one, which took it after asking for it or waits
 // for a head that this group asked for.
 // 96 rows of 64 heads, up to 6 tokens each: 134 us, 6.0 TB/s.
-template <typename IO>
+template <typename IO, bool DELTA>
 __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_constant__ DecodeArgs a, int heads) {
     using F = Flow<IO>;
     constexpr int K = F::K, V = F::V, NR = K / 4, AHEAD = kTok<IO>;
@@ -330,8 +335,8 @@ __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_c
         x.tok = at;
         x.g = x.beta = 0.f;
         if (lane < x.m) {
-            x.g = a.g[x.u.b * a.sg.batch + x.h * a.sg.head + x.tok * a.sg.token];
-            x.beta = a.beta[x.u.b * a.sb.batch + x.h * a.sb.head + x.tok * a.sb.token];
+            if (DELTA || a.g) x.g = a.g[x.u.b * a.sg.batch + x.h * a.sg.head + x.tok * a.sg.token];
+            if constexpr (DELTA) x.beta = a.beta[x.u.b * a.sb.batch + x.h * a.sb.head + x.tok * a.sb.token];
         }
         return x;
     };
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_c
         const int slot = i % F::slots, n = item / a.Hv, h = item - n * a.Hv;
         const int next = item + F::slots * gridDim.x;
         const Run u = run_of(a, n);
-        const Head<K, V, IO> head(a, s, u, n, h, h / a.G, 0, tid, bar, true);
+        const Head<K, V, IO, DELTA> head(a, s, u, n, h, h / a.G, 0, tid, bar, true);
         const bool live = u.valid && u.slot >= 0 && u.slot < a.n_slots;
         int m = 0;
         bool more = false, bad = false;
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_c
             if (issued[j]) mbar_drain(full + 8 * j, (issued[j] - 1) & 1);
 }
 
-template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
+template <int K, typename IO, bool DELTA> cudaError_t launch(const DecodeArgs &a, cudaStream_t st) {
     const int64_t heads = (int64_t)a.n_seqs * a.Hv;
     // rows that a bulk copy, or 16-byte ones, can take: multiples of 16 bytes apart
     const int64_t strides = a.sk.batch | a.sk.token | a.sk.head | a.sv.batch | a.sv.token | a.sv.head |
@@ -456,18 +461,22 @@ template <int K, typename IO> cudaError_t launch(const DecodeArgs &a, cudaStream
     if constexpr (K == 128)
         if (a.token_indices && a.V == kGroup && heads >= 12 * kSMs && rows16) {
             static std::atomic<uint64_t> done{0};
-            const cudaError_t e = allow_smem(k_recurrent_flow<IO>, Flow<IO>::bytes, done);
+            const cudaError_t e = allow_smem(k_recurrent_flow<IO, DELTA>, Flow<IO>::bytes, done);
             if (e != cudaSuccess) return e;
-            return launch_behind(k_recurrent_flow<IO>, dim3(kSMs), 2 * kGroup, Flow<IO>::bytes, st, a, (int)heads);
+            return launch_behind(k_recurrent_flow<IO, DELTA>, dim3(kSMs), 2 * kGroup, Flow<IO>::bytes, st, a, (int)heads);
         }
-    return launch_behind(k_recurrent<K, IO>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)(a.G * (a.V / kTile))), kTile, 0, st, a, rows16);
+    return launch_behind(k_recurrent<K, IO, DELTA>, dim3((unsigned)a.n_seqs, (unsigned)a.Hq, (unsigned)(a.G * (a.V / kTile))), kTile, 0, st, a, rows16);
 }
 
 }  // namespace
 
 cudaError_t launch_recurrent(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st) {
-    if (io == GDN_BF16) return K == 128 ? launch<128, __nv_bfloat16>(a, st) : launch<64, __nv_bfloat16>(a, st);
-    return K == 128 ? launch<128, float>(a, st) : launch<64, float>(a, st);
+    if (io == GDN_BF16) return K == 128 ? launch<128, __nv_bfloat16, true>(a, st) : launch<64, __nv_bfloat16, true>(a, st);
+    return K == 128 ? launch<128, float, true>(a, st) : launch<64, float, true>(a, st);
+}
+cudaError_t launch_linear_recurrent(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st) {
+    if (io == GDN_BF16) return K == 128 ? launch<128, __nv_bfloat16, false>(a, st) : launch<64, __nv_bfloat16, false>(a, st);
+    return K == 128 ? launch<128, float, false>(a, st) : launch<64, float, false>(a, st);
 }
 
 }  // namespace gdn

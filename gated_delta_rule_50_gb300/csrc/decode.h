@@ -58,6 +58,7 @@ cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int block, size_
 }
 
 cudaError_t launch_recurrent(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st);
+cudaError_t launch_linear_recurrent(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st);  // without beta; g may be null
 cudaError_t launch_tree(const DecodeArgs &a, int K, gdn_dtype io, cudaStream_t st);
 
 cudaError_t launch_tree_tc(const DecodeArgs &a, int K, cudaStream_t st);  // bf16 io
@@ -76,6 +77,21 @@ struct BeamArgs {
 };
 int beam_chunk(int64_t rows, int64_t vocab, int64_t n, gdn_dtype io);
 cudaError_t launch_beam(const BeamArgs &a, gdn_dtype io, cudaStream_t st);
+
+struct SampleArgs {
+    const void *logits;
+    const float *u;
+    const uint8_t *mask;
+    int64_t logits_row, mask_row;
+    int B, vocab;
+    const float *temperatures, *top_ps, *min_ps;  // nullptr: the one number for all rows
+    const int32_t *top_ks;
+    float temperature, top_p, min_p;
+    int top_k;
+    int32_t *tokens;
+    float *logprobs;
+};
+cudaError_t launch_sample(const SampleArgs &a, gdn_dtype io, cudaStream_t st);
 
 constexpr int kMaxViews = 32;
 struct ReorderArgs {

@@ -17,7 +17,7 @@ bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t
 gdn_status launched(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 gdn_status decode_args(const gdn_decode_problem *p, const void *q, const void *k, const void *v, const float *g,
-                       const float *beta, const float *state, void *o, DecodeArgs *a) {
+                       const float *beta, const float *state, void *o, DecodeArgs *a, bool delta = true) {
     if (!p) return GDN_ERR_INVALID_ARG;
     if (p->B < 0 || p->T < 0 || p->Hq < 1 || p->Hv < 1 || p->K < 1 || p->V < 1 || p->Hv % p->Hq)
         return GDN_ERR_INVALID_ARG;
@@ -34,7 +34,7 @@ gdn_status decode_args(const gdn_decode_problem *p, const void *q, const void *k
     const bool none = p->n_seqs == 0;  // nothing will be read
     const bool tokens = p->B > 0 && p->T > 0;
     const unsigned elem = p->io_dtype == GDN_BF16 ? 2 : 4;
-    if (!none && tokens && (!k || !v || !g || !beta)) return GDN_ERR_INVALID_ARG;
+    if (!none && tokens && (!k || !v || (delta && (!g || !beta)))) return GDN_ERR_INVALID_ARG;
     if (!none && p->n_slots > 0 && !state) return GDN_ERR_INVALID_ARG;
     if (!aligned(q, elem) || !aligned(k, elem) || !aligned(v, elem) || !aligned(o, 16) || !aligned(g, 4) ||
         !aligned(beta, 4) || !aligned(state, 16) || !aligned(p->state_indices, 4) || !aligned(p->cu_seqlens, 4) ||
@@ -76,14 +76,10 @@ size_t beam_layout(const BeamArgs &a, size_t *stats, size_t *keys) {
     return c.off;
 }
 
-}  // namespace
-
-extern "C" {
-
-gdn_status gdn_recurrent(const gdn_decode_problem *p, const void *q, const void *k, const void *v, const float *g,
-                         const float *beta, float *state, float *out_state, void *o, gdn_stream_t stream) {
+gdn_status recurrent(const gdn_decode_problem *p, const void *q, const void *k, const void *v, const float *g,
+                     const float *beta, float *state, float *out_state, void *o, bool delta, gdn_stream_t stream) {
     DecodeArgs a;
-    const gdn_status s = decode_args(p, q, k, v, g, beta, state, o, &a);
+    const gdn_status s = decode_args(p, q, k, v, g, beta, state, o, &a, delta);
     if (s != GDN_OK) return s;
     const bool out = (p->token_indices ? p->n_seqs * p->n_steps : p->B * p->T) > 0;
     if (out && p->B * p->T > 0 && !q != !o) return GDN_ERR_INVALID_ARG;
@@ -97,8 +93,25 @@ gdn_status gdn_recurrent(const gdn_decode_problem *p, const void *q, const void 
     a.out_state = out_state;
     if (p->n_seqs == 0) return GDN_OK;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    ProfScope scope("recurrent", st);
-    return launched(launch_recurrent(a, (int)p->K, p->io_dtype, st));
+    ProfScope scope(delta ? "recurrent" : "linear_recurrent", st);
+    return launched((delta ? launch_recurrent : launch_linear_recurrent)(a, (int)p->K, p->io_dtype, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_recurrent(const gdn_decode_problem *p, const void *q, const void *k, const void *v, const float *g,
+                         const float *beta, float *state, float *out_state, void *o, gdn_stream_t stream) {
+    return recurrent(p, q, k, v, g, beta, state, out_state, o, true, stream);
+}
+
+gdn_status gdn_linear_recurrent(const gdn_decode_problem *p, const void *q, const void *k, const void *v, const float *g,
+                                float *state, float *out_state, void *o, gdn_stream_t stream) {
+    if (!p) return GDN_ERR_INVALID_ARG;
+    gdn_decode_problem d = *p;  // one g per head
+    d.g = {0, 0, 1};
+    return recurrent(&d, q, k, v, g, nullptr, state, out_state, o, false, stream);
 }
 
 gdn_status gdn_tree(const gdn_decode_problem *p, const void *q, const void *k, const void *v, const float *g,
@@ -146,6 +159,29 @@ gdn_status gdn_beam_search(const gdn_beam_problem *p, const void *logits, const 
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     ProfScope scope("beam_search", st);
     return launched(launch_beam(a, p->logits_dtype, st));
+}
+
+gdn_status gdn_sample(const gdn_sample_problem *p, const void *logits, const float *u, const uint8_t *mask, int32_t *tokens,
+                      float *logprobs, gdn_stream_t stream) {
+    if (!p || p->B < 0 || p->vocab < 1) return GDN_ERR_INVALID_ARG;
+    if (p->logits_dtype != GDN_F32 && p->logits_dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+    if (p->vocab > GDN_SAMPLE_VOCAB_MAX || p->B > (1 << 20)) return GDN_ERR_UNSUPPORTED;
+    if (p->B == 0) return GDN_OK;
+    if (!logits || !u || !tokens) return GDN_ERR_INVALID_ARG;
+    if (!aligned(logits, p->logits_dtype == GDN_BF16 ? 2 : 4) || !aligned(u, 4) || !aligned(tokens, 4) ||
+        !aligned(logprobs, 4) || !aligned(p->temperatures, 4) || !aligned(p->top_ps, 4) || !aligned(p->min_ps, 4) ||
+        !aligned(p->top_ks, 4))
+        return GDN_ERR_INVALID_ARG;
+    SampleArgs a;
+    a.logits = logits, a.u = u, a.mask = mask;
+    a.logits_row = p->logits_row, a.mask_row = p->mask_row;
+    a.B = (int)p->B, a.vocab = (int)p->vocab;
+    a.temperatures = p->temperatures, a.top_ps = p->top_ps, a.min_ps = p->min_ps, a.top_ks = p->top_ks;
+    a.temperature = p->temperature, a.top_p = p->top_p, a.min_p = p->min_p, a.top_k = p->top_k;
+    a.tokens = tokens, a.logprobs = logprobs;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    ProfScope scope("sample", st);
+    return launched(launch_sample(a, p->logits_dtype, st));
 }
 
 gdn_status gdn_reorder_states(const gdn_state_view *views, int64_t n_views, int64_t n_slots, int64_t B, int64_t W,

@@ -1,4 +1,4 @@
-"""Decoding with the gated delta rule: the calls that follow a prefill.
+"""Decoding with the gated delta rule and with linear attention: the calls that follow a prefill.
 
 ``chunk_gated_delta_rule(..., output_final_state=True)`` leaves one state per sequence; kept in a pool
 ``[slots, Hv, K, V]`` (fp32), it is moved on and read by
@@ -7,12 +7,15 @@
     o = tree_gated_delta_rule(q, k, v, g, beta, parents, state, ...)             # drafted tokens, state kept
     scores, tokens, parents = beam_search_step(logits, scores, ...)              # one selection
     reorder_states(states, parents, ...)                                         # the states follow it
+    tokens, logprobs = sample_tokens(logits, random, ...)                        # or one token drawn per row
+
+``recurrent_linear_attention`` is the step for states that ``chunk_linear_attention`` left.
 
 The calls go through an extension module (``csrc/binding.cpp``) onto the decoding entry points of
 ``include/gdn.h``, which also says what happens to indices that are out of range (whatever integers hold them: they
 are read as int32, and what does not fit stays out of range).  Nothing here synchronises or copies to the host, so
 the calls can be captured in a CUDA graph.  There is no CPU path and no derivative: training runs through
-``chunk_gated_delta_rule``, and inputs that require a gradient or carry a tangent are refused (under
+``chunk_gated_delta_rule`` and ``chunk_linear_attention``, and inputs that require a gradient or carry a tangent are refused (under
 ``torch.no_grad()`` the former are taken).
 """
 from __future__ import annotations
@@ -28,7 +31,7 @@ from . import GdnError, load_library
 from . import build as _build
 
 __all__ = ["recurrent_gated_delta_rule", "tree_gated_delta_rule", "beam_search_step", "reorder_states",
-           "load_binding", "TREE_MAX", "BEAM_MAX"]
+           "recurrent_linear_attention", "sample_tokens", "load_binding", "TREE_MAX", "BEAM_MAX"]
 
 TREE_MAX = 64
 BEAM_MAX = 64
@@ -78,6 +81,21 @@ def recurrent_gated_delta_rule(q: Optional[torch.Tensor], k: torch.Tensor, v: to
                                                  out_state)
 
 
+def recurrent_linear_attention(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, g: Optional[torch.Tensor],
+                               state: torch.Tensor, scale: Optional[float] = None,
+                               state_indices: Optional[torch.Tensor] = None,
+                               cu_seqlens: Optional[torch.Tensor] = None,
+                               token_indices: Optional[torch.Tensor] = None,
+                               out_state: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """New tokens of every sequence through linear attention, S <- e^g S + k v^T and o = scale S^T q; ``state`` is
+    updated in place.
+
+    g [Hv]: the logarithm of each head's decay (None: no decay).  Everything else as in recurrent_gated_delta_rule.
+    """
+    return (_native or load_binding()).linear_recurrent(q, k, v, g, None, state, scale, state_indices, cu_seqlens,
+                                                        token_indices, out_state)
+
+
 def tree_gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
                           parents: torch.Tensor, state: torch.Tensor, scale: Optional[float] = None,
                           state_indices: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -104,6 +122,25 @@ def beam_search_step(logits: torch.Tensor, scores: torch.Tensor, finished: Optio
     j % W.
     """
     return (_native or load_binding()).beam(logits, scores, finished, mask, num_candidates, workspace)
+
+
+def sample_tokens(logits: torch.Tensor, random: torch.Tensor, temperature: Union[float, torch.Tensor] = 1.0,
+                  top_k: Union[int, torch.Tensor, None] = None, top_p: Union[float, torch.Tensor, None] = None,
+                  min_p: Union[float, torch.Tensor, None] = None, mask: Optional[torch.Tensor] = None):
+    """One token for each row, drawn with a given random number: (tokens int32 [B], logprobs fp32 [B]).
+
+    logits [B,vocab] (bf16 or fp32, the vocabulary contiguous); random [B] fp32 in [0, 1); temperature, top_k, top_p and
+    min_p are numbers or tensors [B], one for each row; mask bool, broadcastable to logits: False forbids a token,
+    whatever its logit holds.
+
+    Of the allowed tokens, best first and equal ones by the lower token, the ``top_k`` first are kept (0 or below: all);
+    of these, with shares softmax(logits / temperature), the fewest whose shares sum to ``top_p`` at least (1 or above:
+    all); of these those with ``min_p`` times the best one's share at least.  What is left is run through in the order
+    of the vocabulary: the token is the first where the running sum of shares exceeds ``random`` times their sum, its
+    logprob the logarithm of its part in that sum.  temperature 0: the best token, logprob 0.  A row without a choice
+    (nothing allowed, a NaN or +inf among what is, a parameter that is none) has the token -1 and the logprob -inf.
+    """
+    return (_native or load_binding()).sample(logits, random, temperature, top_k, top_p, min_p, mask)
 
 
 def reorder_states(states: Union[torch.Tensor, Sequence[torch.Tensor]], parents: torch.Tensor,

@@ -402,6 +402,92 @@ gdn_status gdn_reorder_states(const gdn_state_view *views, int64_t n_views, int6
                               const int32_t *parents, const int32_t *state_indices, gdn_stream_t stream);
 
 /*
+ * gdn_linear_recurrent: the same calls for linear attention,
+ *     S_t = exp(g_h) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,
+ * whose decay is a constant of the head: g [Hv] fp32 (NULL: 0).  p->g and
+ * p->beta are not read; everything else is as for gdn_recurrent.
+ */
+gdn_status gdn_linear_recurrent(const gdn_decode_problem *p, const void *q, const void *k, const void *v,
+                                const float *g, float *state, float *out_state, void *o, gdn_stream_t stream);
+
+/*
+ * One token for each row of logits, drawn with a given random number.  Of a
+ * row's allowed logits x (mask byte not 0, not -inf), best first and equal
+ * ones by the lower token, the top_k first are kept; of these, with shares
+ * e^(x / temperature) / sum, the fewest whose shares reach top_p; of these
+ * those with at least min_p times the best one's share.  Among what is left,
+ * in the order of the vocabulary, the token is the first whose running sum of
+ * shares exceeds u times their sum; the log of its own part in that sum comes
+ * beside it.  temperature 0: the best token, log 0.
+ *   top_k of 0 and below, or above the number of tokens: all of them.  top_p of 1 and
+ *   above, min_p of 0 and below: no limit; top_p of 0 and below: the best one;
+ *   min_p above 1 counts as 1, u outside [0, 1) as the nearest number in it,
+ *   NaN as 0.
+ *   A row without a choice -- no allowed logit, a NaN or +inf among them, a
+ *   temperature below 0, of +inf or NaN, a NaN for top_p or min_p -- has the
+ *   token -1 and the log -inf.
+ * Parameters are given for each row (fp32 or int32 [B] on the device) or, with
+ * a NULL pointer, once for all rows.  Shares are whole numbers of 2^-42 of the
+ * best one's: smaller ones are never drawn, and no sum depends on an order.
+ */
+typedef struct {
+    int64_t B, vocab;                       /* vocab <= GDN_SAMPLE_VOCAB_MAX                     */
+    int64_t logits_row, mask_row;           /* strides in elements and bytes; mask_row 0: shared */
+    gdn_dtype logits_dtype;
+    const float *temperatures, *top_ps, *min_ps;
+    const int32_t *top_ks;
+    float temperature, top_p, min_p;
+    int32_t top_k;
+} gdn_sample_problem;
+#define GDN_SAMPLE_VOCAB_MAX (1 << 20)
+
+/* u [B] fp32, mask bytes (nullable) -> tokens int32 [B], logprobs fp32 [B] (nullable). */
+gdn_status gdn_sample(const gdn_sample_problem *p, const void *logits, const float *u, const uint8_t *mask,
+                      int32_t *tokens, float *logprobs, gdn_stream_t stream);
+
+/*
+ * ---- Linear attention over whole sequences ----
+ *
+ *     S_t = exp(g_h) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ *
+ * with a decay that is a constant of the head, taken by the chunk of GDN_CHUNK
+ * tokens, forward and backward.  Shapes, grouped value heads and sequences are
+ * those of gdn_fwd, but for
+ *   g [Hv] fp32 (NULL: 0), the logarithm of the decay, <= 0 expected; it has
+ *     no gradient;
+ *   q, k, v, d_o with strides of their own (in elements, each row of K or V values
+ *     contiguous); o, dq, dk, dv are contiguous;
+ *   offsets that are read on the device alone, so that nothing is needed of
+ *     them on the host: a sequence whose offsets fall or leave the T tokens counts as empty.
+ *     Rows of the outputs that no sequence claims become 0.
+ * Neither call synchronises or allocates; both can be captured in a graph.
+ * The sequences are split over the GPU where they are few, and joined exactly.
+ * bf16: the tensor cores' kernels; fp32: the CUDA cores'.  A token that is not
+ * finite reaches those of its own chunk before it, and all that follow it in its
+ * sequence, none of another sequence.
+ */
+typedef struct {
+    int64_t B, T, Hq, Hv, K, V;    /* K, V in {64, 128}; Hv % Hq == 0; Hv <= 16383; B T < 2^31  */
+    int64_t n_seqs;                /* = B, or number of sequences when varlen                   */
+    const int32_t *cu_seqlens;     /* device [n_seqs + 1] or NULL; requires B == 1              */
+    gdn_dtype io_dtype;
+    float scale;
+    gdn_strides q, k, v, d_o;
+} gdn_linear_problem;
+
+size_t gdn_linear_fwd_workspace_bytes(const gdn_linear_problem *p);
+size_t gdn_linear_bwd_workspace_bytes(const gdn_linear_problem *p);
+/* h0 (nullable), final_state (nullable) [n_seqs, Hv, K, V] fp32. */
+gdn_status gdn_linear_fwd(const gdn_linear_problem *p, const void *q, const void *k, const void *v, const float *g,
+                          const float *h0, void *o, float *final_state, void *workspace, size_t workspace_bytes,
+                          gdn_stream_t stream);
+/* From d_o and dht (nullable: 0): dq, dk, dv in the io type, each nullable where it is not wanted, and dh0
+ * (nullable). */
+gdn_status gdn_linear_bwd(const gdn_linear_problem *p, const void *q, const void *k, const void *v, const float *g,
+                          const float *h0, const void *d_o, const float *dht, void *dq, void *dk, void *dv,
+                          float *dh0, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
  * Test aid for the bounded device-side waits (process-wide; set it only while
  * no other thread calls the library).  Problems planned after this call use
  * wait_ns as the limit of every mbarrier wait of the forward's state-chain
