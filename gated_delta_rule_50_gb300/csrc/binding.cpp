@@ -404,7 +404,7 @@ struct Linear {
         shaped(k, "k", q.sizes(), dev);
         shaped(v, "v", {p.B, p.T, p.Hv, p.V}, dev);
         if (k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type()) type_error("q, k and v must have one dtype");
-        q = inner_contiguous(q), k = inner_contiguous(k), v = inner_contiguous(v);
+        q = mappable(q), k = mappable(k), v = mappable(v);
         p.q = strides_of(q), p.k = strides_of(k), p.v = strides_of(v);
         if (g.defined()) {
             shaped(g, "g", {p.Hv}, dev);
@@ -423,6 +423,15 @@ struct Linear {
             p.cu_seqlens = ptr<int32_t>(cu);
         }
         h0 = state(h0, "initial_state");
+    }
+    // As it is where the tensor cores' kernel can take it (rows on 16-byte boundaries, none shared), else a copy
+    static Tensor mappable(const Tensor &t) {
+        bool ok = t.stride(3) == 1;
+        if (t.scalar_type() == at::kBFloat16) {
+            ok = ok && (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15) == 0;
+            for (int d = 0; d < 3; ++d) ok = ok && (t.size(d) <= 1 || (t.stride(d) > 0 && t.stride(d) % 8 == 0));
+        }
+        return ok ? t : t.clone(at::MemoryFormat::Contiguous);
     }
     Tensor state(const Tensor &t, const char *name) const {
         if (!t.defined()) return t;
@@ -466,7 +475,7 @@ PyObject *linear_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
         Tensor d_o = tensor(a[7], "do");
         shaped(d_o, "do", {x.p.B, x.p.T, x.p.Hv, x.p.V}, x.dev);
         if (d_o.scalar_type() != x.q.scalar_type()) type_error("do must have the dtype of q, k and v");
-        d_o = inner_contiguous(d_o);
+        d_o = Linear::mappable(d_o);
         x.p.d_o = strides_of(d_o);
         const Tensor dht = x.state(optional(a[8], "dht"), "dht");
         below_autograd({&d_o, &dht});

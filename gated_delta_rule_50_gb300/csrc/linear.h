@@ -59,6 +59,9 @@ __device__ __forceinline__ LinearSpan linear_span(const LinearRun &r, int s) {
     return x;
 }
 
+// The tensor cores' kernel: bf16, rows on 16-byte boundaries.  What it does not take, the CUDA cores' does
+bool linear_tc_supported(const LinearRun &r, gdn_dtype io);
+cudaError_t launch_linear_tc(const LinearRun &r, cudaStream_t st);
 cudaError_t launch_linear_simt(const LinearRun &r, gdn_dtype io, cudaStream_t st);
 cudaError_t launch_linear_join(const LinearRun &r, cudaStream_t st);
 // out[tokens][heads][d] (io type) = sum over each group of x[tokens][heads G][d] (fp32)

@@ -38,17 +38,16 @@ int segments(const gdn_linear_problem *p) {
 }
 
 struct Layout {
-    size_t err, seg, partial, bytes;
+    size_t seg, partial, bytes;
     int n_seg;
 };
 Layout layout(const gdn_linear_problem *p, bool backward) {
     Layout l;
     Carve c;
     l.n_seg = segments(p);
-    l.err = c.take<uint32_t>(64);
     l.seg = c.take<float>(l.n_seg > 1 ? (size_t)(p->n_seqs * p->Hv * l.n_seg * p->K * p->V) : 0);
     l.partial = c.take<float>(backward && p->Hv != p->Hq ? (size_t)(p->B * p->T * p->Hv * p->K) : 0);
-    l.bytes = c.off;
+    l.bytes = c.off ? c.off : 256;
     return l;
 }
 
@@ -58,7 +57,7 @@ cudaError_t run(LinearRun r, const gdn_linear_problem *p, const Layout &l, unsig
     auto launch = [&](int mode) {
         r.mode = mode;
         ProfScope scope(mode == LIN_SEG ? "linear_segments" : "linear", st);
-        return launch_linear_simt(r, p->io_dtype, st);
+        return linear_tc_supported(r, p->io_dtype) ? launch_linear_tc(r, st) : launch_linear_simt(r, p->io_dtype, st);
     };
     if (r.n_seg == 1) return launch(LIN_WHOLE);
     cudaError_t e = launch(LIN_SEG);
@@ -95,7 +94,6 @@ gdn_status gdn_linear_fwd(const gdn_linear_problem *p, const void *q, const void
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.bytes) return GDN_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(ws + l.err, 0, 256, st) != cudaSuccess) return GDN_ERR_CUDA;
     if (p->cu_seqlens && tokens &&
         launch_unclaimed(o, (int)p->T, p->Hv * p->V * elem, p->cu_seqlens, (int)p->n_seqs, st) != cudaSuccess)
         return GDN_ERR_CUDA;
@@ -124,7 +122,6 @@ gdn_status gdn_linear_bwd(const gdn_linear_problem *p, const void *q, const void
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.bytes) return GDN_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(ws + l.err, 0, 256, st) != cudaSuccess) return GDN_ERR_CUDA;
     const int G = (int)(p->Hv / p->Hq);
     const int64_t rows = p->B * p->T;
     float *partial = reinterpret_cast<float *>(ws + l.partial);
