@@ -19,10 +19,10 @@
 // Tokens past the end of a sequence in its last chunk belong to its neighbour, and may hold anything: the producer clears
 // them in shared memory before anyone reads them.
 //
-// Roles (512 threads): warps 0 and 1 make P~, warp 2 loads (TMA, three stages), warp 3 issues the products, warps 4 .. 11
-// keep the state, warps 12 .. 15 make w c and write out.  Per chunk the tensor cores are asked for, in this order,
+// Roles (384 threads): warps 0 and 1 make P~, warp 2 loads (TMA, three stages), warp 3 issues the products, warps 4 .. 11
+// keep the state, make w c and write out.  Per chunk the tensor cores are asked for, in this order,
 //     U(j), I(j), O(j), P(j + 1)
-// so that the state's conversion runs under the products of the chunk before and the next one's w c under I, O and P.
+// and the eight warps follow them: w c and U while I(j - 1) and O(j - 1) run, X and out while P(j) and U(j) do.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -36,25 +36,24 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 512, kStages = 3;
-constexpr int W_TMA = 2, W_MMA = 3, W_STATE0 = 4, W_AUX0 = 12;  // warps 0 and 1: P~
-constexpr uint32_t kStateWarps = 8, kAuxWarps = 4;
+constexpr int kThreads = 384, kStages = 3;
+constexpr int W_TMA = 2, W_MMA = 3, W_MAIN0 = 4;  // warps 0 and 1: P~
+constexpr uint32_t kMainWarps = 8;
 
 // shared memory (bytes from a 1024-aligned base)
 constexpr uint32_t STAGE = 49152, BOX = 8192;  // a stage: {a, b} of columns 0 .. 63, {a, b} of 64 .. 127, c of both
 constexpr uint32_t B_OFF = BOX, KB = 2 * BOX, C_OFF = 4 * BOX;
 constexpr uint32_t SM_P = kStages * STAGE;   // P~ {hi, lo} [64 r][64 i]
 constexpr uint32_t SM_W3 = SM_P + 2 * BOX;   // third part of (w c)^T [128 y][64 i]
-constexpr uint32_t SM_OUT = SM_W3 + 2 * BOX; // out on its way, 4 KB per warp
-constexpr uint32_t SM_TAB = SM_OUT + kAuxWarps * 4096;
+constexpr uint32_t SM_OUT = SM_W3 + 2 * BOX; // out on its way, 2 KB per warp
+constexpr uint32_t SM_TAB = SM_OUT + kMainWarps * 2048;
 struct Tables {
     float mask[128];               // p_scale l^d, d = r - i in the order of the scan, at 64 + r - i of the tile's rows; 0 for d < 0
     float into[2][64], up[2][64];  // weights of I's and of c's rows; [1]: of the last chunk
 };
 constexpr uint32_t SM_BAR = SM_TAB + (uint32_t)sizeof(Tables);
 enum {
-    FULL0 = 0, EMPTY0 = FULL0 + kStages, TAIL = EMPTY0 + kStages, PDONE, PREADY, WREADY, UDONE, UFREE, XREADY, IDONE, ODONE,
-    OFREE, FINAL, BARRIERS
+    FULL0 = 0, EMPTY0 = FULL0 + kStages, TAIL = EMPTY0 + kStages, PDONE, PREADY, WREADY, UDONE, XREADY, ODONE, FINAL, BARRIERS
 };
 constexpr uint32_t SM_MISC = SM_BAR + 8 * 32;
 constexpr uint32_t SMEM_BYTES = SM_MISC + 64 + 1024;
@@ -69,6 +68,32 @@ struct Maps {
     CUtensorMap a, b, c;
 };
 
+// A try at a wait that may last kHold ns: warps that wait then issue nothing (tries without it end after some 80 cycles, and
+// their loops took a third of all issue slots)
+constexpr uint32_t kHold = 100000;
+__device__ __forceinline__ bool try_for(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kHold)
+        : "memory");
+    return ok != 0;
+}
+// Waits of one thread and of a whole warp, with one answer: false, and *abort set, after WAIT_NS, or once another has given up
+__device__ __forceinline__ bool wait_alone(uint32_t bar, uint32_t parity, volatile int *abort) {
+    if (try_for(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!try_for(bar, parity)) {
+        if (!*abort && global_ns() - t0 < WAIT_NS) continue;
+        *abort = 1;
+        return false;
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(~0u, wait_alone(bar, parity, abort));
+}
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
     uint64_t p;
     asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
@@ -107,6 +132,42 @@ __device__ __forceinline__ uint32_t last_bf16(uint64_t x) {
     halves(x, x0, x1);
     return pack_bf16(x0, x1);
 }
+// Products are issued by one elected thread, unrolled: the compiler then keeps addresses in uniform registers, and an issue
+// takes about 30 cycles (52 by a thread that it cannot tell for one, 65 and 90 in loops; the product itself takes 32 at
+// N = 64).  Descriptors (sdesc_sw128) as their lower words: the upper one is the same for all, groups of eight rows are
+// 1024 bytes apart.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+    return r != 0;
+}
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc(uint32_t addr, uint32_t lbo) { return ((addr & 0x3FFFFu) >> 4) | (lbo >> 4 << 16); }
+template <uint32_t IDESC, bool ADD> __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint32_t b) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "n"((int)ADD), "n"(IDESC), "n"(kDescHigh)
+        : "memory");
+}
+template <uint32_t IDESC, bool ADD> __device__ __forceinline__ void product_ta(uint32_t d, uint32_t a, uint32_t b) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "n"((int)ADD), "n"(IDESC), "n"(kDescHigh)
+        : "memory");
+}
+// Four steps of 16 along the contraction: descriptors advance by ASTEP and BSTEP (16 bytes), A in TMEM by 8 columns
+template <uint32_t IDESC, bool ADD, int ASTEP, int BSTEP> __device__ __forceinline__ void products(uint32_t d, uint32_t a, uint32_t b) {
+    product<IDESC, ADD>(d, a, b);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) product<IDESC, true>(d, a + i * ASTEP, b + i * BSTEP);
+}
+template <uint32_t IDESC, bool ADD, int BSTEP> __device__ __forceinline__ void products_ta(uint32_t d, uint32_t a, uint32_t b) {
+    product_ta<IDESC, ADD>(d, a, b);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) product_ta<IDESC, true>(d, a + 8 * i, b + i * BSTEP);
+}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z, int w) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
@@ -114,7 +175,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-template <int DA, bool F32OUT>
+enum { NO_OUT, BF16_OUT, F32_OUT };
+template <int DA, int OUT, bool THIRD>
 __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant__ Maps maps, const __grid_constant__ LinearRun r) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_align1024(smem_raw);
@@ -126,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
     auto bar = [&](int i) { return sb + SM_BAR + 8u * (uint32_t)i; };
 
     if (threadIdx.x == 0) {
-        const uint32_t w = kStateWarps, x = kAuxWarps;
-        const uint32_t counts[BARRIERS] = {1, 1, 1, 1, 1, 1, 1, 1, 2, x, 1, w, w, 1, 1, x, 1};
+        const uint32_t w = kMainWarps;
+        const uint32_t counts[BARRIERS] = {1, 1, 1, 1, 1, 1, 1, 1, 2, w, 1, w, 1, 1};
         for (int i = 0; i < BARRIERS; ++i) mbar_init(bar(i), counts[i]);
         misc[1] = 0;
         fence_mbar_init();
@@ -142,9 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
     const int64_t unit = (int64_t)seq * r.Hv + h, words = (int64_t)DA * r.dc;
     const float *init = r.init ? r.init + unit * words : nullptr;
     float *fin = r.fin ? r.fin + unit * words : nullptr;
-    bool init_t = r.transposed, fin_t = r.transposed, outs = r.out != nullptr, live = true;
+    constexpr bool outs = OUT != NO_OUT, F32OUT = OUT == F32_OUT;
+    bool init_t = r.transposed, fin_t = r.transposed, live = true;
     if (r.mode == LIN_SEG) {  // the last segment feeds no other
-        live = c1 < span.chunks && c0 < c1, outs = false;
+        live = c1 < span.chunks && c0 < c1;
         init = nullptr, fin = r.seg + (unit * r.n_seg + part) * words, fin_t = false;
     } else {
         if (part > 0) {
@@ -154,7 +217,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
         if (c1 < span.chunks || !live) fin = nullptr;
     }
     const int nck = live ? c1 - c0 : 0, updates = fin ? nck : nck - 1;  // chunks whose part in the state is wanted
-    const bool third = r.fin != nullptr && fin != nullptr;
     const int first = r.cu ? (int)span.first : 0, batch = r.cu ? 0 : seq;
     // chunk j of this CTA: its lowest token in the row, and its tokens
     auto tokens = [&](int j) { return min(C, span.tokens - (c0 + j) * C); };
@@ -194,9 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
         const int ha = h / r.ga, hb = h / r.gb, hc = h / r.gc;
         int issued = 0;
         bool tail = false;
+#pragma unroll 1
         for (int j = 0; j < nck; ++j) {
             const int st = j % kStages;
-            if (j >= kStages && !mbar_wait_warp(bar(EMPTY0 + st), (j / kStages - 1) & 1, abort_flag)) break;
+            if (j >= kStages && !wait_for(bar(EMPTY0 + st), (j / kStages - 1) & 1, abort_flag)) break;
             tail = tokens(j) < C;
             const uint32_t to = tail ? bar(TAIL) : bar(FULL0 + st), at = stage(j);
             if (lane == 0) {
@@ -210,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             }
             issued = j + 1;
             if (tail) {  // the last chunk: clears what is not this sequence's
-                const bool ok = mbar_wait_warp(to, 0, abort_flag);
+                const bool ok = wait_for(to, 0, abort_flag);
                 if (!ok) break;
                 const int n = tokens(j);
                 for (uint32_t x = 0; x < 4 + boxes_c; ++x) {
@@ -231,221 +294,256 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
         }
         __syncwarp();
     } else if (warp == W_MMA) {
-        if (lane == 0 && nck > 0) {
-            auto wait = [&](int id, uint32_t parity) { return mbar_wait(bar(id), parity, abort_flag); };
+        if (nck > 0 && elected()) {
+            const uint32_t tm = tmem;
+            auto wait = [&](int id, uint32_t parity) { return wait_alone(bar(id), parity, abort_flag); };
             auto full = [&](int j) { return wait(FULL0 + j % kStages, (j / kStages) & 1); };
-            auto product_p = [&](int j) {
-                for (int x = 0; x < DA / 64; ++x)
-                    mma_chain<4, 2, 2>(tmem + TM_P, sdesc_sw128(stage(j) + x * KB, 16, 1024),
-                                       sdesc_sw128(stage(j) + x * KB + B_OFF, 16, 1024), ID_N64, x);
+            auto product_p = [&](uint32_t at) {
+                products<ID_N64, false, 2, 2>(tm + TM_P, desc(at, 16), desc(at + B_OFF, 16));
+                if (DA == 128) products<ID_N64, true, 2, 2>(tm + TM_P, desc(at + KB, 16), desc(at + KB + B_OFF, 16));
                 mma_commit(bar(PDONE));
             };
             bool ok = full(0);
             tc_fence_after();
-            if (ok && outs) product_p(0);
+            if (ok && outs) product_p(stage(0));
+#pragma unroll 1
             for (int j = 0; ok && j < nck; ++j) {
                 const uint32_t ph = j & 1, at = stage(j);
                 if (j < updates) {
-                    if (!(ok = wait(WREADY, ph)) || (j > 0 && !(ok = wait(UFREE, (j - 1) & 1)))) break;
+                    if (!(ok = wait(WREADY, ph))) break;
                     tc_fence_after();
                     constexpr uint32_t ID_U = idesc_bf16(128, DA, 0, 1);
-                    const uint64_t b = sdesc_sw128(at + B_OFF, KB, 1024);
-                    for (int x = 0; x < 2; ++x) mma_chain_ta<4, 128>(tmem + TM_U, tmem + (x ? TM_WL : TM_WH), b, ID_U, x);
-                    if (third) mma_chain<4, 2, 128>(tmem + TM_U, sdesc_sw128(sb + SM_W3, 16, 1024), b, ID_U, 1);
+                    const uint32_t b = desc(at + B_OFF, KB);
+                    products_ta<ID_U, false, 128>(tm + TM_U, tm + TM_WH, b);
+                    products_ta<ID_U, true, 128>(tm + TM_U, tm + TM_WL, b);
+                    if (THIRD) products<ID_U, true, 2, 128>(tm + TM_U, desc(sb + SM_W3, 16), b);
                     mma_commit(bar(UDONE));
                 }
                 if (outs) {
-                    if (!(ok = wait(XREADY, ph)) || (j > 0 && !(ok = wait(OFREE, (j - 1) & 1)))) break;
+                    if (!(ok = wait(XREADY, ph))) break;
                     tc_fence_after();
-                    for (int x = 0; x < 2; ++x)
-                        for (int y = 0; y < DA / 64; ++y)
-                            mma_chain_ta<4, 2>(tmem + TM_I, tmem + (x ? TM_XL : TM_XH) + 32 * y, sdesc_sw128(at + y * KB, 16, 1024),
-                                               ID_N64, x | y);
-                    mma_commit(bar(IDONE));
+                    products_ta<ID_N64, false, 2>(tm + TM_I, tm + TM_XH, desc(at, 16));
+                    if (DA == 128) products_ta<ID_N64, true, 2>(tm + TM_I, tm + TM_XH + 32, desc(at + KB, 16));
+                    products_ta<ID_N64, true, 2>(tm + TM_I, tm + TM_XL, desc(at, 16));
+                    if (DA == 128) products_ta<ID_N64, true, 2>(tm + TM_I, tm + TM_XL + 32, desc(at + KB, 16));
                     if (!(ok = wait(PREADY, ph))) break;
                     tc_fence_after();
-                    for (int x = 0; x < 2; ++x)
-                        mma_chain<4, 128, 2>(tmem + TM_O, sdesc_sw128(at + C_OFF, BOX, 1024),
-                                             sdesc_sw128(sb + SM_P + x * BOX, 16, 1024), ID_N64_AMN, x);
+                    products<ID_N64_AMN, false, 128, 2>(tm + TM_O, desc(at + C_OFF, BOX), desc(sb + SM_P, 16));
+                    products<ID_N64_AMN, true, 128, 2>(tm + TM_O, desc(at + C_OFF, BOX), desc(sb + SM_P + BOX, 16));
                     mma_commit(bar(ODONE));
                 }
                 mma_commit(bar(EMPTY0 + j % kStages));
                 if (j + 1 < nck) {
                     if (!(ok = full(j + 1))) break;
                     tc_fence_after();
-                    if (outs) product_p(j + 1);
+                    if (outs) product_p(stage(j + 1));
                 }
             }
             mma_commit(bar(FINAL));  // every product completes before TMEM is released
             mbar_drain(bar(FINAL), 0);
         }
         __syncwarp();
-    } else if (warp >= W_STATE0 && warp < W_AUX0) {
-        // the state: column y of c, half hh of its row
-        const int quarter = warp & 3, y = 32 * quarter + lane, hh = (warp - W_STATE0) >> 2;
-        const bool mine = 32 * quarter < r.dc;
-        constexpr int HALF = DA / 2;
-        const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
-        uint64_t X[HALF / 2];
-#pragma unroll
-        for (int i = 0; i < HALF / 2; ++i) {
-            const int x = HALF * hh + 2 * i;
-            float v0 = 0.f, v1 = 0.f;
-            if (init && live && mine) {
-                v0 = init[init_t ? y * DA + x : x * r.dc + y];
-                v1 = init[init_t ? y * DA + x + 1 : (x + 1) * r.dc + y];
+    } else if (warp >= W_MAIN0) {
+        // column y of c; half hh of the state's row (HALF columns of a) and of the chunk (32 tokens)
+        const int quarter = warp & 3, y = 32 * quarter + lane, hh = (warp - W_MAIN0) >> 2;
+        auto wait = [&](int id, int use) { return wait_for(bar(id), use & 1, abort_flag); };
+        if (32 * quarter >= r.dc) {  // 64 columns: no work for half of the warps, they only come along
+#pragma unroll 1
+            for (int j = 0; j < nck; ++j) {
+                if (j > 0 && !wait(outs ? ODONE : UDONE, j - 1)) break;
+                if (j < updates) mbar_arrive_warp(bar(WREADY));
+                if (outs) mbar_arrive_warp(bar(XREADY));
             }
-            X[i] = pair_of(v0, v1);
-        }
-        bool ok = true;
-        for (int j = 0; j < nck && ok; ++j) {
-            if (outs) {
-                if (j > 0 && !(ok = mbar_wait_warp(bar(IDONE), (j - 1) & 1, abort_flag))) break;
-                tc_fence_after();
-                if (mine) {
-#pragma unroll
-                    for (int q = 0; q < HALF / 16; ++q) {
-                        uint32_t hi[8], lo[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            uint64_t x = X[8 * q + i];
-                            hi[i] = take_bf16(x), lo[i] = last_bf16(x);
-                        }
-                        const uint32_t to = HALF / 2 * hh + 8 * q;
-                        tmem_st8x2(trow + TM_XH + to, hi, trow + TM_XL + to, lo);
-                    }
-                }
-                tc_fence_before();
-                mbar_arrive_warp(bar(XREADY));
-            }
-            if (j >= updates) break;
-            const float l1 = expm1f(g * (float)tokens(j));  // X l^n as X + l1 X: nothing is lost where l is all but 1
-            const uint64_t l2 = pair_of(l1, l1);
-            if (!(ok = mbar_wait_warp(bar(UDONE), j & 1, abort_flag))) break;
-            tc_fence_after();
-            if (mine) {
-#pragma unroll
-                for (int q = 0; q < HALF / 16; ++q) {
-                    uint32_t u[16];
-                    tmem_ld16(trow + TM_U + HALF * hh + 16 * q, u);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint64_t &x = X[8 * q + i];
-                        x = add2(x, fma2(l2, x, pair_of(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))));
-                    }
-                }
-            }
-            tc_fence_before();
-            mbar_arrive_warp(bar(UFREE));
-        }
-        if (fin && mine) {
-            const bool bad = *abort_flag != 0;
+        } else {
+            constexpr int HALF = DA / 2;
+            const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16), t_x = trow + TM_XH + HALF / 2 * hh, t_u = trow + TM_U + HALF * hh,
+                           t_w = trow + TM_WH + 16 * hh, t_io = trow + TM_I + 32 * hh;
+            unsigned char *staged = sm + SM_OUT + 2048 * (warp - W_MAIN0);
+            uint64_t X[HALF / 2];
 #pragma unroll
             for (int i = 0; i < HALF / 2; ++i) {
                 const int x = HALF * hh + 2 * i;
-                float v0, v1;
-                halves(X[i], v0, v1);
-                if (bad) v0 = v1 = __int_as_float(0x7fffffff);
-                fin[fin_t ? y * DA + x : x * r.dc + y] = v0;
-                fin[fin_t ? y * DA + x + 1 : (x + 1) * r.dc + y] = v1;
+                float v0 = 0.f, v1 = 0.f;
+                if (init && live) {
+                    v0 = init[init_t ? y * DA + x : x * r.dc + y];
+                    v1 = init[init_t ? y * DA + x + 1 : (x + 1) * r.dc + y];
+                }
+                X[i] = pair_of(v0, v1);
             }
-        }
-    } else if (warp >= W_AUX0) {
-        // w c, and out: column y of c
-        const int quarter = warp & 3, y = 32 * quarter + lane;
-        const bool mine = 32 * quarter < r.dc;
-        const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16);
-        unsigned char *staged = sm + SM_OUT + 4096 * (warp - W_AUX0);
-        auto write_out = [&](int j) {
-            if (!mbar_wait_warp(bar(ODONE), j & 1, abort_flag)) return false;
-            tc_fence_after();
-            const int n = tokens(j);
-            const float *w = tab.into[n < C ? 1 : 0];
-            const int64_t at = (((int64_t)batch * r.T + token0(j)) * r.Hv + h) * r.dc + 32 * quarter;  // of out
+            // X l^n as X + (l^n - 1) X: nothing is lost where l is all but 1; any chunk but the last has C tokens
+            const float l1_full = expm1f(g * (float)C), l1_last = nck > 0 ? expm1f(g * (float)tokens(nck - 1)) : 0.f;
+            auto update = [&](float l1) {
+                const uint64_t l2 = pair_of(l1, l1);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // 16 tokens
-                uint32_t in[16], o[16];
-                float ww[16];
-                lds16f(w + 16 * q, ww);
-                if (mine) tmem_ld16x2(trow + TM_I + 16 * q, in, trow + TM_O + 16 * q, o);
-                if (q == 3) {
+                for (int q = 0; q < HALF / 32; ++q) {
+                    uint32_t u[32];
+                    tmem_ld32(t_u + 32 * q, u);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        X[16 * q + i] = add2(X[16 * q + i], fma2(l2, X[16 * q + i], pair_of(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))));
+                }
+            };
+            auto store_x = [&] {
+#pragma unroll
+                for (int q = 0; q < HALF / 32; ++q) {
+                    uint32_t xh[16], xl[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        uint64_t x = X[16 * q + i];
+                        xh[i] = take_bf16(x), xl[i] = last_bf16(x);
+                    }
+                    tmem_st16x2(t_x + 16 * q, xh, t_x + (TM_XL - TM_XH) + 16 * q, xl);
+                }
+            };
+            // 32 tokens of out of a chunk, staged as bf16 (or held as fp32), and their way to memory
+            const int64_t row = (int64_t)r.Hv * r.dc;
+            const int64_t low = first + (r.reverse ? (int64_t)span.tokens - (c0 + 1) * C : c0 * C);  // of chunk 0, were it whole
+            const int64_t at0 = ((int64_t)batch * r.T + low + 32 * hh) * row + h * r.dc + 32 * quarter;
+            const int64_t step = r.reverse ? -C * row : C * row;
+            const uint32_t stage_to = smem_u32(staged) + lane * 2;
+            auto write_out = [&](int j) {  // reads I and O, says so, and goes on
+                const bool last = j + 1 == nck;
+                const float *w = tab.into[last ? 1 : 0] + 32 * hh;
+                // in the order of the scan the last chunk is the only short one; in reverse it is cut at its lower end
+                int64_t at = at0 + j * step;
+                int n = 32;
+                if (last) {
+                    n = tokens(j) - 32 * hh;
+                    if (r.reverse) at += (C - tokens(j)) * row;
+                }
+                float *of = static_cast<float *>(r.out) + at + lane;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t in[16], o[16];
+                    float ww[16];
+                    lds16f(w + 16 * q, ww);
+                    tmem_ld16x2(t_io + 16 * q, in, t_io + (TM_O - TM_I) + 16 * q, o);
+                    if (q == 1) {
+                        tc_fence_before();
+                        mbar_arrive_warp(bar(XREADY));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const uint64_t v = fma2(pair_of(ww[i], ww[i + 1]), pair_of(__uint_as_float(in[i]), __uint_as_float(in[i + 1])),
+                                                pair_of(__uint_as_float(o[i]), __uint_as_float(o[i + 1])));
+                        if constexpr (F32OUT) {
+                            float v0, v1;
+                            halves(v, v0, v1);
+                            if (16 * q + i < n) of[(16 * q + i) * row] = v0;
+                            if (16 * q + i + 1 < n) of[(16 * q + i + 1) * row] = v1;
+                        } else {
+                            const uint32_t b = last_bf16(v);
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage_to + (16 * q + i) * 64), "h"((uint16_t)b) : "memory");
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage_to + (16 * q + i + 1) * 64), "h"((uint16_t)(b >> 16)) : "memory");
+                        }
+                    }
+                }
+                if constexpr (!F32OUT) {  // 64-byte pieces of the rows by 16-byte stores
+                    __syncwarp();
+                    __nv_bfloat16 *ob = static_cast<__nv_bfloat16 *>(r.out) + at + (lane >> 2) * row + 8 * (lane & 3);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(staged + i * 512 + lane * 16);
+                        if (8 * i + (lane >> 2) < n) __stcs(reinterpret_cast<uint4 *>(ob + i * 8 * row), x);
+                    }
+                    __syncwarp();
+                }
+            };
+            // w c of a chunk's 32 tokens
+            uint32_t hi[16], lo[16], rest[16];
+            const uint32_t c_at = sb + C_OFF + (uint32_t)(y >> 6) * BOX + 32 * hh * 128 + (uint32_t)(y & 7) * 2;
+            uint32_t c_chunk[8];  // where the column lies in rows 0 .. 7 (mod 8)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c_chunk[i] = (uint32_t)(((y & 63) >> 3) ^ i) << 4;
+            auto make_w = [&](int j) {
+                const uint32_t c = c_at + (uint32_t)(j % kStages) * STAGE;
+                const float *up = tab.up[j + 1 < nck ? 0 : 1] + 32 * hh;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float w[16];
+                    lds16f(up + 16 * q, w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint16_t c0, c1;
+                        const int t = 16 * q + 2 * i;
+                        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(c0) : "r"(c + t * 128 + c_chunk[t & 7]));
+                        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(c1) : "r"(c + (t + 1) * 128 + c_chunk[(t + 1) & 7]));
+                        uint64_t x = mul2(pair_of(__uint_as_float((uint32_t)c0 << 16), __uint_as_float((uint32_t)c1 << 16)), pair_of(w[2 * i], w[2 * i + 1]));
+                        hi[8 * q + i] = take_bf16(x);
+                        if (THIRD) lo[8 * q + i] = take_bf16(x), rest[8 * q + i] = last_bf16(x);
+                        else lo[8 * q + i] = last_bf16(x);
+                    }
+                }
+            };
+            bool ok = true;
+#pragma unroll 1
+            for (int j = 0; j < nck; ++j) {
+                const bool more = j < updates;
+                if (more) {  // before there is room for it
+                    if (!(ok = wait(FULL0 + j % kStages, j / kStages))) break;
+                    make_w(j);
+                }
+                if (j > 0) {
+                    if (!(ok = wait(UDONE, j - 1))) break;
+                    tc_fence_after();
+                }
+                if (more) {
+                    tmem_st16x2(t_w, hi, t_w + (TM_WL - TM_WH), lo);
+                    if (THIRD) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            st_shared_v4(sw128_addr(sb + SM_W3, y, 4 * hh + k), rest[4 * k], rest[4 * k + 1], rest[4 * k + 2], rest[4 * k + 3]);
+                        fence_proxy_async_smem();
+                    }
+                }
+                if (j > 0) update(l1_full);
+                if (more) {
                     tc_fence_before();
-                    mbar_arrive_warp(bar(OFREE));
+                    mbar_arrive_warp(bar(WREADY));
                 }
-                if (!mine) continue;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float v = fmaf(ww[i], __uint_as_float(in[i]), __uint_as_float(o[i]));
-                    if (F32OUT) {
-                        if (16 * q + i < n) static_cast<float *>(r.out)[at + (int64_t)(16 * q + i) * r.Hv * r.dc + lane] = v;
-                    } else {
-                        reinterpret_cast<__nv_bfloat16 *>(staged)[(16 * q + i) * 32 + lane] = __float2bfloat16_rn(v);
-                    }
+                if (!outs) continue;
+                if (j > 0) {
+                    if (!(ok = wait(ODONE, j - 1))) break;
+                    tc_fence_after();
+                }
+                store_x();
+                if (j > 0) {
+                    write_out(j - 1);
+                } else {
+                    tc_fence_before();
+                    mbar_arrive_warp(bar(XREADY));
                 }
             }
-            if (!F32OUT && mine) {
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = 8 * i + (lane >> 2);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(staged + row * 64 + (lane & 3) * 16);
-                    if (row < n)
-                        __stcs(reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(r.out) + at + (int64_t)row * r.Hv * r.dc + 8 * (lane & 3)), v);
-                }
-                __syncwarp();
-            }
-            return true;
-        };
-        bool ok = true;
-        for (int j = 0; j < nck && ok; ++j) {
-            if (j < updates) {
-                if (!(ok = mbar_wait_warp(bar(FULL0 + j % kStages), (j / kStages) & 1, abort_flag))) break;
-                if (j > 0 && !(ok = mbar_wait_warp(bar(UDONE), (j - 1) & 1, abort_flag))) break;
+            if (ok && nck > 0 && updates == nck && (ok = wait(UDONE, nck - 1))) {
                 tc_fence_after();
-                if (mine) {
-                    const unsigned char *c = sm + (j % kStages) * STAGE + C_OFF + (y >> 6) * BOX + (y & 7) * 2;
-                    const float *up = tab.up[tokens(j) < C ? 1 : 0];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {  // 16 tokens
-                        float w[16];
-                        lds16f(up + 16 * q, w);
-                        uint32_t hi[8], lo[8], rest[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float v[2];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int t = 16 * q + 2 * i + k;
-                                v[k] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(
-                                    c + t * 128 + ((((y & 63) >> 3) ^ (t & 7)) << 4)));
-                            }
-                            uint64_t x = mul2(pair_of(v[0], v[1]), pair_of(w[2 * i], w[2 * i + 1]));
-                            hi[i] = take_bf16(x), lo[i] = take_bf16(x), rest[i] = last_bf16(x);
-                        }
-                        tmem_st8x2(trow + TM_WH + 8 * q, hi, trow + TM_WL + 8 * q, lo);
-                        if (third) {
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                st_shared_v4(sw128_addr(sb + SM_W3, y, 2 * q + k), rest[4 * k], rest[4 * k + 1], rest[4 * k + 2],
-                                             rest[4 * k + 3]);
-                        }
-                    }
-                    if (third) fence_proxy_async_smem();
-                }
-                tc_fence_before();
-                mbar_arrive_warp(bar(WREADY));
+                update(l1_last);
             }
-            if (outs && j > 0) ok = write_out(j - 1);
+            if (ok && nck > 0 && outs && wait(ODONE, nck - 1)) {
+                tc_fence_after();
+                write_out(nck - 1);
+            }
+            if (fin) {
+                const bool bad = *abort_flag != 0;
+#pragma unroll
+                for (int i = 0; i < HALF / 2; ++i) {
+                    const int x = HALF * hh + 2 * i;
+                    float v0, v1;
+                    halves(X[i], v0, v1);
+                    if (bad) v0 = v1 = __int_as_float(0x7fffffff);
+                    fin[fin_t ? y * DA + x : x * r.dc + y] = v0;
+                    fin[fin_t ? y * DA + x + 1 : (x + 1) * r.dc + y] = v1;
+                }
+            }
         }
-        if (ok && outs && nck > 0) write_out(nck - 1);
     } else {
         // P~: row y of the chunk.  The products are issued in order, so that with P(j) the one that read P~(j - 1) is done
         const int y = 32 * warp + lane;
         const uint32_t trow = tmem + ((uint32_t)(32 * warp) << 16) + TM_P;
+#pragma unroll 1
         for (int j = 0; outs && j < nck; ++j) {
-            if (!mbar_wait_warp(bar(PDONE), j & 1, abort_flag)) break;
+            if (!wait_for(bar(PDONE), j & 1, abort_flag)) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < 2; ++x) {  // columns 32 x ..
                 if (r.reverse ? x < warp : x > warp) continue;
                 uint32_t p[32];
@@ -473,9 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
     __syncthreads();
     tc_fence_after();
     if (warp == W_MMA) tmem_dealloc(tmem, 512);
-    if (*abort_flag && outs) {  // a wait ran out: all that this CTA answers for shows it
+    if (outs && *abort_flag) {  // a wait ran out: all that this CTA answers for shows it
         const int from = token0(r.reverse ? nck - 1 : 0), n = min(span.tokens - c0 * C, nck * C);
         const float nan = __int_as_float(0x7fffffff);
+#pragma unroll 1
         for (int64_t i = threadIdx.x; i < (int64_t)n * r.dc; i += kThreads) {
             const int64_t at = (((int64_t)batch * r.T + from + i / r.dc) * r.Hv + h) * r.dc + i % r.dc;
             if (F32OUT) static_cast<float *>(r.out)[at] = nan;
@@ -506,17 +605,24 @@ bool make_map(CUtensorMap *m, const void *x, const gdn_strides &s, int d, int he
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DA, bool F32OUT> cudaError_t launch(const Maps &maps, const LinearRun &r, cudaStream_t st) {
+template <int DA, int OUT, bool THIRD> cudaError_t launch(const Maps &maps, const LinearRun &r, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(k_linear_tc<DA, F32OUT>, (int)SMEM_BYTES, done);
+    const cudaError_t e = allow_smem(k_linear_tc<DA, OUT, THIRD>, (int)SMEM_BYTES, done);
     if (e != cudaSuccess) return e;
-    return launch_behind(k_linear_tc<DA, F32OUT>, dim3((unsigned)(r.n_seqs * r.n_seg), (unsigned)r.Hv), kThreads, SMEM_BYTES, st, maps, r);
+    return launch_behind(k_linear_tc<DA, OUT, THIRD>, dim3((unsigned)(r.n_seqs * r.n_seg), (unsigned)r.Hv), kThreads, SMEM_BYTES, st, maps, r);
 }
 
 // A dimension that is stepped over needs a positive stride of a multiple of 16 bytes
 bool mappable(const void *x, const gdn_strides &s, int heads, int64_t T, int64_t B) {
     auto steps = [](int64_t stride, int64_t n) { return n <= 1 || (stride > 0 && stride % 8 == 0 && stride < (int64_t)1 << 38); };
     return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && steps(s.head, heads) && steps(s.token, T) && steps(s.batch, B);
+}
+
+template <int DA> cudaError_t launch(const Maps &maps, const LinearRun &r, int out, cudaStream_t st) {
+    const bool third = r.fin != nullptr;  // segments' states are parts of it
+    if (out == NO_OUT) return third ? launch<DA, NO_OUT, true>(maps, r, st) : launch<DA, NO_OUT, false>(maps, r, st);
+    if (out == BF16_OUT) return third ? launch<DA, BF16_OUT, true>(maps, r, st) : launch<DA, BF16_OUT, false>(maps, r, st);
+    return third ? launch<DA, F32_OUT, true>(maps, r, st) : launch<DA, F32_OUT, false>(maps, r, st);
 }
 
 }  // namespace
@@ -531,8 +637,8 @@ cudaError_t launch_linear_tc(const LinearRun &r, cudaStream_t st) {
     if (!make_map(&maps.a, r.a, r.sa, r.da, r.Hv / r.ga, r.T, r.B) || !make_map(&maps.b, r.b, r.sb, r.da, r.Hv / r.gb, r.T, r.B) ||
         !make_map(&maps.c, r.c, r.sc, r.dc, r.Hv / r.gc, r.T, r.B))
         return cudaErrorInvalidValue;
-    if (r.da == 128) return r.out_f32 ? launch<128, true>(maps, r, st) : launch<128, false>(maps, r, st);
-    return r.out_f32 ? launch<64, true>(maps, r, st) : launch<64, false>(maps, r, st);
+    const int out = r.mode == LIN_SEG || !r.out ? NO_OUT : r.out_f32 ? F32_OUT : BF16_OUT;
+    return r.da == 128 ? launch<128>(maps, r, out, st) : launch<64>(maps, r, out, st);
 }
 
 }  // namespace gdn
