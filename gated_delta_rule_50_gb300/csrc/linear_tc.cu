@@ -19,10 +19,10 @@
 // Tokens past the end of a sequence in its last chunk belong to its neighbour, and may hold anything: the producer clears
 // them in shared memory before anyone reads them.
 //
-// Roles (384 threads): warps 0 and 1 make P~, warp 2 loads (TMA, three stages), warp 3 issues the products, warps 4 .. 11
-// keep the state, make w c and write out.  Per chunk the tensor cores are asked for, in this order,
-//     U(j), I(j), O(j), P(j + 1)
-// and the eight warps follow them: w c and U while I(j - 1) and O(j - 1) run, X and out while P(j) and U(j) do.
+// Roles (512 threads): warps 0 and 1 make P~, warp 2 loads (TMA, three stages), warp 3 issues the products, warps 4 .. 11
+// keep the state and write out, warps 12 .. 15 make w c.  Per chunk the tensor cores are asked for, in this order,
+//     U(j), P(j + 1), I(j), O(j)
+// and the others follow them: w c and U while I(j - 1) and O(j - 1) run, X and out while U(j) and P(j + 1) do, P~(j + 1) until O(j + 1).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -36,16 +36,16 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384, kStages = 3;
-constexpr int W_TMA = 2, W_MMA = 3, W_MAIN0 = 4;  // warps 0 and 1: P~
-constexpr uint32_t kMainWarps = 8;
+constexpr int kThreads = 512, kStages = 3;
+constexpr int W_TMA = 2, W_MMA = 3, W_MAIN0 = 4, W_W0 = 12;  // warps 0 and 1: P~
+constexpr uint32_t kMainWarps = 8, kWWarps = 4;
 
 // shared memory (bytes from a 1024-aligned base)
 constexpr uint32_t STAGE = 49152, BOX = 8192;  // a stage: {a, b} of columns 0 .. 63, {a, b} of 64 .. 127, c of both
 constexpr uint32_t B_OFF = BOX, KB = 2 * BOX, C_OFF = 4 * BOX;
-constexpr uint32_t SM_P = kStages * STAGE;   // P~ {hi, lo} [64 r][64 i]
-constexpr uint32_t SM_W3 = SM_P + 2 * BOX;   // third part of (w c)^T [128 y][64 i]
-constexpr uint32_t SM_OUT = SM_W3 + 2 * BOX; // out on its way, 2 KB per warp
+constexpr uint32_t SM_P = kStages * STAGE;   // P~ {hi, lo} [64 r][64 i], two buffers
+constexpr uint32_t SM_W3 = SM_P + 4 * BOX;   // third part of (w c)^T [128 y][64 i], two buffers
+constexpr uint32_t SM_OUT = SM_W3 + 4 * BOX; // out on its way, 2 KB per warp
 constexpr uint32_t SM_TAB = SM_OUT + kMainWarps * 2048;
 struct Tables {
     float mask[128];               // p_scale l^d, d = r - i in the order of the scan, at 64 + r - i of the tile's rows; 0 for d < 0
@@ -53,7 +53,7 @@ struct Tables {
 };
 constexpr uint32_t SM_BAR = SM_TAB + (uint32_t)sizeof(Tables);
 enum {
-    FULL0 = 0, EMPTY0 = FULL0 + kStages, TAIL = EMPTY0 + kStages, PDONE, PREADY, WREADY, UDONE, XREADY, ODONE, FINAL, BARRIERS
+    FULL0 = 0, EMPTY0 = FULL0 + kStages, TAIL = EMPTY0 + kStages, PDONE, PREAD, PREADY0, PREADY1, WREADY, UDONE, XREADY, IDONE, ODONE, FINAL, BARRIERS
 };
 constexpr uint32_t SM_MISC = SM_BAR + 8 * 32;
 constexpr uint32_t SMEM_BYTES = SM_MISC + 64 + 1024;
@@ -188,8 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
     auto bar = [&](int i) { return sb + SM_BAR + 8u * (uint32_t)i; };
 
     if (threadIdx.x == 0) {
-        const uint32_t w = kMainWarps;
-        const uint32_t counts[BARRIERS] = {1, 1, 1, 1, 1, 1, 1, 1, 2, w, 1, w, 1, 1};
+        // of 64 columns only half of these warps have any
+        const uint32_t x = r.dc == 128 ? kMainWarps : kMainWarps / 2, w = x + (r.dc == 128 ? kWWarps : kWWarps / 2);
+        const uint32_t counts[BARRIERS] = {1, 1, 1, 1, 1, 1, 1, 1, 2, 2, 2, w, 1, x, 1, 1, 1};
         for (int i = 0; i < BARRIERS; ++i) mbar_init(bar(i), counts[i]);
         misc[1] = 0;
         fence_mbar_init();
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             else tab.up[which][i] = i < m ? r.s_scale * power(m - j - r.e) : 0.f;
         }
         // what the order of the scan forbids stays 0: rows 0 .. 31 with columns 32 .. 63, or the reverse
-        for (int i = t; i < 2 * 32 * 4; i += kThreads) {  // half, row, 16 bytes
+        for (int i = t; i < 4 * 32 * 4; i += kThreads) {  // buffer and half, row, 16 bytes
             const int row = (i >> 2 & 31) + (r.reverse ? 32 : 0), chunk = (i & 3) + (r.reverse ? 0 : 4);
             st_shared_v4(sw128_addr(sb + SM_P + (uint32_t)(i >> 7) * BOX, row, chunk), 0, 0, 0, 0);
         }
@@ -316,8 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
                     const uint32_t b = desc(at + B_OFF, KB);
                     products_ta<ID_U, false, 128>(tm + TM_U, tm + TM_WH, b);
                     products_ta<ID_U, true, 128>(tm + TM_U, tm + TM_WL, b);
-                    if (THIRD) products<ID_U, true, 2, 128>(tm + TM_U, desc(sb + SM_W3, 16), b);
+                    if (THIRD) products<ID_U, true, 2, 128>(tm + TM_U, desc(sb + SM_W3 + ph * 2 * BOX, 16), b);
                     mma_commit(bar(UDONE));
+                }
+                if (j + 1 < nck) {
+                    if (!(ok = full(j + 1)) || (outs && !(ok = wait(PREAD, ph)))) break;
+                    tc_fence_after();
+                    if (outs) product_p(stage(j + 1));
                 }
                 if (outs) {
                     if (!(ok = wait(XREADY, ph))) break;
@@ -326,38 +332,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
                     if (DA == 128) products_ta<ID_N64, true, 2>(tm + TM_I, tm + TM_XH + 32, desc(at + KB, 16));
                     products_ta<ID_N64, true, 2>(tm + TM_I, tm + TM_XL, desc(at, 16));
                     if (DA == 128) products_ta<ID_N64, true, 2>(tm + TM_I, tm + TM_XL + 32, desc(at + KB, 16));
-                    if (!(ok = wait(PREADY, ph))) break;
+                    mma_commit(bar(IDONE));
+                    if (!(ok = wait(PREADY0 + ph, (j >> 1) & 1))) break;  // P~(j + 1) may be ready before it is looked for: a barrier for each buffer
                     tc_fence_after();
-                    products<ID_N64_AMN, false, 128, 2>(tm + TM_O, desc(at + C_OFF, BOX), desc(sb + SM_P, 16));
-                    products<ID_N64_AMN, true, 128, 2>(tm + TM_O, desc(at + C_OFF, BOX), desc(sb + SM_P + BOX, 16));
+                    products<ID_N64_AMN, false, 128, 2>(tm + TM_O, desc(at + C_OFF, BOX), desc(sb + SM_P + ph * 2 * BOX, 16));
+                    products<ID_N64_AMN, true, 128, 2>(tm + TM_O, desc(at + C_OFF, BOX), desc(sb + SM_P + ph * 2 * BOX + BOX, 16));
                     mma_commit(bar(ODONE));
                 }
                 mma_commit(bar(EMPTY0 + j % kStages));
-                if (j + 1 < nck) {
-                    if (!(ok = full(j + 1))) break;
-                    tc_fence_after();
-                    if (outs) product_p(stage(j + 1));
-                }
             }
             mma_commit(bar(FINAL));  // every product completes before TMEM is released
             mbar_drain(bar(FINAL), 0);
         }
         __syncwarp();
-    } else if (warp >= W_MAIN0) {
-        // column y of c; half hh of the state's row (HALF columns of a) and of the chunk (32 tokens)
+    } else if (warp >= W_MAIN0 && warp < W_W0) {
+        // column y of c; half hh of the state's row (HALF columns of a) and of out's tokens (32)
         const int quarter = warp & 3, y = 32 * quarter + lane, hh = (warp - W_MAIN0) >> 2;
         auto wait = [&](int id, int use) { return wait_for(bar(id), use & 1, abort_flag); };
-        if (32 * quarter >= r.dc) {  // 64 columns: no work for half of the warps, they only come along
-#pragma unroll 1
-            for (int j = 0; j < nck; ++j) {
-                if (j > 0 && !wait(outs ? ODONE : UDONE, j - 1)) break;
-                if (j < updates) mbar_arrive_warp(bar(WREADY));
-                if (outs) mbar_arrive_warp(bar(XREADY));
-            }
-        } else {
+        if (32 * quarter < r.dc) {
             constexpr int HALF = DA / 2;
             const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16), t_x = trow + TM_XH + HALF / 2 * hh, t_u = trow + TM_U + HALF * hh,
-                           t_w = trow + TM_WH + 16 * hh, t_io = trow + TM_I + 32 * hh;
+                           t_io = trow + TM_I + 32 * hh;
             unsigned char *staged = sm + SM_OUT + 2048 * (warp - W_MAIN0);
             uint64_t X[HALF / 2];
 #pragma unroll
@@ -372,12 +367,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             }
             // X l^n as X + (l^n - 1) X: nothing is lost where l is all but 1; any chunk but the last has C tokens
             const float l1_full = expm1f(g * (float)C), l1_last = nck > 0 ? expm1f(g * (float)tokens(nck - 1)) : 0.f;
-            auto update = [&](float l1) {
+            auto update = [&](float l1, bool say) {  // says that U is read
+
                 const uint64_t l2 = pair_of(l1, l1);
 #pragma unroll
                 for (int q = 0; q < HALF / 32; ++q) {
                     uint32_t u[32];
                     tmem_ld32(t_u + 32 * q, u);
+                    if (q + 1 == HALF / 32 && say) {
+                        tc_fence_before();
+                        mbar_arrive_warp(bar(WREADY));
+                    }
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         X[16 * q + i] = add2(X[16 * q + i], fma2(l2, X[16 * q + i], pair_of(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))));
@@ -449,65 +449,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
                     __syncwarp();
                 }
             };
-            // w c of a chunk's 32 tokens
-            uint32_t hi[16], lo[16], rest[16];
-            const uint32_t c_at = sb + C_OFF + (uint32_t)(y >> 6) * BOX + 32 * hh * 128 + (uint32_t)(y & 7) * 2;
-            uint32_t c_chunk[8];  // where the column lies in rows 0 .. 7 (mod 8)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c_chunk[i] = (uint32_t)(((y & 63) >> 3) ^ i) << 4;
-            auto make_w = [&](int j) {
-                const uint32_t c = c_at + (uint32_t)(j % kStages) * STAGE;
-                const float *up = tab.up[j + 1 < nck ? 0 : 1] + 32 * hh;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float w[16];
-                    lds16f(up + 16 * q, w);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint16_t c0, c1;
-                        const int t = 16 * q + 2 * i;
-                        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(c0) : "r"(c + t * 128 + c_chunk[t & 7]));
-                        asm volatile("ld.shared.b16 %0, [%1];" : "=h"(c1) : "r"(c + (t + 1) * 128 + c_chunk[(t + 1) & 7]));
-                        uint64_t x = mul2(pair_of(__uint_as_float((uint32_t)c0 << 16), __uint_as_float((uint32_t)c1 << 16)), pair_of(w[2 * i], w[2 * i + 1]));
-                        hi[8 * q + i] = take_bf16(x);
-                        if (THIRD) lo[8 * q + i] = take_bf16(x), rest[8 * q + i] = last_bf16(x);
-                        else lo[8 * q + i] = last_bf16(x);
-                    }
-                }
-            };
             bool ok = true;
 #pragma unroll 1
             for (int j = 0; j < nck; ++j) {
-                const bool more = j < updates;
-                if (more) {  // before there is room for it
-                    if (!(ok = wait(FULL0 + j % kStages, j / kStages))) break;
-                    make_w(j);
-                }
                 if (j > 0) {
                     if (!(ok = wait(UDONE, j - 1))) break;
                     tc_fence_after();
-                }
-                if (more) {
-                    tmem_st16x2(t_w, hi, t_w + (TM_WL - TM_WH), lo);
-                    if (THIRD) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            st_shared_v4(sw128_addr(sb + SM_W3, y, 4 * hh + k), rest[4 * k], rest[4 * k + 1], rest[4 * k + 2], rest[4 * k + 3]);
-                        fence_proxy_async_smem();
-                    }
-                }
-                if (j > 0) update(l1_full);
-                if (more) {
-                    tc_fence_before();
+                    update(l1_full, j < updates);
+                } else if (updates > 0) {
                     mbar_arrive_warp(bar(WREADY));
                 }
                 if (!outs) continue;
                 if (j > 0) {
-                    if (!(ok = wait(ODONE, j - 1))) break;
+                    if (!(ok = wait(IDONE, j - 1))) break;
                     tc_fence_after();
                 }
                 store_x();
                 if (j > 0) {
+                    if (!(ok = wait(ODONE, j - 1))) break;
+                    tc_fence_after();
                     write_out(j - 1);
                 } else {
                     tc_fence_before();
@@ -516,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             }
             if (ok && nck > 0 && updates == nck && (ok = wait(UDONE, nck - 1))) {
                 tc_fence_after();
-                update(l1_last);
+                update(l1_last, false);
             }
             if (ok && nck > 0 && outs && wait(ODONE, nck - 1)) {
                 tc_fence_after();
@@ -535,36 +495,87 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
                 }
             }
         }
+    } else if (warp >= W_W0) {
+        // w c: column y of c
+        const int quarter = warp & 3, y = 32 * quarter + lane;
+        const uint32_t t_w = tmem + ((uint32_t)(32 * quarter) << 16) + TM_WH;
+        const uint32_t c_at = sb + C_OFF + (uint32_t)(y >> 6) * BOX + (uint32_t)(y & 7) * 2;
+        uint32_t piece[8];  // where the column lies in rows 0 .. 7 (mod 8)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) piece[i] = (uint32_t)(i * 128) + ((uint32_t)(((y & 63) >> 3) ^ i) << 4);
+#pragma unroll 1
+        for (int j = 0; 32 * quarter < r.dc && j < updates; ++j) {
+            if (!wait_for(bar(FULL0 + j % kStages), (j / kStages) & 1, abort_flag)) break;
+            const uint32_t c = c_at + (uint32_t)(j % kStages) * STAGE, w3 = sb + SM_W3 + (j & 1) * 2 * BOX;
+            const float *up = tab.up[j + 1 < nck ? 0 : 1];
+            uint32_t hi[32], lo[32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // 16 tokens
+                float w[16];
+                uint32_t rest[8];
+                lds16f(up + 16 * q, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint16_t v0, v1;
+                    const int t = 16 * q + 2 * i;
+                    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v0) : "r"(c + (t >> 3) * 1024 + piece[t & 7]));
+                    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v1) : "r"(c + (t >> 3) * 1024 + piece[(t + 1) & 7]));
+                    uint64_t x = mul2(pair_of(__uint_as_float((uint32_t)v0 << 16), __uint_as_float((uint32_t)v1 << 16)), pair_of(w[2 * i], w[2 * i + 1]));
+                    hi[8 * q + i] = take_bf16(x);
+                    if (THIRD) lo[8 * q + i] = take_bf16(x), rest[i] = last_bf16(x);
+                    else lo[8 * q + i] = last_bf16(x);
+                }
+                if (THIRD) {  // into the buffer whose reader, U(j - 2), is done: it was waited for before the last W was stored
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        st_shared_v4(sw128_addr(w3, y, 2 * q + k), rest[4 * k], rest[4 * k + 1], rest[4 * k + 2], rest[4 * k + 3]);
+                }
+            }
+            if (THIRD) fence_proxy_async_smem();
+            if (j > 0 && !wait_for(bar(UDONE), (j - 1) & 1, abort_flag)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                tmem_st16x2(t_w + 16 * k, reinterpret_cast<uint32_t(&)[16]>(hi[16 * k]), t_w + (TM_WL - TM_WH) + 16 * k, reinterpret_cast<uint32_t(&)[16]>(lo[16 * k]));
+            tc_fence_before();
+            mbar_arrive_warp(bar(WREADY));
+        }
     } else {
-        // P~: row y of the chunk.  The products are issued in order, so that with P(j) the one that read P~(j - 1) is done
+        // P~: row y of the chunk, 32 columns that its own row cuts off and, for one of the two warps, 32 before them
         const int y = 32 * warp + lane;
+        const bool two = r.reverse ? warp == 0 : warp == 1;
+        const int other = r.reverse ? 1 : 0;
         const uint32_t trow = tmem + ((uint32_t)(32 * warp) << 16) + TM_P;
+        auto convert = [&](const uint32_t (&p)[32], int x, uint32_t to) {
+            const float *w = tab.mask + 64 + y - 32 * x;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = 8 * q + 2 * i;
+                    uint64_t v = mul2(pair_of(__uint_as_float(p[k]), __uint_as_float(p[k + 1])), pair_of(w[-k], w[-k - 1]));
+                    hi[i] = take_bf16(v), lo[i] = last_bf16(v);
+                }
+                st_shared_v4(sw128_addr(to, y, 4 * x + q), hi[0], hi[1], hi[2], hi[3]);
+                st_shared_v4(sw128_addr(to + BOX, y, 4 * x + q), lo[0], lo[1], lo[2], lo[3]);
+            }
+        };
 #pragma unroll 1
         for (int j = 0; outs && j < nck; ++j) {
             if (!wait_for(bar(PDONE), j & 1, abort_flag)) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int x = 0; x < 2; ++x) {  // columns 32 x ..
-                if (r.reverse ? x < warp : x > warp) continue;
-                uint32_t p[32];
-                tmem_ld32(trow + 32 * x, p);
-                const float *w = tab.mask + 64 + y - 32 * x;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int k = 8 * q + 2 * i;
-                        uint64_t v = mul2(pair_of(__uint_as_float(p[k]), __uint_as_float(p[k + 1])), pair_of(w[-k], w[-k - 1]));
-                        hi[i] = take_bf16(v), lo[i] = last_bf16(v);
-                    }
-                    st_shared_v4(sw128_addr(sb + SM_P, y, 4 * x + q), hi[0], hi[1], hi[2], hi[3]);
-                    st_shared_v4(sw128_addr(sb + SM_P + BOX, y, 4 * x + q), lo[0], lo[1], lo[2], lo[3]);
-                }
-            }
-            fence_proxy_async_smem();
+            uint32_t p0[32], p1[32];
+            tmem_ld32(trow + 32 * warp, p0);
+            if (two) tmem_ld32(trow + 32 * other, p1);
             tc_fence_before();
-            mbar_arrive_warp(bar(PREADY));
+            mbar_arrive_warp(bar(PREAD));
+            // products end in the order of their issue: with P(j), O(j - 2), the buffer's last reader, is done
+            const uint32_t to = sb + SM_P + (j & 1) * 2 * BOX;
+            convert(p0, warp, to);
+            if (two) convert(p1, other, to);
+            fence_proxy_async_smem();
+            mbar_arrive_warp(bar(PREADY0 + (j & 1)));
         }
     }
     tc_fence_before();
