@@ -90,6 +90,7 @@ struct SampleArgs {
     int top_k;
     int32_t *tokens;
     float *logprobs;
+    bool cached;  // a CTA's slice of a row stays in shared memory
 };
 cudaError_t launch_sample(const SampleArgs &a, gdn_dtype io, cudaStream_t st);
 

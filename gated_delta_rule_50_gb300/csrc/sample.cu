@@ -9,14 +9,14 @@
 // rounding leaves, times the constant as a pair), 2^t a table of 64 steps an octave times 1 + e with e in fp32: off by
 // 2^-31 of itself, a border is mistaken about once in 10^9 / (tokens of that size).
 //
-// A cut is found by counting.  Bins of 1/32 octave of t (kBins of them; below the last every w is 0 and a token counts
-// for nothing) get their sums of w, or for top-k their number of tokens; the running sum over them says in which bin the
-// cut lies.  If all up to there fit a list (kList), they are collected and sorted, and the rest of the work is done on
-// the list.  If not, that bin is cut into kSub further ones and what lies in one of those is collected and sorted to find
-// the cut; where even that is too much for the list (many equal logits), the cut is searched for by bisection, over the
-// logit and then over the tokens that share it.
-//
-// The CTAs of a cluster share a row: slices of it, read again in each pass (they come from L2).
+// The CTAs of a cluster share a row; each reads its slice once and keeps it in shared memory, -inf for what the mask
+// forbids.  A cut is found by bins of 1/8 octave of t, whose running sum (of w, or of tokens for top-k) says in which bin
+// it lies.  At first they take the best of every thread's elements alone: what these reach, all reach, so that the true
+// cut lies in that bin or before it, and for all but flat distributions no more than kList tokens do.  Those are collected
+// and sorted, and the rest of the work is done on that list.  Where they are too many, the bins take every element, the
+// cut's bin is cut into kSub further ones, and what lies in one of those is collected and sorted to find the cut; where
+// even that is too much for the list (many equal logits), the cut is searched for by bisection, over the logit and then
+// over the tokens that share it.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -30,9 +30,12 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kOctave = 32, kBins = 44 * kOctave;  // w = 0 from t = -43 on
-constexpr int kSub = 1024;
+constexpr int kOctave = 8, kBins = 44 * kOctave;  // w = 0 from t = -43 on
+constexpr int kSub = kThreads;
 constexpr int kList = 1024;
+constexpr int kSlice = 1 << 17;  // elements of a CTA, at most: then sums of a bin's 15-bit parts stay within 32 bits
+constexpr int kCache = 96 << 10; // bytes of shared memory for the slice; larger ones are read again in every pass
+static_assert(kBins <= kThreads, "a thread per bin");
 constexpr int kShift = 42;
 
 __device__ __forceinline__ uint32_t ordered(float x) {  // larger for larger x; +0 and -0 alike
@@ -70,23 +73,22 @@ __device__ __forceinline__ uint64_t shfl_up64(uint64_t x, int d) { return __shfl
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int d) { return __shfl_xor_sync(~0u, (unsigned long long)x, d); }
 
 struct Shared {
-    uint32_t lo[kBins], hi[kBins];  // sums of w, in two halves
-    uint32_t count[kBins];
+    uint32_t part[3][kSub];  // sums of w by bins, in three parts of 15 bits
+    uint32_t count[kSub];
     uint64_t key[kList], w[kList];
     uint64_t table[65];  // 2^(42 + j / 64), j = -32 .. 32
     uint64_t warp_w[kWarps];
     uint32_t warp_n[kWarps];
     uint64_t best;       // of the CTA's slice
     int bad;
-    Sums part[2];        // what the CTA adds to a sum over the cluster
+    Sums sum[2];         // what the CTA adds to a sum over the cluster
     uint64_t warp_kept[kWarps];
     uint32_t listed;     // entries of the list (the first CTA's)
     uint64_t cut;        // found by the first CTA
     int at_bin;
-    Sums before;         // what lies in the bins before it
+    uint64_t before;     // what lies in the bins before it
     float c_hi, c_lo;
     double min_p;        // temperature ln(min_p)
-    int found;
 };
 
 template <typename IO> struct Sampler {
@@ -95,36 +97,48 @@ template <typename IO> struct Sampler {
     const cg::cluster_group cluster;
     const IO *x;          // the row
     const uint8_t *mask;  // the row's, or nullptr
+    uint4 *cache;         // the slice, or nullptr where it does not fit
     int vocab, v0, v1;    // this CTA's vectors; vector v has the elements VEC v - skew ..
     int skew;             // elements by which the row begins behind a 16-byte boundary
-    bool mask8;           // the mask's bytes of a vector can be read at once
+    bool mask16;          // the mask's bytes of a vector can be read at once
     float m, c_hi, c_lo;
     int turn;
 
-    // f(x, token) for every allowed element of this warp's part of the slice, in ascending vectors by lane
-    template <typename F> __device__ __forceinline__ void vector(int v, F f) const {
+    // Vector v as it lies in memory, -inf in place of what the mask forbids and of what lies outside the row
+    __device__ __forceinline__ uint4 fetch(int v) const {
         const int at = v * VEC - skew;
-        IO e[VEC];
-        uint8_t ok[VEC];
+        uint4 raw;
+        IO *e = reinterpret_cast<IO *>(&raw);
         if (at >= 0 && at + VEC <= vocab) {
-            *reinterpret_cast<uint4 *>(e) = __ldg(reinterpret_cast<const uint4 *>(x + at));
+            raw = __ldg(reinterpret_cast<const uint4 *>(x + at));
             if (mask) {
-                if (mask8) {
+                uint8_t ok[VEC];
+                if (mask16) {
                     if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(ok) = __ldg(reinterpret_cast<const uint2 *>(mask + at));
                     else *reinterpret_cast<uint32_t *>(ok) = __ldg(reinterpret_cast<const uint32_t *>(mask + at));
                 } else {
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) ok[i] = mask[at + i];
                 }
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (!ok[i]) e[i] = from_f<IO>(-INFINITY);
             }
+        } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                if (!mask || ok[i]) f(to_f<IO>(e[i]), at + i);
-        } else {
-            for (int i = 0; i < VEC; ++i)
-                if (at + i >= 0 && at + i < vocab && (!mask || mask[at + i])) f(to_f<IO>(x[at + i]), at + i);
+                e[i] = at + i >= 0 && at + i < vocab && (!mask || mask[at + i]) ? x[at + i] : from_f<IO>(-INFINITY);
         }
+        return raw;
     }
+    // f(x, token) for the elements of a vector; those that are forbidden or outside the row have x = -inf
+    template <typename F> __device__ __forceinline__ void elements(uint4 raw, int v, F f) const {
+        const IO *e = reinterpret_cast<const IO *>(&raw);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f(to_f<IO>(e[i]), v * VEC - skew + i);
+    }
+    template <typename F> __device__ __forceinline__ void vector(int v, F f) const { elements(cache ? cache[v - v0] : fetch(v), v, f); }
+    // Warps have consecutive parts of the slice
     __device__ __forceinline__ void warp_part(int warp, int &a, int &b) const {
         const int each = (v1 - v0 + kWarps - 1) / kWarps;
         a = min(v1, v0 + warp * each), b = min(v1, a + each);
@@ -132,7 +146,39 @@ template <typename IO> struct Sampler {
     template <typename F> __device__ __forceinline__ void each(F f) const {
         int a, b;
         warp_part(threadIdx.x >> 5, a, b);
-        for (int v = a + (threadIdx.x & 31); v < b; v += 32) vector(v, f);
+        a += threadIdx.x & 31;
+        if (cache) {
+#pragma unroll 1
+            for (int v = a; v < b; v += 32) elements(cache[v - v0], v, f);
+        } else {
+#pragma unroll 1
+            for (int v = a; v < b; v += 64) {  // two vectors on their way
+                const uint4 first = fetch(v);
+                uint4 second;
+                if (v + 32 < b) second = fetch(v + 32);
+                elements(first, v, f);
+                if (v + 32 < b) elements(second, v + 32, f);
+            }
+        }
+    }
+    // The first pass: into the cache too
+    template <typename F> __device__ __forceinline__ void each_first(F f) const {
+        int a, b;
+        warp_part(threadIdx.x >> 5, a, b);
+        a += threadIdx.x & 31;
+#pragma unroll 1
+        for (int v = a; v < b; v += 128) {
+            uint4 raw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (v + 32 * i < b) raw[i] = fetch(v + 32 * i);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (v + 32 * i < b) {
+                    if (cache) cache[v + 32 * i - v0] = raw[i];
+                    elements(raw[i], v + 32 * i, f);
+                }
+        }
     }
 
     __device__ __forceinline__ float t_of(float y) const { return (y - m) * c_hi; }
@@ -179,31 +225,34 @@ template <typename IO> struct Sampler {
     // Sums over the cluster, to all threads; two turns' parts are apart, so that one sync serves each
     __device__ __forceinline__ Sums row_sum(Sums a) {
         a = block_sum(a);
-        if (threadIdx.x == 0) s.part[turn] = a;
+        if (threadIdx.x == 0) s.sum[turn] = a;
         cluster.sync();
         Sums all = {0, 0};
-        for (unsigned r = 0; r < cluster.num_blocks(); ++r) all = all + *cluster.map_shared_rank(&s.part[turn], r);
+        for (unsigned r = 0; r < cluster.num_blocks(); ++r) all = all + *cluster.map_shared_rank(&s.sum[turn], r);
         turn ^= 1;
         return all;
     }
 
-    // Where in bins 0 .. n - 1 (over the cluster) the running sum reaches `need` (of w, or of tokens): at_bin (n: nowhere)
-    // and what lies before it.  The bins stay as they are until the next sync.
-    __device__ __forceinline__ void locate(int n, bool by_count, uint64_t need) {
-        const int per = (n + kThreads - 1) / kThreads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        constexpr int MOST = (kBins + kThreads - 1) / kThreads;
-        uint64_t v[MOST];
+    // Where in the bins (over the cluster; a thread for each) the running sum reaches `need`, of w or of tokens: at_bin
+    // (kThreads: nowhere) and what lies before it.  The bins stay as they are until the next sync.
+    __device__ __forceinline__ void locate(bool by_count, uint64_t need) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         uint64_t mine = 0;
+        const unsigned ranks = cluster.num_blocks();
+        if (by_count) {
+            uint32_t n[kMaxCluster];
 #pragma unroll
-        for (int i = 0; i < MOST; ++i) {
-            v[i] = 0;
-            const int bin = threadIdx.x * per + i;
-            if (i < per && bin < n)
-                for (unsigned r = 0; r < cluster.num_blocks(); ++r) {
-                    const Shared *o = cluster.map_shared_rank(&s, r);
-                    v[i] += by_count ? o->count[bin] : ((uint64_t)o->hi[bin] << 32) + o->lo[bin];
-                }
-            mine += v[i];
+            for (unsigned r = 0; r < kMaxCluster; ++r) n[r] = r < ranks ? cluster.map_shared_rank(&s, r)->count[threadIdx.x] : 0;
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r) mine += n[r];
+        } else {
+            uint32_t p[3][kMaxCluster];
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r)
+#pragma unroll
+                for (int i = 0; i < 3; ++i) p[i][r] = r < ranks ? cluster.map_shared_rank(&s, r)->part[i][threadIdx.x] : 0;
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r) mine += ((uint64_t)p[2][r] << 30) + ((uint64_t)p[1][r] << 15) + p[0][r];
         }
         uint64_t run = mine;
 #pragma unroll
@@ -213,32 +262,20 @@ template <typename IO> struct Sampler {
         }
         __syncthreads();
         if (lane == 31) s.warp_w[warp] = run;
-        if (threadIdx.x == 0) s.at_bin = n;
+        if (threadIdx.x == 0) s.at_bin = kThreads;
         __syncthreads();
         for (int i = 0; i < warp; ++i) run += s.warp_w[i];
-        uint64_t before = run - mine;
-        if (before < need && run >= need) {
-#pragma unroll
-            for (int i = 0; i < MOST; ++i) {
-                if (before < need && before + v[i] >= need) s.at_bin = threadIdx.x * per + i, s.before = {before, (uint32_t)before};
-                before += v[i];
-            }
-        }
+        if (run - mine < need && run >= need) s.at_bin = threadIdx.x, s.before = run - mine;
         __syncthreads();
     }
     __device__ __forceinline__ void clear_bins() {
-        for (int i = threadIdx.x; i < kBins; i += kThreads) s.lo[i] = s.hi[i] = s.count[i] = 0;
+        s.count[threadIdx.x] = s.part[0][threadIdx.x] = s.part[1][threadIdx.x] = s.part[2][threadIdx.x] = 0;
         __syncthreads();
     }
-    __device__ __forceinline__ void add(int bin, bool by_count, float y) {
-        if (by_count) {
-            atomicAdd(&s.count[bin], 1u);
-        } else {
-            const uint64_t w = weight(y);
-            const uint32_t low = (uint32_t)w, old = atomicAdd(&s.lo[bin], low);
-            const uint32_t high = (uint32_t)(w >> 32) + (old + low < old ? 1u : 0u);
-            if (high) atomicAdd(&s.hi[bin], high);
-        }
+    __device__ __forceinline__ void add(int bin, uint64_t w) {
+        atomicAdd(&s.part[0][bin], (uint32_t)w & 0x7FFFu);
+        atomicAdd(&s.part[1][bin], (uint32_t)(w >> 15) & 0x7FFFu);
+        if (w >> 30) atomicAdd(&s.part[2][bin], (uint32_t)(w >> 30));
     }
     // Into the first CTA's list
     __device__ __forceinline__ void collect(uint64_t key) {
@@ -246,23 +283,48 @@ template <typename IO> struct Sampler {
         const uint32_t at = atomicAdd(&first->listed, 1u);
         if (at < kList) first->key[at] = key;
     }
-    // Sorts the first n entries of the list (the rest of a power of two filled up): descending keys
-    __device__ __forceinline__ int sort_list(int n) {
+    // Sorts the first n entries of the list: descending keys.  E entries a thread, those of tid + 512 e; partners less than
+    // a warp apart meet by shuffles
+    template <int E> __device__ __forceinline__ void sort_entries(int n, int size) {
+        uint64_t k[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int i = threadIdx.x + e * kThreads;
+            k[e] = i < n ? s.key[i] : 0;
+        }
+        __syncthreads();
+        for (int g = 2; g <= size; g <<= 1)
+            for (int j = g >> 1; j; j >>= 1) {
+                if (E == 2 && j == kThreads) {
+                    if (k[0] < k[E - 1]) {  // the last merge: descending
+                        const uint64_t y = k[0];
+                        k[0] = k[E - 1], k[E - 1] = y;
+                    }
+                    continue;
+                }
+                if (j >= 32) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) s.key[threadIdx.x + e * kThreads] = k[e];
+                    __syncthreads();
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int i = threadIdx.x + e * kThreads;
+                    const uint64_t y = j >= 32 ? s.key[i ^ j] : shfl_xor64(k[e], j);
+                    const bool keep_larger = ((i & g) == 0) == ((i & j) == 0);
+                    k[e] = keep_larger ? max(k[e], y) : min(k[e], y);
+                }
+                if (j >= 32) __syncthreads();
+            }
+#pragma unroll
+        for (int e = 0; e < E; ++e) s.key[threadIdx.x + e * kThreads] = k[e];
+        __syncthreads();
+    }
+    __device__ __forceinline__ void sort_list(int n) {
         int size = 32;
         while (size < n) size <<= 1;
-        for (int i = n + threadIdx.x; i < size; i += kThreads) s.key[i] = 0;
-        __syncthreads();
-        for (int k = 2; k <= size; k <<= 1)
-            for (int j = k >> 1; j; j >>= 1) {
-                for (int i = threadIdx.x; i < size / 2; i += kThreads) {
-                    const int a = (i / j) * 2 * j + i % j, b = a + j;
-                    const bool down = (a & k) == 0;
-                    const uint64_t x0 = s.key[a], x1 = s.key[b];
-                    if ((x0 < x1) == down) s.key[a] = x1, s.key[b] = x0;
-                }
-                __syncthreads();
-            }
-        return size;
+        if (size <= kThreads) sort_entries<1>(n, size);
+        else sort_entries<2>(n, size);
     }
     // w[i] of the list's n entries becomes the running sum of its tokens' shares
     __device__ __forceinline__ void scan_list(int n) {
@@ -305,13 +367,15 @@ template <typename IO> struct Sampler {
         clear_bins();
         if (threadIdx.x == 0) s.listed = 0;
         each([&](float y, int token) {
-            if (bin_of(y) == bin && make_key(y, token) >= floor) add(sub_of(y, bin), by_count, y);
+            if (bin_of(y) != bin || make_key(y, token) < floor) return;
+            if (by_count) atomicAdd(&s.count[sub_of(y, bin)], 1u);
+            else add(sub_of(y, bin), weight(y));
         });
         cluster.sync();
-        locate(kSub, by_count, need);
+        locate(by_count, need);
         const int sub = s.at_bin;
-        if (sub == kSub) return floor;  // all of it
-        need -= s.before.w;
+        if (sub == kThreads) return floor;  // all of it
+        need -= s.before;
         uint32_t n = 0;
         each([&](float y, int token) {
             const uint64_t key = make_key(y, token);
@@ -360,7 +424,8 @@ template <typename IO> struct Sampler {
     }
 };
 
-template <typename IO> __global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ SampleArgs a) {
+template <typename IO> __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ SampleArgs a) {
+    extern __shared__ uint4 sample_cache[];
     __shared__ Shared s;
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -370,10 +435,11 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) k_sample(cons
     z.mask = a.mask ? a.mask + row * a.mask_row : nullptr;
     z.vocab = a.vocab, z.turn = 0;
     z.skew = (int)((reinterpret_cast<uintptr_t>(z.x) & 15) / sizeof(IO));
-    z.mask8 = z.mask && ((reinterpret_cast<uintptr_t>(z.mask) - z.skew) & (Sampler<IO>::VEC - 1)) == 0;
+    z.mask16 = z.mask && ((reinterpret_cast<uintptr_t>(z.mask) - z.skew) & (Sampler<IO>::VEC - 1)) == 0;
     const int vectors = (a.vocab + z.skew + Sampler<IO>::VEC - 1) / Sampler<IO>::VEC;
     const int slice = (vectors + ranks - 1) / ranks;
     z.v0 = min(vectors, rank * slice), z.v1 = min(vectors, z.v0 + slice);
+    z.cache = a.cached ? sample_cache : nullptr;
     wait_for_previous();
     const float heat = a.temperatures ? a.temperatures[row] : a.temperature;
     const int top_k = a.top_ks ? a.top_ks[row] : a.top_k;
@@ -391,21 +457,23 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) k_sample(cons
     if (tid == 64) s.min_p = min_p > 0.f ? (double)heat * log((double)min_p) : 0.;
     if (tid >= 128 && tid < 128 + 65) s.table[tid - 128] = kPowers.of[tid - 128];
     __syncthreads();
-    // the best logit
+    // the best logit, of this thread's elements and of the row
+    float mine = -INFINITY;
     {
         float best = -INFINITY;
         int at = 0;
         bool bad = false;
-        z.each([&](float y, int token) {
+        z.each_first([&](float y, int token) {
             bad |= !(y < INFINITY);
             if (y > best) best = y, at = token;
         });
+        mine = best;
         uint64_t key = best > -INFINITY ? make_key(best, at) : 0;
 #pragma unroll
         for (int d = 16; d; d >>= 1) key = max(key, shfl_xor64(key, d));
         if (lane == 0) s.warp_w[warp] = key;
         if (bad) s.bad = 1;
-        __syncthreads();
+        z.clear_bins();
         if (tid == 0) {
             for (int i = 1; i < kWarps; ++i) key = max(key, s.warp_w[i]);
             s.best = key;
@@ -443,54 +511,54 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) k_sample(cons
     if (min_p > 0.f) cut = (uint64_t)ordered(__double2float_ru((double)z.m + s.min_p)) << 32;
     const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
     if (by_k || by_p) {
-        // bins of what can be drawn: tokens for top-k, else shares
-        z.clear_bins();
-        Sums all = {0, 0};
-        z.each([&](float y, int) {
-            const int bin = z.bin_of(y);
-            if (bin < kBins) z.add(bin, by_k, y);
-            if (!by_k) all.w += z.weight(y);
-        });
         auto share = [&](uint64_t of) { return max((uint64_t)1, (uint64_t)ceil((double)fmaxf(top_p, 0.f) * (double)of)); };
-        if (!by_k) all = z.row_sum(all);
-        else cluster.sync();
-        z.locate(kBins, by_k, by_k ? (uint64_t)top_k : share(all.w));
-        const int bin = s.at_bin;
-        const Sums before = s.before;
-        // do all up to this bin fit the list?
-        Sums listed = {0, 0};
-        z.each([&](float y, int) { listed.n += z.bin_of(y) <= bin; });
-        listed = z.row_sum(listed);
-        if (listed.n <= kList) {
+        Sums all = {0, 0};
+        const int own = z.bin_of(mine);
+        if (by_k) {
+            if (own < kBins) atomicAdd(&s.count[own], 1u);
+            cluster.sync();
+        } else {
+            if (own < kBins) z.add(own, z.weight(mine));
+            z.each([&](float y, int) { all.w += z.weight(y); });
+            all = z.row_sum(all);
+        }
+        z.locate(by_k, by_k ? (uint64_t)top_k : share(all.w));
+        // all up to this bin; where the best ones do not reach so far, there are too many (or the row is no longer than the list)
+        const int reach = min(s.at_bin, kBins);
+        uint32_t n = kList + 1;
+        if (reach < kBins || a.vocab <= kList) {
             z.each([&](float y, int token) {
-                if (z.bin_of(y) <= bin) z.collect(make_key(y, token));
+                if (y > -INFINITY && z.bin_of(y) <= reach) z.collect(make_key(y, token));
             });
             cluster.sync();
+            n = cluster.map_shared_rank(&s, 0)->listed;
+        }
+        if (n <= kList) {
             if (rank == 0) {
-                int n = (int)listed.n;
-                z.sort_list(n);
-                z.scan_list(n);
-                if (by_k) n = min(n, top_k);
-                if (by_p) n = min(n, z.place(n, share(by_k ? s.w[n - 1] : all.w)) + 1);
+                z.sort_list((int)n);
+                z.scan_list((int)n);
+                int kept = by_k ? min((int)n, top_k) : (int)n;
+                if (by_p) kept = min(kept, z.place(kept, share(by_k ? s.w[kept - 1] : all.w)) + 1);
                 {  // min-p: entries before the first below it
-                    int lo = 1, hi = n;
+                    int lo = 1, hi = kept;
                     while (lo < hi) {
                         const int mid = (lo + hi) >> 1;
                         if (s.key[mid] < cut) hi = mid;
                         else lo = mid + 1;
                     }
-                    n = lo;
+                    kept = lo;
                 }
-                const uint64_t total = s.w[n - 1];
+                const uint64_t total = s.w[kept - 1];
                 __syncthreads();
                 // by the tokens' numbers: entries with their halves exchanged
-                for (int i = tid; i < n; i += kThreads) s.key[i] = s.key[i] << 32 | s.key[i] >> 32;
-                z.sort_list(n);
-                for (int i = tid; i < n; i += kThreads) s.key[i] = s.key[i] << 32 | s.key[i] >> 32;
+                for (int i = tid; i < kept; i += kThreads) s.key[i] = s.key[i] << 32 | s.key[i] >> 32;
                 __syncthreads();
-                z.scan_list(n);
+                z.sort_list(kept);
+                for (int i = tid; i < kept; i += kThreads) s.key[i] = s.key[i] << 32 | s.key[i] >> 32;
+                __syncthreads();
+                z.scan_list(kept);
                 if (tid == 0) {
-                    const int i = min(z.place(n, (uint64_t)((double)u * (double)total) + 1), n - 1);
+                    const int i = min(z.place(kept, (uint64_t)((double)u * (double)total) + 1), kept - 1);
                     const float y = unordered((uint32_t)(s.key[i] >> 32));
                     answer((int)key_token(s.key[i]), logprob(y, s.w[i] - (i ? s.w[i - 1] : 0), total));
                 }
@@ -498,23 +566,29 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) k_sample(cons
             cluster.sync();
             return;
         }
+        // every element into the bins; the cut of top-k, then that of top-p behind it
         uint64_t floor = 0;
-        if (by_k && bin < kBins) floor = z.cut_in(bin, true, (uint64_t)top_k - before.w, 0);
-        if (by_p) {
-            if (by_k) {
-                cluster.sync();
-                z.clear_bins();
-                all = {0, 0};
-                z.each([&](float y, int token) {
-                    const int b = z.bin_of(y);
-                    if (b < kBins && make_key(y, token) >= floor) z.add(b, false, y), all.w += z.weight(y);
-                });
-                all = z.row_sum(all);
-                z.locate(kBins, false, share(all.w));
-            }
-            const int at = s.at_bin;
-            const uint64_t need = share(all.w) - s.before.w;
-            if (at < kBins) floor = z.cut_in(at, false, need, floor);
+        for (int filter = by_k ? 0 : 1; filter < (by_p ? 2 : 1); ++filter) {
+            const bool by_count = filter == 0;
+            cluster.sync();
+            z.clear_bins();
+            all = {0, 0};
+            z.each([&](float y, int token) {
+                const int bin = z.bin_of(y);
+                if (bin >= kBins || make_key(y, token) < floor) return;
+                if (by_count) {
+                    atomicAdd(&s.count[bin], 1u);
+                } else {
+                    const uint64_t w = z.weight(y);
+                    z.add(bin, w);
+                    all.w += w;
+                }
+            });
+            all = z.row_sum(all);
+            const uint64_t need = by_count ? (uint64_t)top_k : share(all.w);
+            z.locate(by_count, need);
+            const int bin = s.at_bin;
+            if (bin < kBins) floor = z.cut_in(bin, by_count, need - s.before, floor);
         }
         cut = max(cut, floor);
     }
@@ -524,17 +598,17 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) k_sample(cons
         if (make_key(y, token) >= cut) kept.w += z.weight(y);
     });
     const Sums total = z.row_sum(kept);
-    uint64_t mine = kept.w;
+    uint64_t warp_sum = kept.w;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) mine += shfl_xor64(mine, d);
+    for (int d = 16; d; d >>= 1) warp_sum += shfl_xor64(warp_sum, d);
     uint64_t before = 0;
-    for (int r = 0; r < rank; ++r) before += cluster.map_shared_rank(&s.part[z.turn ^ 1], r)->w;
+    for (int r = 0; r < rank; ++r) before += cluster.map_shared_rank(&s.sum[z.turn ^ 1], r)->w;
     __syncthreads();
-    if (lane == 0) s.warp_kept[warp] = mine;
+    if (lane == 0) s.warp_kept[warp] = warp_sum;
     __syncthreads();
     for (int i = 0; i < warp; ++i) before += s.warp_kept[i];
     const uint64_t need = (uint64_t)((double)u * (double)total.w) + 1;
-    if (before < need && before + mine >= need) {  // one warp of the row
+    if (before < need && before + warp_sum >= need) {  // one warp of the row
         int lo, hi;
         z.warp_part(warp, lo, hi);
         for (int v = lo; v < hi; v += 32) {
@@ -567,13 +641,22 @@ template <typename IO> __global__ void __launch_bounds__(kThreads) k_sample(cons
     cluster.sync();
 }
 
-template <typename IO> cudaError_t launch(const SampleArgs &a, cudaStream_t st) {
-    // CTAs per row: up to 8 while the rows leave SMs free and each has 2048 tokens at least
+template <typename IO> cudaError_t launch(SampleArgs a, cudaStream_t st) {
+    // CTAs per row: up to 8 while the rows leave SMs free and each has 2048 tokens at least, and as many as a slice's
+    // limit needs
     int ranks = 1;
-    while (ranks < kMaxCluster && (int64_t)a.B * ranks * 2 <= 2 * 152 && a.vocab / (ranks * 2) >= 2048) ranks *= 2;
+    while (ranks < kMaxCluster && (((int64_t)a.B * ranks * 2 <= 2 * 152 && a.vocab / (ranks * 2) >= 2048) || a.vocab + 16 > ranks * kSlice))
+        ranks *= 2;
+    constexpr int VEC = 16 / (int)sizeof(IO);
+    const int bytes = ((a.vocab + 2 * VEC - 1) / VEC + ranks - 1) / ranks * 16;  // of a slice, whatever the row's alignment
+    a.cached = bytes <= kCache;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(k_sample<IO>, kCache, done);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * ranks));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = a.cached ? bytes : 0;
     cfg.stream = st;
     cudaLaunchAttribute at[2] = {};
     at[0].id = cudaLaunchAttributeClusterDimension;
