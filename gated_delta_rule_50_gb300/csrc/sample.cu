@@ -11,12 +11,11 @@
 //
 // The CTAs of a cluster share a row; each reads its slice once and keeps it in shared memory, -inf for what the mask
 // forbids.  A cut is found by bins of 1/8 octave of t, whose running sum (of w, or of tokens for top-k) says in which bin
-// it lies.  At first they take the best of every thread's elements alone: what these reach, all reach, so that the true
-// cut lies in that bin or before it, and for all but flat distributions no more than kList tokens do.  Those are collected
-// and sorted, and the rest of the work is done on that list.  Where they are too many, the bins take every element, the
-// cut's bin is cut into kSub further ones, and what lies in one of those is collected and sorted to find the cut; where
-// even that is too much for the list (many equal logits), the cut is searched for by bisection, over the logit and then
-// over the tokens that share it.
+// it lies.  For top-k they take at first the best of every thread's elements alone: what these reach, all reach, so that
+// the true cut lies in that bin or before it.  If no more than kList tokens do, those are collected and sorted, and the
+// rest of the work is done on that list.  If they are too many, what lies in the cut's bin (or in one of kSub parts of
+// it) is collected and sorted to find the cut; where even that is too much for the list (many equal logits), the cut is
+// searched for by bisection, over the logit and then over the tokens that share it.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -75,21 +74,34 @@ __device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int d) { return __shf
 struct Shared {
     uint32_t part[3][kSub];  // sums of w by bins, in three parts of 15 bits
     uint32_t count[kSub];
+    uint64_t total[kSub];    // of either, as whole numbers
     uint64_t key[kList], w[kList];
     uint64_t table[65];  // 2^(42 + j / 64), j = -32 .. 32
     uint64_t warp_w[kWarps];
     uint32_t warp_n[kWarps];
-    uint64_t best;       // of the CTA's slice
-    int bad;
+    uint64_t best;       // of the CTA's slice; all ones where there is what must not be
     Sums sum[2];         // what the CTA adds to a sum over the cluster
     uint64_t warp_kept[kWarps];
     uint32_t listed;     // entries of the list (the first CTA's)
     uint64_t cut;        // found by the first CTA
     int at_bin;
-    uint64_t before;     // what lies in the bins before it
-    float c_hi, c_lo;
-    double min_p;        // temperature ln(min_p)
+    uint64_t before, here;  // what lies in the bins before it, and in it
+    float warp_f[kWarps], most;  // how many tokens these and that bin have at most, where w was summed
 };
+// floor or ceil of f x for an f from [0, 1]
+__device__ __forceinline__ uint64_t part_of(float f, uint64_t x, bool up) {
+    const uint32_t u = __float_as_uint(f);
+    const int e = max((int)(u >> 23), 1);  // f = c 2^(e - 150)
+    const uint64_t c = (u & 0x7FFFFFu) | (u >> 23 ? 0x800000u : 0u);
+    const uint64_t lo = c * x, hi = __umul64hi(c, x);
+    const int down = 150 - e;  // 23 .. 149
+    uint64_t whole, rest;
+    if (down < 64) whole = hi << (64 - down) | lo >> down, rest = lo << (64 - down);
+    else if (down < 128) whole = down == 64 ? hi : hi >> (down - 64), rest = lo | (down == 64 ? 0 : hi << (128 - down));
+    else whole = 0, rest = lo | hi;
+    return whole + (up && rest ? 1 : 0);
+}
+
 
 template <typename IO> struct Sampler {
     static constexpr int VEC = 16 / (int)sizeof(IO);
@@ -227,45 +239,51 @@ template <typename IO> struct Sampler {
         a = block_sum(a);
         if (threadIdx.x == 0) s.sum[turn] = a;
         cluster.sync();
+        return read_sum();
+    }
+    __device__ __forceinline__ Sums read_sum() {  // of what lies in sum[turn]
+        const unsigned r = threadIdx.x & 31;
         Sums all = {0, 0};
-        for (unsigned r = 0; r < cluster.num_blocks(); ++r) all = all + *cluster.map_shared_rank(&s.sum[turn], r);
+        if (r < cluster.num_blocks()) all = *cluster.map_shared_rank(&s.sum[turn], r);
+#pragma unroll
+        for (int d = kMaxCluster / 2; d; d >>= 1) all.w += shfl_xor64(all.w, d), all.n += __shfl_xor_sync(~0u, all.n, d);
+        all.w = __shfl_sync(~0u, (unsigned long long)all.w, 0), all.n = __shfl_sync(~0u, all.n, 0);
         turn ^= 1;
         return all;
     }
 
+    // The CTA's bins as whole numbers, for locate() behind the next sync
+    __device__ __forceinline__ void close_bins(bool by_count) {
+        __syncthreads();
+        const int i = threadIdx.x;
+        s.total[i] = by_count ? s.count[i] : ((uint64_t)s.part[2][i] << 30) + ((uint64_t)s.part[1][i] << 15) + s.part[0][i];
+    }
     // Where in the bins (over the cluster; a thread for each) the running sum reaches `need`, of w or of tokens: at_bin
-    // (kThreads: nowhere) and what lies before it.  The bins stay as they are until the next sync.
+    // (kThreads: nowhere), what lies before it and in it, and how many tokens that are at most.  Bins of t only, where w was
+    // summed: a token of bin i has 2^(42 - (i + 1) / kOctave) at least.
     __device__ __forceinline__ void locate(bool by_count, uint64_t need) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        uint64_t mine = 0;
+        uint64_t part[kMaxCluster], mine = 0;
         const unsigned ranks = cluster.num_blocks();
-        if (by_count) {
-            uint32_t n[kMaxCluster];
 #pragma unroll
-            for (unsigned r = 0; r < kMaxCluster; ++r) n[r] = r < ranks ? cluster.map_shared_rank(&s, r)->count[threadIdx.x] : 0;
+        for (unsigned r = 0; r < kMaxCluster; ++r) part[r] = r < ranks ? cluster.map_shared_rank(&s, r)->total[threadIdx.x] : 0;
 #pragma unroll
-            for (unsigned r = 0; r < kMaxCluster; ++r) mine += n[r];
-        } else {
-            uint32_t p[3][kMaxCluster];
-#pragma unroll
-            for (unsigned r = 0; r < kMaxCluster; ++r)
-#pragma unroll
-                for (int i = 0; i < 3; ++i) p[i][r] = r < ranks ? cluster.map_shared_rank(&s, r)->part[i][threadIdx.x] : 0;
-#pragma unroll
-            for (unsigned r = 0; r < kMaxCluster; ++r) mine += ((uint64_t)p[2][r] << 30) + ((uint64_t)p[1][r] << 15) + p[0][r];
-        }
+        for (unsigned r = 0; r < kMaxCluster; ++r) mine += part[r];
+        const float most = by_count ? 0.f : (float)mine * exp2f((float)(threadIdx.x + 1) * (1.f / kOctave) - (float)kShift) * 1.001f;
         uint64_t run = mine;
+        float tokens = most;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const uint64_t y = shfl_up64(run, d);
-            if (lane >= d) run += y;
+            const float f = __shfl_up_sync(~0u, tokens, d);
+            if (lane >= d) run += y, tokens += f;
         }
         __syncthreads();
-        if (lane == 31) s.warp_w[warp] = run;
+        if (lane == 31) s.warp_w[warp] = run, s.warp_f[warp] = tokens;
         if (threadIdx.x == 0) s.at_bin = kThreads;
         __syncthreads();
-        for (int i = 0; i < warp; ++i) run += s.warp_w[i];
-        if (run - mine < need && run >= need) s.at_bin = threadIdx.x, s.before = run - mine;
+        for (int i = 0; i < warp; ++i) run += s.warp_w[i], tokens += s.warp_f[i];
+        if (run - mine < need && run >= need) s.at_bin = threadIdx.x, s.before = run - mine, s.here = mine, s.most = by_count ? (float)run : tokens;
         __syncthreads();
     }
     __device__ __forceinline__ void clear_bins() {
@@ -284,7 +302,7 @@ template <typename IO> struct Sampler {
         if (at < kList) first->key[at] = key;
     }
     // Sorts the first n entries of the list: descending keys.  E entries a thread, those of tid + 512 e; partners less than
-    // a warp apart meet by shuffles
+    // a warp apart meet by shuffles.  Warps without entries stay out of it.
     template <int E> __device__ __forceinline__ void sort_entries(int n, int size) {
         uint64_t k[E];
 #pragma unroll
@@ -292,7 +310,13 @@ template <typename IO> struct Sampler {
             const int i = threadIdx.x + e * kThreads;
             k[e] = i < n ? s.key[i] : 0;
         }
-        __syncthreads();
+        const int threads = min(size, kThreads);
+        if ((int)threadIdx.x >= threads) {
+            __syncthreads();
+            return;
+        }
+        auto meet = [&] { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); };
+        meet();
         for (int g = 2; g <= size; g <<= 1)
             for (int j = g >> 1; j; j >>= 1) {
                 if (E == 2 && j == kThreads) {
@@ -305,7 +329,7 @@ template <typename IO> struct Sampler {
                 if (j >= 32) {
 #pragma unroll
                     for (int e = 0; e < E; ++e) s.key[threadIdx.x + e * kThreads] = k[e];
-                    __syncthreads();
+                    meet();
                 }
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
@@ -314,7 +338,7 @@ template <typename IO> struct Sampler {
                     const bool keep_larger = ((i & g) == 0) == ((i & j) == 0);
                     k[e] = keep_larger ? max(k[e], y) : min(k[e], y);
                 }
-                if (j >= 32) __syncthreads();
+                if (j >= 32) meet();
             }
 #pragma unroll
         for (int e = 0; e < E; ++e) s.key[threadIdx.x + e * kThreads] = k[e];
@@ -361,25 +385,34 @@ template <typename IO> struct Sampler {
         return lo;
     }
 
-    // The cut in a bin: the key at which, among the keys from `floor` on, the running sum over the bin reaches need
-    __device__ __forceinline__ uint64_t cut_in(int bin, bool by_count, uint64_t need, uint64_t floor) {
-        cluster.sync();  // all have read the bins
-        clear_bins();
-        if (threadIdx.x == 0) s.listed = 0;
-        each([&](float y, int token) {
-            if (bin_of(y) != bin || make_key(y, token) < floor) return;
-            if (by_count) atomicAdd(&s.count[sub_of(y, bin)], 1u);
-            else add(sub_of(y, bin), weight(y));
-        });
-        cluster.sync();
-        locate(by_count, need);
-        const int sub = s.at_bin;
-        if (sub == kThreads) return floor;  // all of it
+    // The cut in a bin, as locate() left it: the key at which, among the keys from `floor` on, the running sum reaches need
+    __device__ __forceinline__ uint64_t cut_in(bool by_count, uint64_t need, uint64_t floor) {
+        const int bin = s.at_bin;
         need -= s.before;
+        const float most = by_count ? (float)s.here : (float)s.here * exp2f((float)(bin + 1) * (1.f / kOctave) - (float)kShift) * 1.001f;
+        int sub = -1;  // all of the bin
+        cluster.sync();  // all have read the bins
+        if (threadIdx.x == 0) s.listed = 0;
+        if (most > (float)kList) {
+            clear_bins();
+            each([&](float y, int token) {
+                if (bin_of(y) != bin || make_key(y, token) < floor) return;
+                if (by_count) atomicAdd(&s.count[sub_of(y, bin)], 1u);
+                else add(sub_of(y, bin), weight(y));
+            });
+            close_bins(by_count);
+            cluster.sync();
+            locate(by_count, need);
+            sub = s.at_bin;
+            if (sub == kThreads) return floor;  // all of it
+            need -= s.before;
+        } else {
+            cluster.sync();
+        }
         uint32_t n = 0;
         each([&](float y, int token) {
             const uint64_t key = make_key(y, token);
-            if (bin_of(y) == bin && key >= floor && sub_of(y, bin) == sub) collect(key), ++n;
+            if (bin_of(y) == bin && key >= floor && (sub < 0 || sub_of(y, bin) == sub)) collect(key), ++n;
         });
         n = row_sum({0, n}).n;
         if (n <= kList) {
@@ -398,7 +431,7 @@ template <typename IO> struct Sampler {
             const uint32_t mid = lo + (hi - lo) / 2 + 1;
             Sums a = {0, 0};
             each([&](float y, int token) {
-                if (ordered(y) >= mid && bin_of(y) == bin && make_key(y, token) >= floor && sub_of(y, bin) == sub)
+                if (ordered(y) >= mid && bin_of(y) == bin && make_key(y, token) >= floor && (sub < 0 || sub_of(y, bin) == sub))
                     a.w += weight(y), ++a.n;
             });
             a = row_sum(a);
@@ -448,15 +481,15 @@ template <typename IO> __global__ void __launch_bounds__(kThreads, 2) k_sample(c
     const bool none = !(heat >= 0.f) || heat == INFINITY || isnan(top_p) || isnan(given_min_p);
     float u = a.u[row];
     u = u >= 0.f ? fminf(u, 0.99999994f) : 0.f;
-    if (tid == 0) s.bad = 0, s.listed = 0;
-    if (tid == 32) {
-        const double c = 1.4426950408889634 / (double)heat;
-        s.c_hi = c < 3e38 ? (float)c : 3e38f;
-        s.c_lo = c < 3e38 ? (float)(c - (double)s.c_hi) : 0.f;
+    if (tid == 0) s.listed = 0;
+    if (tid < 65) s.table[tid] = kPowers.of[tid];
+    {  // log2(e) / temperature as a pair
+        constexpr double c = 1.4426950408889634;
+        constexpr float hi = (float)c, lo = (float)(c - (double)hi);
+        z.c_hi = fminf(hi / heat, 3e38f);
+        const float rest = fmaf(-z.c_hi, heat, hi) + lo;
+        z.c_lo = z.c_hi < 3e38f ? rest / heat : 0.f;
     }
-    if (tid == 64) s.min_p = min_p > 0.f ? (double)heat * log((double)min_p) : 0.;
-    if (tid >= 128 && tid < 128 + 65) s.table[tid - 128] = kPowers.of[tid - 128];
-    __syncthreads();
     // the best logit, of this thread's elements and of the row
     float mine = -INFINITY;
     {
@@ -472,21 +505,21 @@ template <typename IO> __global__ void __launch_bounds__(kThreads, 2) k_sample(c
 #pragma unroll
         for (int d = 16; d; d >>= 1) key = max(key, shfl_xor64(key, d));
         if (lane == 0) s.warp_w[warp] = key;
-        if (bad) s.bad = 1;
         z.clear_bins();
-        if (tid == 0) {
-            for (int i = 1; i < kWarps; ++i) key = max(key, s.warp_w[i]);
-            s.best = key;
+        const int anywhere = __syncthreads_or(bad);
+        if (warp == 0) {
+            key = lane < kWarps ? s.warp_w[lane] : 0;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) key = max(key, shfl_xor64(key, d));
+            if (lane == 0) s.best = anywhere ? ~0ull : key;
         }
         cluster.sync();
     }
-    uint64_t best = 0;
-    bool bad = none;
-    for (int r = 0; r < ranks; ++r) {
-        const Shared *o = cluster.map_shared_rank(&s, r);
-        best = max(best, o->best);
-        bad |= o->bad != 0;
-    }
+    uint64_t best = lane < ranks ? cluster.map_shared_rank(&s, lane)->best : 0;
+#pragma unroll
+    for (int d = kMaxCluster / 2; d; d >>= 1) best = max(best, shfl_xor64(best, d));
+    best = __shfl_sync(~0u, (unsigned long long)best, 0);
+    const bool bad = none || best == ~0ull;
     auto answer = [&](int token, float logprob) {
         a.tokens[row] = token;
         if (a.logprobs) a.logprobs[row] = logprob;
@@ -500,7 +533,6 @@ template <typename IO> __global__ void __launch_bounds__(kThreads, 2) k_sample(c
         return;
     }
     z.m = unordered((uint32_t)(best >> 32));
-    z.c_hi = s.c_hi, z.c_lo = s.c_lo;
     auto logprob = [&](float y, uint64_t w, uint64_t total) {  // near 1 by what is left of it
         if (w > total / 2) return log1pf(-((float)(total - w) / (float)total));
         float low;
@@ -508,27 +540,46 @@ template <typename IO> __global__ void __launch_bounds__(kThreads, 2) k_sample(c
         return (t + low) * 0.693147181f - logf((float)total * (1.f / (float)(1ull << kShift)));
     };
     uint64_t cut = 0;
-    if (min_p > 0.f) cut = (uint64_t)ordered(__double2float_ru((double)z.m + s.min_p)) << 32;
+    const uint64_t least = min_p > 0.f ? part_of(min_p, 1ull << kShift, true) : 0;  // share that min-p asks for
     const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.f;
     if (by_k || by_p) {
-        auto share = [&](uint64_t of) { return max((uint64_t)1, (uint64_t)ceil((double)fmaxf(top_p, 0.f) * (double)of)); };
+        auto share = [&](uint64_t of) { return max((uint64_t)1, part_of(fmaxf(top_p, 0.f), of, true)); };
         Sums all = {0, 0};
-        const int own = z.bin_of(mine);
-        if (by_k) {
+        const bool by_best = by_k && top_k <= kList / 2;
+        auto fill = [&](bool by_count, uint64_t floor) {  // the bins, of every element from a key on; what their w sum to
+            Sums sum = {0, 0};
+            z.each([&](float y, int token) {
+                const int bin = z.bin_of(y);
+                if (bin >= kBins || make_key(y, token) < floor) return;
+                if (by_count) {
+                    atomicAdd(&s.count[bin], 1u);
+                } else {
+                    const uint64_t w = z.weight(y);
+                    z.add(bin, w);
+                    sum.w += w;
+                }
+            });
+            z.close_bins(by_count);
+            return z.row_sum(sum);
+        };
+        if (by_best) {
+            const int own = z.bin_of(mine);
             if (own < kBins) atomicAdd(&s.count[own], 1u);
+            z.close_bins(true);
             cluster.sync();
         } else {
-            if (own < kBins) z.add(own, z.weight(mine));
-            z.each([&](float y, int) { all.w += z.weight(y); });
-            all = z.row_sum(all);
+            all = fill(by_k, 0);
         }
         z.locate(by_k, by_k ? (uint64_t)top_k : share(all.w));
-        // all up to this bin; where the best ones do not reach so far, there are too many (or the row is no longer than the list)
+        // All up to this bin into the list, if they may fit.  (Where the best ones do not reach so far, they do only if the
+        // row itself is no longer.)
         const int reach = min(s.at_bin, kBins);
         uint32_t n = kList + 1;
-        if (reach < kBins || a.vocab <= kList) {
+        if (reach < kBins ? by_best || s.most <= (float)kList : a.vocab <= kList) {
+            // by a logit that is below all of these bins': what is listed is a beginning of the order all the same
+            const float low = reach < kBins ? z.m - (float)(reach + 1) / (z.c_hi * kOctave) * 1.0001f - fabsf(z.m) * 1e-6f : -INFINITY;
             z.each([&](float y, int token) {
-                if (y > -INFINITY && z.bin_of(y) <= reach) z.collect(make_key(y, token));
+                if (y >= low && y > -INFINITY) z.collect(make_key(y, token));
             });
             cluster.sync();
             n = cluster.map_shared_rank(&s, 0)->listed;
@@ -539,11 +590,11 @@ template <typename IO> __global__ void __launch_bounds__(kThreads, 2) k_sample(c
                 z.scan_list((int)n);
                 int kept = by_k ? min((int)n, top_k) : (int)n;
                 if (by_p) kept = min(kept, z.place(kept, share(by_k ? s.w[kept - 1] : all.w)) + 1);
-                {  // min-p: entries before the first below it
+                {  // min-p: entries before the first below it; the best one is none of these
                     int lo = 1, hi = kept;
                     while (lo < hi) {
                         const int mid = (lo + hi) >> 1;
-                        if (s.key[mid] < cut) hi = mid;
+                        if (s.w[mid] - s.w[mid - 1] < least) hi = mid;
                         else lo = mid + 1;
                     }
                     kept = lo;
@@ -558,7 +609,7 @@ template <typename IO> __global__ void __launch_bounds__(kThreads, 2) k_sample(c
                 __syncthreads();
                 z.scan_list(kept);
                 if (tid == 0) {
-                    const int i = min(z.place(kept, (uint64_t)((double)u * (double)total) + 1), kept - 1);
+                    const int i = min(z.place(kept, part_of(u, total, false) + 1), kept - 1);
                     const float y = unordered((uint32_t)(s.key[i] >> 32));
                     answer((int)key_token(s.key[i]), logprob(y, s.w[i] - (i ? s.w[i - 1] : 0), total));
                 }
@@ -566,57 +617,56 @@ template <typename IO> __global__ void __launch_bounds__(kThreads, 2) k_sample(c
             cluster.sync();
             return;
         }
-        // every element into the bins; the cut of top-k, then that of top-p behind it
+        // the cut of top-k, then that of top-p behind it
         uint64_t floor = 0;
-        for (int filter = by_k ? 0 : 1; filter < (by_p ? 2 : 1); ++filter) {
-            const bool by_count = filter == 0;
-            cluster.sync();
-            z.clear_bins();
-            all = {0, 0};
-            z.each([&](float y, int token) {
-                const int bin = z.bin_of(y);
-                if (bin >= kBins || make_key(y, token) < floor) return;
-                if (by_count) {
-                    atomicAdd(&s.count[bin], 1u);
-                } else {
-                    const uint64_t w = z.weight(y);
-                    z.add(bin, w);
-                    all.w += w;
-                }
-            });
-            all = z.row_sum(all);
-            const uint64_t need = by_count ? (uint64_t)top_k : share(all.w);
-            z.locate(by_count, need);
-            const int bin = s.at_bin;
-            if (bin < kBins) floor = z.cut_in(bin, by_count, need - s.before, floor);
+        if (by_k) {
+            if (by_best) {
+                cluster.sync();
+                z.clear_bins();
+                fill(true, 0);
+                z.locate(true, (uint64_t)top_k);
+            }
+            if (s.at_bin < kBins) floor = z.cut_in(true, (uint64_t)top_k, 0);
         }
-        cut = max(cut, floor);
+        if (by_p) {
+            if (by_k) {
+                cluster.sync();
+                z.clear_bins();
+                all = fill(false, floor);
+                z.locate(false, share(all.w));
+            }
+            if (s.at_bin < kBins) floor = z.cut_in(false, share(all.w), floor);
+        }
+        cut = floor;
     }
     // the token in the order of the vocabulary: sums of the warps' parts, then the part that has it
     Sums kept = {0, 0};
-    z.each([&](float y, int token) {
-        if (make_key(y, token) >= cut) kept.w += z.weight(y);
-    });
+    auto kept_weight = [&](float y, int token) {
+        const uint64_t w = make_key(y, token) >= cut ? z.weight(y) : 0;
+        return w >= least ? w : 0;
+    };
+    z.each([&](float y, int token) { kept.w += kept_weight(y, token); });
     const Sums total = z.row_sum(kept);
     uint64_t warp_sum = kept.w;
 #pragma unroll
     for (int d = 16; d; d >>= 1) warp_sum += shfl_xor64(warp_sum, d);
     uint64_t before = 0;
-    for (int r = 0; r < rank; ++r) before += cluster.map_shared_rank(&s.sum[z.turn ^ 1], r)->w;
+    if (lane < rank) before = cluster.map_shared_rank(&s.sum[z.turn ^ 1], lane)->w;
+#pragma unroll
+    for (int d = kMaxCluster / 2; d; d >>= 1) before += shfl_xor64(before, d);
+    before = __shfl_sync(~0u, (unsigned long long)before, 0);
     __syncthreads();
     if (lane == 0) s.warp_kept[warp] = warp_sum;
     __syncthreads();
     for (int i = 0; i < warp; ++i) before += s.warp_kept[i];
-    const uint64_t need = (uint64_t)((double)u * (double)total.w) + 1;
+    const uint64_t need = part_of(u, total.w, false) + 1;
     if (before < need && before + warp_sum >= need) {  // one warp of the row
         int lo, hi;
         z.warp_part(warp, lo, hi);
         for (int v = lo; v < hi; v += 32) {
             uint64_t run = 0;
             if (v + lane < hi)
-                z.vector(v + lane, [&](float y, int token) {
-                    if (make_key(y, token) >= cut) run += z.weight(y);
-                });
+                z.vector(v + lane, [&](float y, int token) { run += kept_weight(y, token); });
             const uint64_t own = run;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -628,8 +678,7 @@ template <typename IO> __global__ void __launch_bounds__(kThreads, 2) k_sample(c
             if (before + all >= need) {
                 if (at < need && at + own >= need)
                     z.vector(v + lane, [&](float y, int token) {
-                        if (make_key(y, token) < cut) return;
-                        const uint64_t w = z.weight(y);
+                        const uint64_t w = kept_weight(y, token);
                         if (at < need && at + w >= need) answer(token, logprob(y, w, total.w));
                         at += w;
                     });
