@@ -59,6 +59,20 @@ __device__ __forceinline__ LinearSpan linear_span(const LinearRun &r, int s) {
     return x;
 }
 
+// The sequence that the CTAs of place `slot` take: where packed sequences are few they go longest first, so that a long one
+// does not begin when the others are done.  A whole warp
+__device__ __forceinline__ int linear_seq(const LinearRun &r, int slot) {
+    if (!r.cu || r.n_seqs > 32 || r.n_seqs == 1) return slot;
+    const int lane = threadIdx.x & 31;
+    const int mine = lane < r.n_seqs ? r.cu[lane + 1] - r.cu[lane] : 0;
+    int rank = 0;
+    for (int s = 0; s < r.n_seqs; ++s) {
+        const int other = __shfl_sync(~0u, mine, s);
+        rank += other > mine || (other == mine && s < lane);
+    }
+    return __ffs(__ballot_sync(~0u, lane < r.n_seqs && rank == slot)) - 1;
+}
+
 // The tensor cores' kernel: bf16, rows on 16-byte boundaries.  What it does not take, the CUDA cores' does
 bool linear_tc_supported(const LinearRun &r, gdn_dtype io);
 cudaError_t launch_linear_tc(const LinearRun &r, cudaStream_t st);

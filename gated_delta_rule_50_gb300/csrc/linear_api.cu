@@ -25,16 +25,18 @@ gdn_status problem_ok(const gdn_linear_problem *p) {
     if (p->cu_seqlens ? p->B != 1 : p->n_seqs != p->B) return GDN_ERR_INVALID_ARG;
     if ((p->K != 64 && p->K != 128) || (p->V != 64 && p->V != 128)) return GDN_ERR_UNSUPPORTED;
     if (p->Hv > 16383 || p->B > INT32_MAX || p->T > INT32_MAX - C || p->n_seqs > INT32_MAX / 64) return GDN_ERR_UNSUPPORTED;
-    if (p->B * p->T > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (p->B * p->T > INT32_MAX || p->n_seqs * p->Hv > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
 // Into how many segments sequences are cut.  A head of a sequence keeps one SM busy; where these are fewer than the SMs,
-// each is cut so that they fill them, but into segments of four chunks at least.
+// each is cut so that they fill them.  Every token's part in the state is then taken twice, and there are two launches more.
+// Measured on the tensor cores, us: 2.2 a chunk and 6 for whole ones, 1.5 + 2.2 a chunk of a segment and 16 for cut ones.
 int segments(const gdn_linear_problem *p) {
     const int64_t chains = p->n_seqs * p->Hv, chunks = (p->T + C - 1) / C;
-    if (chains == 0) return 1;
-    return (int)std::max<int64_t>(1, std::min(kSMs / chains, chunks / 4));
+    if (chains == 0 || chains > kSMs / 2) return 1;
+    const int64_t n = std::min(kSMs / chains, chunks), each = n ? (chunks + n - 1) / n : 0;
+    return n > 1 && 3.7 * each + 16 < 2.2 * chunks + 6 ? (int)((chunks + each - 1) / each) : 1;
 }
 
 struct Layout {

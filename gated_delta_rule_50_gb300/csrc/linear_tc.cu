@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
     if (warp == W_TMA && lane == 0) prefetch_tmap(&maps.a), prefetch_tmap(&maps.b), prefetch_tmap(&maps.c);
     wait_for_previous();
 
-    const int h = blockIdx.y, seq = blockIdx.x / r.n_seg, part = blockIdx.x % r.n_seg;
+    const int h = blockIdx.x % r.Hv, part = blockIdx.x / r.Hv % r.n_seg, seq = linear_seq(r, blockIdx.x / r.Hv / r.n_seg);
     const LinearSpan span = linear_span(r, seq);
     const int c0 = min(span.chunks, part * span.per_seg), c1 = min(span.chunks, c0 + span.per_seg);
     const int64_t unit = (int64_t)seq * r.Hv + h, words = (int64_t)DA * r.dc;
@@ -620,7 +620,7 @@ template <int DA, int OUT, bool THIRD> cudaError_t launch(const Maps &maps, cons
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k_linear_tc<DA, OUT, THIRD>, (int)SMEM_BYTES, done);
     if (e != cudaSuccess) return e;
-    return launch_behind(k_linear_tc<DA, OUT, THIRD>, dim3((unsigned)(r.n_seqs * r.n_seg), (unsigned)r.Hv), kThreads, SMEM_BYTES, st, maps, r);
+    return launch_behind(k_linear_tc<DA, OUT, THIRD>, dim3((unsigned)(r.n_seqs * r.n_seg * r.Hv)), kThreads, SMEM_BYTES, st, maps, r);
 }
 
 // A dimension that is stepped over needs a positive stride of a multiple of 16 bytes
