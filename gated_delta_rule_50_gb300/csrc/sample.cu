@@ -702,19 +702,7 @@ template <typename IO> cudaError_t launch(SampleArgs a, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k_sample<IO>, kCache, done);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.B * ranks));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = a.cached ? bytes : 0;
-    cfg.stream = st;
-    cudaLaunchAttribute at[2] = {};
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)ranks, at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_sample<IO>, a);
+    return launch_clusters(k_sample<IO>, ranks, dim3((unsigned)(a.B * ranks)), kThreads, a.cached ? (size_t)bytes : 0, st, a);
 }
 
 }  // namespace

@@ -103,3 +103,17 @@ def test_backward(case):
         ref = reference(x, backward=True)
     for name, got in zip(("dq", "dk", "dv", "dh0"), grads):
         verify(name, got, ref[name], case[6])
+
+
+@pytest.mark.parametrize("G", [2, 3, 4, 5, 8])
+@pytest.mark.parametrize("K", [64, 128])
+def test_shared_heads(G, K):
+    """Gradients of q and k are sums over the value heads that share them, in groups that the kernel sums itself and others."""
+    x = make(2, 150, 2, 2 * G, K, 128, bf16, seed=G + K)
+    leaves = [x[n].requires_grad_() for n in ("q", "k", "v", "h0")]
+    o, ht = gdn.chunk_linear_attention(x["q"], x["k"], x["v"], x["g"], initial_state=x["h0"], output_final_state=True)
+    grads = torch.autograd.grad([o, ht], leaves, [x["do"], x["dht"]])
+    with torch.no_grad():
+        ref = reference(x, backward=True)
+    for name, got in zip(("dq", "dk", "dv", "dh0"), grads):
+        verify(name, got, ref[name], bf16)
