@@ -22,7 +22,7 @@
 // Roles (512 threads): warps 0 and 1 make P~, warp 2 loads (TMA, three stages), warp 3 issues the products, warps 4 .. 11
 // keep the state and write out, warps 12 .. 15 make w c.  Per chunk the tensor cores are asked for, in this order,
 //     U(j), P(j + 1), I(j), O(j)
-// and the others follow them: w c and U while I(j - 1) and O(j - 1) run, X and out while U(j) and P(j + 1) do, P~(j + 1) until O(j + 1).
+// and the others follow them: w c while I(j - 1) and O(j - 1) run, U, X and out from I(j - 1)'s end on, P~(j + 1) until O(j + 1).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -63,6 +63,25 @@ static_assert(BARRIERS <= 32 && SMEM_BYTES <= 232448, "shared memory");
 constexpr uint32_t TM_XH = 0, TM_XL = 64, TM_U = 128, TM_P = 256, TM_I = 320, TM_O = 384, TM_WH = 448, TM_WL = 480;
 
 constexpr uint32_t ID_N64 = idesc_bf16(128, 64, 0, 0), ID_N64_AMN = idesc_bf16(128, 64, 1, 0);
+
+// Two loads of 16 lanes x 32 columns, waited: thread t has, of every eight columns, 2 (t % 4) and the next one of lane t / 4
+// (two registers) and of lane t / 4 + 8 (two more), as a matrix fragment has them
+#define GDN_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t ta, uint32_t (&a)[16], uint32_t tb, uint32_t (&b)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+        "[%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : GDN_R8(a, 0), GDN_R8(a, 8), GDN_R8(b, 0), GDN_R8(b, 8)
+        : "r"(ta), "r"(tb)
+        : "memory");
+}
+#undef GDN_R8
+// Four 8 x 8 matrices of bf16 fragments, stored with rows and columns exchanged; lane l gives row l % 8 of matrix l / 8
+__device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 
 struct Maps {
     CUtensorMap a, b, c;
@@ -367,32 +386,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             }
             // X l^n as X + (l^n - 1) X: nothing is lost where l is all but 1; any chunk but the last has C tokens
             const float l1_full = expm1f(g * (float)C), l1_last = nck > 0 ? expm1f(g * (float)tokens(nck - 1)) : 0.f;
-            auto update = [&](float l1, bool say) {  // says that U is read
-
+            // X takes U (and says that it is read), and goes to TMEM as hi and lo
+            auto advance = [&](bool update, float l1, bool say, bool store) {
                 const uint64_t l2 = pair_of(l1, l1);
 #pragma unroll
                 for (int q = 0; q < HALF / 32; ++q) {
-                    uint32_t u[32];
-                    tmem_ld32(t_u + 32 * q, u);
-                    if (q + 1 == HALF / 32 && say) {
-                        tc_fence_before();
-                        mbar_arrive_warp(bar(WREADY));
+                    if (update) {
+                        uint32_t u[32];
+                        tmem_ld32(t_u + 32 * q, u);
+                        if (q + 1 == HALF / 32 && say) {
+                            tc_fence_before();
+                            mbar_arrive_warp(bar(WREADY));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            X[16 * q + i] = add2(X[16 * q + i], fma2(l2, X[16 * q + i], pair_of(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))));
                     }
+                    if (store) {
+                        uint32_t xh[16], xl[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        X[16 * q + i] = add2(X[16 * q + i], fma2(l2, X[16 * q + i], pair_of(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))));
-                }
-            };
-            auto store_x = [&] {
-#pragma unroll
-                for (int q = 0; q < HALF / 32; ++q) {
-                    uint32_t xh[16], xl[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        uint64_t x = X[16 * q + i];
-                        xh[i] = take_bf16(x), xl[i] = last_bf16(x);
+                        for (int i = 0; i < 16; ++i) {
+                            uint64_t x = X[16 * q + i];
+                            xh[i] = take_bf16(x), xl[i] = last_bf16(x);
+                        }
+                        tmem_st16x2(t_x + 16 * q, xh, t_x + (TM_XL - TM_XH) + 16 * q, xl);
                     }
-                    tmem_st16x2(t_x + 16 * q, xh, t_x + (TM_XL - TM_XH) + 16 * q, xl);
                 }
             };
             // 32 tokens of out of a chunk, staged as bf16 (or held as fp32), and their way to memory
@@ -400,10 +418,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             const int64_t low = first + (r.reverse ? (int64_t)span.tokens - (c0 + 1) * C : c0 * C);  // of chunk 0, were it whole
             const int64_t at0 = ((int64_t)batch * r.T + low + 32 * hh) * row + h * r.dc + 32 * quarter;
             const int64_t step = r.reverse ? -C * row : C * row;
-            const uint32_t stage_to = smem_u32(staged) + lane * 2;
+            // Fragments: columns (tokens) 8 n + 2 (lane % 4) and the next one, weighted by into[], 16 lanes at a time.  Staged rows
+            // of 64 bytes have their 16-byte pieces exchanged by pairs of rows, so that eight rows meet no bank twice
+            const uint32_t stage_at = smem_u32(staged);
+            auto piece = [&](int t, int c) { return (uint32_t)(t * 64 + ((c ^ (t >> 1 & 3)) << 4)); };
             auto write_out = [&](int j) {  // reads I and O, says so, and goes on
                 const bool last = j + 1 == nck;
-                const float *w = tab.into[last ? 1 : 0] + 32 * hh;
+                const float *into = tab.into[last ? 1 : 0] + 32 * hh;
                 // in the order of the scan the last chunk is the only short one; in reverse it is cut at its lower end
                 int64_t at = at0 + j * step;
                 int n = 32;
@@ -411,40 +432,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
                     n = tokens(j) - 32 * hh;
                     if (r.reverse) at += (C - tokens(j)) * row;
                 }
-                float *of = static_cast<float *>(r.out) + at + lane;
+                if constexpr (F32OUT) {  // a lane's column, token by token: whole lines
+                    float *to = static_cast<float *>(r.out) + at + lane;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t in[16], o[16];
+                        float w[16];
+                        lds16f(into + 16 * q, w);
+                        tmem_ld16x2(t_io + 16 * q, in, t_io + (TM_O - TM_I) + 16 * q, o);
+                        if (q == 1) {
+                            tc_fence_before();
+                            mbar_arrive_warp(bar(XREADY));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (16 * q + i < n) to[(16 * q + i) * row] = fmaf(w[i], __uint_as_float(in[i]), __uint_as_float(o[i]));
+                    }
+                    return;
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
                     uint32_t in[16], o[16];
-                    float ww[16];
-                    lds16f(w + 16 * q, ww);
-                    tmem_ld16x2(t_io + 16 * q, in, t_io + (TM_O - TM_I) + 16 * q, o);
-                    if (q == 1) {
+                    const uint32_t t16 = t_io + ((uint32_t)(16 * half) << 16);
+                    tmem_ld_fragments(t16, in, t16 + (TM_O - TM_I), o);
+                    if (half == 1) {
                         tc_fence_before();
                         mbar_arrive_warp(bar(XREADY));
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const uint64_t v = fma2(pair_of(ww[i], ww[i + 1]), pair_of(__uint_as_float(in[i]), __uint_as_float(in[i + 1])),
-                                                pair_of(__uint_as_float(o[i]), __uint_as_float(o[i + 1])));
-                        if constexpr (F32OUT) {
-                            float v0, v1;
-                            halves(v, v0, v1);
-                            if (16 * q + i < n) of[(16 * q + i) * row] = v0;
-                            if (16 * q + i + 1 < n) of[(16 * q + i + 1) * row] = v1;
-                        } else {
-                            const uint32_t b = last_bf16(v);
-                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage_to + (16 * q + i) * 64), "h"((uint16_t)b) : "memory");
-                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(stage_to + (16 * q + i + 1) * 64), "h"((uint16_t)(b >> 16)) : "memory");
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t b[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {  // tokens 8 (2 m + i / 2) .., lanes 16 half + 8 (i % 2) ..
+                            const int e = 4 * (2 * m + i / 2) + 2 * (i & 1);
+                            const uint64_t w = *reinterpret_cast<const uint64_t *>(into + 8 * (2 * m + i / 2) + 2 * (lane & 3));
+                            b[i] = last_bf16(fma2(w, pair_of(__uint_as_float(in[e]), __uint_as_float(in[e + 1])),
+                                                  pair_of(__uint_as_float(o[e]), __uint_as_float(o[e + 1]))));
                         }
+                        const int i = lane >> 3, t = 8 * (2 * m + (i >> 1)) + (lane & 7);
+                        store_transposed(stage_at + piece(t, 2 * half + (i & 1)), b[0], b[1], b[2], b[3]);
                     }
                 }
-                if constexpr (!F32OUT) {  // 64-byte pieces of the rows by 16-byte stores
+                {  // 64-byte pieces of the rows by 16-byte stores
                     __syncwarp();
                     __nv_bfloat16 *ob = static_cast<__nv_bfloat16 *>(r.out) + at + (lane >> 2) * row + 8 * (lane & 3);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(staged + i * 512 + lane * 16);
-                        if (8 * i + (lane >> 2) < n) __stcs(reinterpret_cast<uint4 *>(ob + i * 8 * row), x);
+                        const int t = 8 * i + (lane >> 2);
+                        const uint4 x = *reinterpret_cast<const uint4 *>(staged + piece(t, lane & 3));
+                        if (t < n) __stcs(reinterpret_cast<uint4 *>(ob + i * 8 * row), x);
                     }
                     __syncwarp();
                 }
@@ -452,19 +488,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             bool ok = true;
 #pragma unroll 1
             for (int j = 0; j < nck; ++j) {
-                if (j > 0) {
-                    if (!(ok = wait(UDONE, j - 1))) break;
+                if (j > 0) {  // I(j - 1) ends after U(j - 1)
+                    if (!(ok = wait(outs ? IDONE : UDONE, j - 1))) break;
                     tc_fence_after();
-                    update(l1_full, j < updates);
                 } else if (updates > 0) {
                     mbar_arrive_warp(bar(WREADY));
                 }
+                advance(j > 0, l1_full, j < updates, outs);
                 if (!outs) continue;
-                if (j > 0) {
-                    if (!(ok = wait(IDONE, j - 1))) break;
-                    tc_fence_after();
-                }
-                store_x();
                 if (j > 0) {
                     if (!(ok = wait(ODONE, j - 1))) break;
                     tc_fence_after();
@@ -476,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             }
             if (ok && nck > 0 && updates == nck && (ok = wait(UDONE, nck - 1))) {
                 tc_fence_after();
-                update(l1_last, false);
+                advance(true, l1_last, false, false);
             }
             if (ok && nck > 0 && outs && wait(ODONE, nck - 1)) {
                 tc_fence_after();
