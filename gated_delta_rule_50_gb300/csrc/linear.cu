@@ -78,21 +78,21 @@ template <typename IO, int DA, bool VEC> __global__ void __launch_bounds__(kThre
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem<DA> &s = *reinterpret_cast<Smem<DA> *>(smem_raw);
     wait_for_previous();
-    const int tid = threadIdx.x, h = blockIdx.x % r.Hv, col0 = blockIdx.y * COLS;
-    const int part = blockIdx.x / r.Hv % r.n_seg, seq = linear_seq(r, blockIdx.x / r.Hv / r.n_seg);
-    const LinearSpan span = linear_span(r, seq);
+    const int tid = threadIdx.x, h = blockIdx.x % r.Hv, col0 = blockIdx.y * COLS, slot = blockIdx.x / r.Hv;
+    int seq, part;
+    const LinearSpan span = linear_place(r, slot, seq, part);
+    if (seq < 0) return;
     const int from = part * span.per_seg * C, to = min(span.tokens, (part + 1) * span.per_seg * C);
     const int64_t unit = (int64_t)seq * r.Hv + h, words = (int64_t)DA * r.dc;
     const float *init = r.init ? r.init + unit * words : nullptr;
-    float *fin = r.fin ? r.fin + unit * words : nullptr;
+    float *fin = r.fin ? r.fin + unit * words : nullptr, *seg = r.seg + ((int64_t)slot * r.Hv + h) * words;
     bool init_t = r.transposed, fin_t = r.transposed;
     if (r.mode == LIN_SEG) {  // the last segment feeds no other
         if (to >= span.tokens) return;
-        init = nullptr, fin = r.seg + (unit * r.n_seg + part) * words, fin_t = false;
+        init = nullptr, fin = seg, fin_t = false;
     } else if (part > 0) {
         if (from >= to) return;
-        init = r.seg + (unit * r.n_seg + part) * words;
-        init_t = false;
+        init = seg, init_t = false;
     }
     if (r.mode != LIN_SEG && to < span.tokens) fin = nullptr;
     const float g = r.g ? r.g[h] : 0.f;
@@ -101,7 +101,7 @@ template <typename IO, int DA, bool VEC> __global__ void __launch_bounds__(kThre
         const int x = i / COLS, y = col0 + i % COLS;
         s.x[x][i % COLS] = init ? init[init_t ? y * DA + x : x * r.dc + y] : 0.f;
     }
-    const int64_t batch = r.cu ? 0 : seq, first = r.cu ? span.first : 0;
+    const int64_t batch = r.cu ? 0 : seq, first = span.first;
     const bool outs = r.mode != LIN_SEG && r.out;
     const IO *a = static_cast<const IO *>(r.a) + batch * r.sa.batch + h / r.ga * r.sa.head;
     const IO *b = static_cast<const IO *>(r.b) + batch * r.sb.batch + h / r.gb * r.sb.head;
@@ -233,7 +233,7 @@ template <typename IO, int DA, bool VEC> cudaError_t launch(const LinearRun &r, 
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k_linear<IO, DA, VEC>, (int)sizeof(Smem<DA>), done);
     if (e != cudaSuccess) return e;
-    return launch_behind(k_linear<IO, DA, VEC>, dim3((unsigned)(r.n_seqs * r.n_seg * r.Hv), (unsigned)(r.dc / COLS)), kThreads, sizeof(Smem<DA>), st, r);
+    return launch_behind(k_linear<IO, DA, VEC>, dim3((unsigned)(r.slots * r.Hv), (unsigned)(r.dc / COLS)), kThreads, sizeof(Smem<DA>), st, r);
 }
 // Whether four values can be read at once
 template <typename IO> bool aligned4(const void *x, const gdn_strides &s) {
@@ -245,32 +245,48 @@ template <typename IO> cudaError_t launch(const LinearRun &r, cudaStream_t st) {
     return r.da == 128 ? launch<IO, 128, false>(r, st) : launch<IO, 64, false>(r, st);
 }
 
-// seg[p], the state that segment p adds, becomes the state that enters segment p.  The parts are asked for ahead: one by
-// one their way to memory took 18 us for 19 segments of 8 states
+// seg[p], the state that segment p adds, becomes the state that enters segment p.  The parts are asked for ahead, four
+// values at a time: one by one their way to memory took 18 us for 19 segments of 8 states
 __global__ void __launch_bounds__(256) k_join(const __grid_constant__ LinearRun r) {
     constexpr int AHEAD = 16;
     wait_for_previous();
-    const int words = r.da * r.dc, seq = blockIdx.x, h = blockIdx.y, i = blockIdx.z * 256 + threadIdx.x;
-    const LinearSpan span = linear_span(r, seq);
+    const int words = r.da * r.dc, seq = blockIdx.x / r.Hv, h = blockIdx.x % r.Hv;
+    LinearSpan span;
+    if (linear_packed(r)) {
+        span = linear_table(r);
+        span.per_seg = __shfl_sync(~0u, span.per_seg, seq), span.slot = __shfl_sync(~0u, span.slot, seq), span.segs = __shfl_sync(~0u, span.segs, seq);
+    } else {
+        span = linear_span(r, seq);
+    }
+    if (span.segs < 2) return;
     const int64_t unit = (int64_t)seq * r.Hv + h;
     const float g = r.g ? r.g[h] : 0.f;
     const float l1 = expm1f(g * (float)(span.per_seg * C));
-    const int x = i / r.dc, y = i % r.dc;
-    float X = r.init ? r.init[unit * words + (r.transposed ? y * r.da + x : i)] : 0.f;
-    float *seg = r.seg + unit * r.n_seg * words + i;
-    const int used = span.per_seg ? (span.chunks + span.per_seg - 1) / span.per_seg : 0;  // segments with tokens
-    for (int p0 = 0; p0 + 1 < used; p0 += AHEAD) {  // all but the last are full
-        float add[AHEAD];
-#pragma unroll
-        for (int p = 0; p < AHEAD; ++p) add[p] = p0 + p + 1 < used ? seg[(int64_t)(p0 + p) * words] : 0.f;
-#pragma unroll
-        for (int p = 0; p < AHEAD; ++p) {
-            if (p0 + p + 1 >= used) break;
-            if (p0 + p > 0) seg[(int64_t)(p0 + p) * words] = X;
-            X += fmaf(l1, X, add[p]);
+    const int64_t next = (int64_t)r.Hv * words;  // of the next segment
+    for (int i = (blockIdx.y * 256 + threadIdx.x) * 4; i < words; i += gridDim.y * 1024) {
+        const int x = i / r.dc, y = i % r.dc;
+        float4 X = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r.init) {
+            const float *init = r.init + unit * words;
+            if (r.transposed) X = make_float4(init[y * r.da + x], init[(y + 1) * r.da + x], init[(y + 2) * r.da + x], init[(y + 3) * r.da + x]);
+            else X = *reinterpret_cast<const float4 *>(init + i);
         }
+        float *seg = r.seg + ((int64_t)span.slot * r.Hv + h) * words + i;
+        for (int p0 = 0; p0 + 1 < span.segs; p0 += AHEAD) {  // all but the last are full
+            float4 add[AHEAD];
+#pragma unroll
+            for (int p = 0; p < AHEAD; ++p)
+                if (p0 + p + 1 < span.segs) add[p] = *reinterpret_cast<const float4 *>(seg + (p0 + p) * next);
+#pragma unroll
+            for (int p = 0; p < AHEAD; ++p) {
+                if (p0 + p + 1 >= span.segs) break;
+                if (p0 + p > 0) *reinterpret_cast<float4 *>(seg + (p0 + p) * next) = X;
+                X.x += fmaf(l1, X.x, add[p].x), X.y += fmaf(l1, X.y, add[p].y);
+                X.z += fmaf(l1, X.z, add[p].z), X.w += fmaf(l1, X.w, add[p].w);
+            }
+        }
+        *reinterpret_cast<float4 *>(seg + (span.segs - 1) * next) = X;
     }
-    if (used > 1) seg[(int64_t)(used - 1) * words] = X;
 }
 
 template <typename IO> __global__ void __launch_bounds__(256) k_group_sum(const float4 *x, IO *out, int64_t n4, int G, int d4) {
@@ -319,7 +335,9 @@ cudaError_t launch_linear_simt(const LinearRun &r, gdn_dtype io, cudaStream_t st
 }
 
 cudaError_t launch_linear_join(const LinearRun &r, cudaStream_t st) {
-    return launch_behind(k_join, dim3((unsigned)r.n_seqs, (unsigned)r.Hv, (unsigned)(r.da * r.dc / 256)), 256, 0, st, r);
+    const int64_t heads = (int64_t)r.n_seqs * r.Hv;
+    const unsigned parts = heads >= 128 ? 4 : 16;  // of a state: the more, the fewer there are
+    return launch_behind(k_join, dim3((unsigned)heads, parts), 256, 0, st, r);
 }
 
 cudaError_t launch_group_sum(const float *x, void *out, int64_t tokens, int heads, int G, int d, gdn_dtype io, cudaStream_t st) {

@@ -37,18 +37,20 @@ struct LinearRun {
     // Sequences are cut into n_seg segments of whole chunks where there are few of them.  LIN_SEG: the state that each
     // segment but the last adds, from 0, into seg; launch_linear_join makes the segments' first states of them; LIN_MAIN:
     // the segments from their first states.
-    int n_seg, mode;
-    float *seg;         // [n_seqs][Hv][n_seg][da][dc]
+    // Of packed sequences (2 to 32) only those are cut that are longer than seg_chunks, if that is not 0.
+    // Segments have numbers, their slots, 0 .. slots - 1 at most.
+    int n_seg, seg_chunks, slots, mode;
+    float *seg;         // [slots][Hv][da][dc]
 };
 
-// First token (of all B T), tokens and chunks of sequence s; offsets that fall or leave the T tokens: an empty one
+// A sequence's first token (of its row of the batch), its tokens and chunks (offsets that fall or leave the T tokens: none),
+// the chunks of its segments, and the slot of its first segment
 struct LinearSpan {
-    int64_t first;
-    int tokens, chunks, per_seg;  // per_seg: chunks of a segment
+    int first, tokens, chunks, per_seg, slot, segs;
 };
 __device__ __forceinline__ LinearSpan linear_span(const LinearRun &r, int s) {
     LinearSpan x;
-    x.first = (int64_t)s * r.T, x.tokens = r.T;
+    x.first = 0, x.tokens = r.T;
     if (r.cu) {
         const int lo = r.cu[s], hi = r.cu[s + 1];
         const bool valid = lo >= 0 && hi >= lo && hi <= r.T;
@@ -56,21 +58,43 @@ __device__ __forceinline__ LinearSpan linear_span(const LinearRun &r, int s) {
     }
     x.chunks = (x.tokens + C - 1) / C;
     x.per_seg = (x.chunks + r.n_seg - 1) / r.n_seg;
+    x.slot = s * r.n_seg, x.segs = x.per_seg ? (x.chunks + x.per_seg - 1) / x.per_seg : 1;
     return x;
 }
-
-// The sequence that the CTAs of place `slot` take: where packed sequences are few they go longest first, so that a long one
-// does not begin when the others are done.  A whole warp
-__device__ __forceinline__ int linear_seq(const LinearRun &r, int slot) {
-    if (!r.cu || r.n_seqs > 32 || r.n_seqs == 1) return slot;
+// Packed sequences: lane s has the s-th one's, and their slots follow each other by the segments' lengths, the longest first,
+// so that a long one does not begin when the others are done.  A whole warp
+__device__ __forceinline__ bool linear_packed(const LinearRun &r) { return r.cu && r.n_seqs > 1 && r.n_seqs <= 32; }
+__device__ __forceinline__ LinearSpan linear_table(const LinearRun &r) {
     const int lane = threadIdx.x & 31;
-    const int mine = lane < r.n_seqs ? r.cu[lane + 1] - r.cu[lane] : 0;
-    int rank = 0;
-    for (int s = 0; s < r.n_seqs; ++s) {
-        const int other = __shfl_sync(~0u, mine, s);
-        rank += other > mine || (other == mine && s < lane);
+    LinearSpan x = {0, 0, 0, 0, 0, 0};
+    if (lane < r.n_seqs) {
+        x = linear_span(r, lane);
+        if (r.seg_chunks) {
+            const int cuts = x.chunks > r.seg_chunks + r.seg_chunks / 4 ? (x.chunks + r.seg_chunks - 1) / r.seg_chunks : 1;
+            x.per_seg = (x.chunks + cuts - 1) / cuts, x.segs = x.per_seg ? (x.chunks + x.per_seg - 1) / x.per_seg : 1;
+        }
     }
-    return __ffs(__ballot_sync(~0u, lane < r.n_seqs && rank == slot)) - 1;
+    if (__reduce_add_sync(~0u, x.segs) > r.slots && lane < r.n_seqs) x.per_seg = x.chunks, x.segs = 1;  // overlapping ones
+    for (int s = 0; s < r.n_seqs; ++s) {
+        const int per = __shfl_sync(~0u, x.per_seg, s), segs = __shfl_sync(~0u, x.segs, s);
+        if (s == 0) x.slot = 0;
+        if (per > x.per_seg || (per == x.per_seg && s < lane)) x.slot += segs;
+    }
+    return x;
+}
+// What the CTAs of a slot take: segment `part` of sequence seq, which is -1 where there is none
+__device__ __forceinline__ LinearSpan linear_place(const LinearRun &r, int slot, int &seq, int &part) {
+    if (!linear_packed(r)) {
+        seq = slot / r.n_seg, part = slot % r.n_seg;
+        return linear_span(r, seq);
+    }
+    LinearSpan x = linear_table(r);
+    seq = __ffs(__ballot_sync(~0u, slot >= x.slot && slot < x.slot + x.segs)) - 1;
+    const int from = seq < 0 ? 0 : seq;
+    x.first = __shfl_sync(~0u, x.first, from), x.tokens = __shfl_sync(~0u, x.tokens, from), x.chunks = __shfl_sync(~0u, x.chunks, from);
+    x.per_seg = __shfl_sync(~0u, x.per_seg, from), x.slot = __shfl_sync(~0u, x.slot, from), x.segs = __shfl_sync(~0u, x.segs, from);
+    part = slot - x.slot;
+    return x;
 }
 
 // The tensor cores' kernel: bf16, rows on 16-byte boundaries.  What it does not take, the CUDA cores' does

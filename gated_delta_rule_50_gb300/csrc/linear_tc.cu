@@ -205,6 +205,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     Tables &tab = *reinterpret_cast<Tables *>(sm + SM_TAB);
     auto bar = [&](int i) { return sb + SM_BAR + 8u * (uint32_t)i; };
+    const int h = blockIdx.x % r.Hv, slot = blockIdx.x / r.Hv;
+    int seq, part;
+    LinearSpan span;
+    if (r.seg_chunks) {  // many slots may have nothing to do: they leave at once
+        wait_for_previous();
+        span = linear_place(r, slot, seq, part);
+        if (seq < 0 || (r.mode == LIN_SEG && part + 1 >= span.segs)) return;
+    }
 
     if (threadIdx.x == 0) {
         // of 64 columns only half of these warps have any
@@ -216,28 +224,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
     }
     if (warp == W_MMA) tmem_alloc(sb + SM_MISC, 512);
     if (warp == W_TMA && lane == 0) prefetch_tmap(&maps.a), prefetch_tmap(&maps.b), prefetch_tmap(&maps.c);
-    wait_for_previous();
+    if (!r.seg_chunks) {
+        wait_for_previous();
+        span = linear_place(r, slot, seq, part);
+    }
 
-    const int h = blockIdx.x % r.Hv, part = blockIdx.x / r.Hv % r.n_seg, seq = linear_seq(r, blockIdx.x / r.Hv / r.n_seg);
-    const LinearSpan span = linear_span(r, seq);
     const int c0 = min(span.chunks, part * span.per_seg), c1 = min(span.chunks, c0 + span.per_seg);
     const int64_t unit = (int64_t)seq * r.Hv + h, words = (int64_t)DA * r.dc;
-    const float *init = r.init ? r.init + unit * words : nullptr;
-    float *fin = r.fin ? r.fin + unit * words : nullptr;
+    bool init_t = r.transposed, fin_t = r.transposed, live = seq >= 0;
+    const float *init = live && r.init ? r.init + unit * words : nullptr;
+    float *fin = live && r.fin ? r.fin + unit * words : nullptr, *seg = r.seg + ((int64_t)slot * r.Hv + h) * words;
     constexpr bool outs = OUT != NO_OUT, F32OUT = OUT == F32_OUT;
-    bool init_t = r.transposed, fin_t = r.transposed, live = true;
     if (r.mode == LIN_SEG) {  // the last segment feeds no other
-        live = c1 < span.chunks && c0 < c1;
-        init = nullptr, fin = r.seg + (unit * r.n_seg + part) * words, fin_t = false;
+        live = live && c1 < span.chunks && c0 < c1;
+        init = nullptr, fin = seg, fin_t = false;
     } else {
         if (part > 0) {
-            live = c0 < c1;
-            init = r.seg + (unit * r.n_seg + part) * words, init_t = false;
+            live = live && c0 < c1;
+            init = seg, init_t = false;
         }
-        if (c1 < span.chunks || !live) fin = nullptr;
     }
+    if (!live || (r.mode != LIN_SEG && c1 < span.chunks)) fin = nullptr;
     const int nck = live ? c1 - c0 : 0, updates = fin ? nck : nck - 1;  // chunks whose part in the state is wanted
-    const int first = r.cu ? (int)span.first : 0, batch = r.cu ? 0 : seq;
+    const int first = span.first, batch = r.cu ? 0 : seq;
     // chunk j of this CTA: its lowest token in the row, and its tokens
     auto tokens = [&](int j) { return min(C, span.tokens - (c0 + j) * C); };
     auto token0 = [&](int j) {
@@ -651,7 +660,7 @@ template <int DA, int OUT, bool THIRD> cudaError_t launch(const Maps &maps, cons
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(k_linear_tc<DA, OUT, THIRD>, (int)SMEM_BYTES, done);
     if (e != cudaSuccess) return e;
-    return launch_behind(k_linear_tc<DA, OUT, THIRD>, dim3((unsigned)(r.n_seqs * r.n_seg * r.Hv)), kThreads, SMEM_BYTES, st, maps, r);
+    return launch_behind(k_linear_tc<DA, OUT, THIRD>, dim3((unsigned)(r.slots * r.Hv)), kThreads, SMEM_BYTES, st, maps, r);
 }
 
 // A dimension that is stepped over needs a positive stride of a multiple of 16 bytes

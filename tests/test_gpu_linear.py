@@ -117,3 +117,34 @@ def test_shared_heads(G, K):
         ref = reference(x, backward=True)
     for name, got in zip(("dq", "dk", "dv", "dh0"), grads):
         verify(name, got, ref[name], bf16)
+
+
+def packed_case(lengths, Hq, Hv, K, V, dtype, seed, T=None):
+    ends = [0]
+    for n in lengths:
+        ends.append(ends[-1] + n)
+    x = make(1, T or ends[-1], Hq, Hv, K, V, dtype, seed=seed, h0=False)
+    gen = torch.Generator().manual_seed(seed + 1)
+    x["h0"], x["dht"] = (torch.randn(len(lengths), Hv, K, V, generator=gen).cuda() for _ in range(2))
+    return x, torch.tensor(ends, dtype=torch.int32).cuda(), [(0, a, b) for a, b in zip(ends, ends[1:])]
+
+
+PACKED = [  # lengths, Hq, Hv, K, V, dtype
+    ([5, 0, 1, 130, 64], 2, 4, 128, 128, bf16), ([300], 1, 2, 128, 128, bf16), ([64, 65, 63], 2, 2, 64, 128, bf16),
+    ([1500, 10, 3, 200, 0, 70, 1], 4, 8, 128, 128, bf16), ([40, 90], 1, 3, 64, 64, f32), ([900, 0, 31, 700, 2], 2, 4, 128, 64, f32),
+    ([3, 1] * 30 + [100], 1, 2, 128, 128, bf16), ([2100, 40, 40, 300], 24, 24, 64, 64, bf16),
+]
+
+
+@pytest.mark.parametrize("case", PACKED, ids=lambda c: "%d_%s" % (len(c[0]), "_".join(map(str, c[1:]))))
+def test_packed(case):
+    x, cu, spans = packed_case(*case, seed=len(case[0]))
+    leaves = [x[n].requires_grad_() for n in ("q", "k", "v", "h0")]
+    o, ht = gdn.chunk_linear_attention(x["q"], x["k"], x["v"], x["g"], initial_state=x["h0"], output_final_state=True, cu_seqlens=cu)
+    grads = torch.autograd.grad([o, ht], leaves, [x["do"], x["dht"]])
+    with torch.no_grad():
+        ref = reference(x, spans, backward=True)
+    verify("o", o, ref["o"], case[5])
+    verify("ht", ht, ref["ht"], case[5])
+    for name, got in zip(("dq", "dk", "dv", "dh0"), grads):
+        verify(name, got, ref[name], case[5])
