@@ -1,7 +1,7 @@
 // linear.cu -- linear attention on the CUDA cores (fp32 inputs; see linear.h for what a run is), and the small
 // kernels around the runs.
 //
-// k_linear: a CTA takes one sequence (or segment of one), head and 64 columns of c, and goes through it in blocks of 32
+// k_linear: a CTA takes one sequence (or segment of one), head and 64 columns of c, and goes through it in blocks of 64
 // tokens with the state [da][64] in shared memory: P = (A B^T) under the decays, O = P C + l^(j + e) A X,
 // X <- l^n X + (w B)^T C.  All in fp32, two at a time; the next block's rows come under a block's work.
 #include <cuda_bf16.h>
@@ -14,7 +14,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int N = 32;     // tokens of a block
+constexpr int N = C;      // tokens of a block
 constexpr int COLS = 64;  // columns of c and the state per CTA
 
 template <int DA> struct Smem {
@@ -106,8 +106,12 @@ template <typename IO, int DA, bool VEC> __global__ void __launch_bounds__(kThre
     const IO *a = static_cast<const IO *>(r.a) + batch * r.sa.batch + h / r.ga * r.sa.head;
     const IO *b = static_cast<const IO *>(r.b) + batch * r.sb.batch + h / r.gb * r.sb.head;
     const IO *c = static_cast<const IO *>(r.c) + batch * r.sc.batch + h / r.gc * r.sc.head + col0;
-    const int ty = tid / 16, tx = tid % 16;  // tiles of 2 x 2 of P, 2 x 4 of O, ROWS x 4 of X
+    // Eight warps, two by four, of eight by four lanes: 4 x 4 of P and O by each thread (rows 8 apart, P's columns 4 apart),
+    // ROWS x 4 of X.  So a read of 16 bytes by a warp meets no bank twice; rows by half warps took twice as many cycles
+    const int wr = tid >> 7, wc = (tid >> 5) & 3, ty = (tid >> 2) & 7, tx = tid & 3;
+    const int j0 = 32 * wr + ty, y0 = 16 * wc + 4 * tx;
     constexpr int ROWS = DA / 16;
+    const int x0 = DA / 2 * wr + ROWS * ty;
     Rows<IO, DA, VEC> ra, rb;
     Rows<IO, COLS, VEC> rc;
     auto fetch = [&](int at) {
@@ -127,83 +131,91 @@ template <typename IO, int DA, bool VEC> __global__ void __launch_bounds__(kThre
         rc.store(&s.c[0][0], COLS);
         __syncthreads();
         if (at + N < to) fetch(at + N);  // arrives under this block's work
-        if (outs) {
-            uint64_t p[2][2] = {};
-#pragma unroll 4
-            for (int x = 0; x < DA; x += 4) {
-                const Four a0 = four(&s.a[2 * ty][x]), a1 = four(&s.a[2 * ty + 1][x]), b0 = four(&s.b[tx][x]), b1 = four(&s.b[tx + 16][x]);
-                p[0][0] = fma2(a0.hi, b0.hi, fma2(a0.lo, b0.lo, p[0][0])), p[0][1] = fma2(a0.hi, b1.hi, fma2(a0.lo, b1.lo, p[0][1]));
-                p[1][0] = fma2(a1.hi, b0.hi, fma2(a1.lo, b0.lo, p[1][0])), p[1][1] = fma2(a1.hi, b1.hi, fma2(a1.lo, b1.lo, p[1][1]));
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const int j = 2 * ty + y, i = tx + 16 * z;
-                    float even, odd;
-                    halves(p[y][z], even, odd);
-                    s.p[j][i] = i <= j ? r.p_scale * s.pow[j - i] * (even + odd) : 0.f;
-                }
-            __syncwarp();  // rows 2 ty and 2 ty + 1 of P are read by the half warp that wrote them
-            uint64_t o[2][2] = {}, q[2][2] = {};
+        if (outs) {  // what lies behind the tokens or before the diagonal is left out
+            if (32 * wr < n && wc < 2 * wr + 2) {
+                uint64_t p[4][4] = {};
 #pragma unroll 2
-            for (int x = 0; x < DA; x += 4) {
-                const float4 a0 = *reinterpret_cast<const float4 *>(&s.a[2 * ty][x]), a1 = *reinterpret_cast<const float4 *>(&s.a[2 * ty + 1][x]);
-                const float av[2][4] = {{a0.x, a0.y, a0.z, a0.w}, {a1.x, a1.y, a1.z, a1.w}};
+                for (int x = 0; x < DA; x += 4) {
+                    Four bb[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const Four xx = four(&s.x[x + k][4 * tx]);
+                    for (int z = 0; z < 4; ++z) bb[z] = four(&s.b[16 * wc + tx + 4 * z][x]);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint64_t aa = pair_of(av[y][k], av[y][k]);
-                        q[y][0] = fma2(aa, xx.lo, q[y][0]), q[y][1] = fma2(aa, xx.hi, q[y][1]);
+                    for (int y = 0; y < 4; ++y) {
+                        const Four aa = four(&s.a[j0 + 8 * y][x]);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) p[y][z] = fma2(aa.hi, bb[z].hi, fma2(aa.lo, bb[z].lo, p[y][z]));
                     }
                 }
-            }
-#pragma unroll 2
-            for (int i = 0; i < N; i += 4) {
-                const float4 p0 = *reinterpret_cast<const float4 *>(&s.p[2 * ty][i]), p1 = *reinterpret_cast<const float4 *>(&s.p[2 * ty + 1][i]);
-                const float pv[2][4] = {{p0.x, p0.y, p0.z, p0.w}, {p1.x, p1.y, p1.z, p1.w}};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const Four cc = four(&s.c[i + k][4 * tx]);
+                for (int y = 0; y < 4; ++y)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint64_t pp = pair_of(pv[y][k], pv[y][k]);
-                        o[y][0] = fma2(pp, cc.lo, o[y][0]), o[y][1] = fma2(pp, cc.hi, o[y][1]);
+                    for (int z = 0; z < 4; ++z) {
+                        const int j = j0 + 8 * y, i = 16 * wc + tx + 4 * z;
+                        float even, odd;
+                        halves(p[y][z], even, odd);
+                        s.p[j][i] = i <= j ? r.p_scale * s.pow[j - i] * (even + odd) : 0.f;
                     }
-                }
             }
+            __syncthreads();
+            if (32 * wr < n) {
+                uint64_t o[4][2] = {};
+                // rows of m by the rows of w, k at a time
+                auto times = [&](const float *m, int pitch, const float *w, int upto) {
+#pragma unroll 2
+                    for (int x = 0; x < upto; x += 4) {
+                        float4 mv[4];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int j = 2 * ty + y;
-                if (j >= n) continue;
-                const float w = r.o_scale * s.pow[j + r.e];
-                const int64_t row = batch * r.T + tok + (r.reverse ? n - 1 - j : j);
-                const int64_t to_at = (row * r.Hv + h) * r.dc + col0 + 4 * tx;
-                const uint64_t ww = pair_of(w, w);
-                float v[4];
-                halves(fma2(ww, q[y][0], o[y][0]), v[0], v[1]);
-                halves(fma2(ww, q[y][1], o[y][1]), v[2], v[3]);
-                if (sizeof(IO) == 4 || r.out_f32) {
-                    *reinterpret_cast<float4 *>(static_cast<float *>(r.out) + to_at) = make_float4(v[0], v[1], v[2], v[3]);
-                } else {
-                    IO *out = static_cast<IO *>(r.out) + to_at;
+                        for (int y = 0; y < 4; ++y) mv[y] = *reinterpret_cast<const float4 *>(m + (j0 + 8 * y) * pitch + x);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) out[z] = from_f<IO>(v[z]);
+                        for (int k = 0; k < 4; ++k) {
+                            const Four ww = four(w + (x + k) * COLS + y0);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const float v = k == 0 ? mv[y].x : k == 1 ? mv[y].y : k == 2 ? mv[y].z : mv[y].w;
+                                const uint64_t vv = pair_of(v, v);
+                                o[y][0] = fma2(vv, ww.lo, o[y][0]), o[y][1] = fma2(vv, ww.hi, o[y][1]);
+                            }
+                        }
+                    }
+                };
+                times(&s.a[0][0], DA + 4, &s.x[0][0], DA);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float w = r.o_scale * s.pow[j0 + 8 * y + r.e];
+                    const uint64_t ww = pair_of(w, w), zero = 0;
+                    o[y][0] = fma2(ww, o[y][0], zero), o[y][1] = fma2(ww, o[y][1], zero);
+                }
+                times(&s.p[0][0], N + 4, &s.c[0][0], 32 * wr + 32);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int j = j0 + 8 * y;
+                    if (j >= n) continue;
+                    const int64_t row = batch * r.T + tok + (r.reverse ? n - 1 - j : j);
+                    const int64_t to_at = (row * r.Hv + h) * r.dc + col0 + y0;
+                    float v[4];
+                    halves(o[y][0], v[0], v[1]), halves(o[y][1], v[2], v[3]);
+                    if (sizeof(IO) == 4 || r.out_f32) {
+                        *reinterpret_cast<float4 *>(static_cast<float *>(r.out) + to_at) = make_float4(v[0], v[1], v[2], v[3]);
+                    } else {
+                        IO *out = static_cast<IO *>(r.out) + to_at;
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) out[z] = from_f<IO>(v[z]);
+                    }
                 }
             }
         }
         __syncthreads();  // X is read
         uint64_t u[ROWS][2] = {};
-#pragma unroll 2
+#pragma unroll 4
         for (int i = 0; i < n; ++i) {
             const float w = r.s_scale * s.pow[n - i - r.e];
-            const Four cc = four(&s.c[i][4 * tx]);
+            const uint64_t w2 = pair_of(w, w), zero = 0;
+            Four cc = four(&s.c[i][y0]);
+            cc.lo = fma2(w2, cc.lo, zero), cc.hi = fma2(w2, cc.hi, zero);
 #pragma unroll
             for (int z = 0; z < ROWS; z += 4) {
-                const float4 bb = *reinterpret_cast<const float4 *>(&s.b[i][ROWS * ty + z]);
-                const float bv[4] = {w * bb.x, w * bb.y, w * bb.z, w * bb.w};
+                const float4 bb = *reinterpret_cast<const float4 *>(&s.b[i][x0 + z]);
+                const float bv[4] = {bb.x, bb.y, bb.z, bb.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint64_t b2 = pair_of(bv[k], bv[k]);
@@ -214,7 +226,7 @@ template <typename IO, int DA, bool VEC> __global__ void __launch_bounds__(kThre
         const float l1 = expm1f(g * n);  // X l^n as X + l1 X: nothing is lost where l is all but 1
 #pragma unroll
         for (int y = 0; y < ROWS; ++y) {
-            float4 &x = *reinterpret_cast<float4 *>(&s.x[ROWS * ty + y][4 * tx]);
+            float4 &x = *reinterpret_cast<float4 *>(&s.x[x0 + y][y0]);
             float v[4];
             halves(u[y][0], v[0], v[1]), halves(u[y][1], v[2], v[3]);
             x.x += fmaf(l1, x.x, v[0]), x.y += fmaf(l1, x.y, v[1]);
