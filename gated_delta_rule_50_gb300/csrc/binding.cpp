@@ -437,7 +437,8 @@ struct Linear {
         if (!t.defined()) return t;
         shaped(t, name, {p.n_seqs, p.Hv, p.K, p.V}, dev);
         if (t.scalar_type() != at::kFloat) type_error(std::string(name) + " must be float32, got " + toString(t.scalar_type()));
-        return t.contiguous();
+        const Tensor c = t.contiguous();
+        return (reinterpret_cast<uintptr_t>(c.data_ptr()) & 15) == 0 ? c : c.clone();
     }
     Tensor new_state() const { return at::detail::empty_cuda({p.n_seqs, p.Hv, p.K, p.V}, at::kFloat, dev, std::nullopt); }
     Tensor workspace(size_t bytes, const char *where) const {

@@ -461,8 +461,11 @@ gdn_status gdn_sample(const gdn_sample_problem *p, const void *logits, const flo
  *     them on the host: a sequence whose offsets fall or leave the T tokens counts as empty.
  *     Rows of the outputs that no sequence claims become 0.
  * Neither call synchronises or allocates; both can be captured in a graph.
+ * Waits of the kernels are bounded (a second); where one ran out, the outputs
+ * and the states that it concerns are NaN.
  * The sequences are split over the GPU where they are few, and joined exactly.
- * bf16: the tensor cores' kernels; fp32: the CUDA cores'.  A token that is not
+ * bf16 whose pointers and strides are multiples of 16 bytes above 0: the tensor
+ * cores' kernels; the rest and fp32: the CUDA cores'.  A token that is not
  * finite reaches those of its own chunk before it, and all that follow it in its
  * sequence, none of another sequence.
  */
