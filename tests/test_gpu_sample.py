@@ -99,3 +99,123 @@ def test_equal_logits(filters, dtype):
     logits[1] = torch.round(logits[1].float() / 4).to(dtype)
     logits[2, : N // 2] = 2.0
     verify(gdn.sample_tokens(logits, u, **filters), logits, u, **filters)
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("N,B", [(1 << 20, 2), (300000, 3), (40000, 200)])
+def test_large(N, B, dtype):
+    """The longest vocabulary (slices that are read again in every pass), and many rows."""
+    logits, u, gen = inputs(B, N, dtype, 5, spread=2.0)
+    kinds = dict(temperature=1.2, top_k=2000, top_p=0.9, min_p=0.001)
+    verify(gdn.sample_tokens(logits, u, **kinds), logits, u, **kinds)
+    verify(gdn.sample_tokens(logits, u, top_p=0.95), logits, u, top_p=0.95)
+
+
+def test_layouts():
+    """Rows of a wider tensor, masks for all rows and for all tokens of a row, parameters of other types."""
+    wide, u, gen = inputs(6, 7001, bf16, 6)
+    logits = wide[:, 3:5004]
+    mask = (torch.rand(1, 5001, generator=gen) < 0.5).cuda()
+    u2 = torch.stack([u, u], 1)[:, 0]
+    heat = torch.full((6,), 0.75, dtype=torch.float64).cuda()
+    k = torch.tensor([1, 5, 2 ** 40, -3, 100, 0]).cuda()
+    got = gdn.sample_tokens(logits, u2, heat, k, 0.875, None, mask)
+    verify(got, logits, u, 0.75, k.clamp(max=10 ** 6).cpu(), 0.875, 0.0, mask)
+    some = torch.tensor([True, False] * 3).cuda().unsqueeze(1)
+    verify(gdn.sample_tokens(logits, u, mask=some), logits, u, mask=some)
+    tight = torch.zeros(6, 5001 + 2, dtype=torch.bool, device="cuda")[:, 1:5002]
+    tight[:, ::3] = True
+    verify(gdn.sample_tokens(logits, u, top_k=50, mask=tight), logits, u, top_k=50, mask=tight)
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+def test_rows_at_their_ends(dtype):
+    N = 3001
+    logits, u, gen = inputs(12, N, dtype, 7)
+    low = torch.finfo(dtype).min
+    logits[0] = -math.inf                       # nothing to choose
+    logits[1, 5] = math.nan
+    logits[2, 6] = math.inf
+    logits[3] = low                             # the type's lowest value everywhere: all alike
+    logits[4, 10:] = low                        # forbidden by that value
+    logits[5, :-1] = -math.inf                  # one choice
+    logits[6] = torch.finfo(dtype).max / 2      # far from 0, and one less
+    logits[6, 7] = low
+    heat = torch.ones(12)
+    heat[7], heat[8], heat[9], heat[10], heat[11] = -1.0, math.nan, math.inf, 1e-30, 1e30
+    got = gdn.sample_tokens(logits, u, heat.cuda(), top_p=0.9)
+    tokens, logprobs = (t.cpu() for t in got)
+    for b in (0, 1, 2, 7, 8, 9):
+        assert tokens[b] == -1 and logprobs[b] == -math.inf
+    rows = [3, 4, 5, 6, 10, 11]
+    verify((tokens[rows], logprobs[rows]), logits[rows], u[rows], heat[rows], top_p=0.9)
+    mask = torch.ones(12, N, dtype=torch.bool)
+    mask[1, 5] = mask[2, 6] = False             # what the mask forbids may hold anything
+    verify([t[1:3] for t in gdn.sample_tokens(logits, u, mask=mask.cuda())], logits[1:3], u[1:3], mask=mask[1:3])
+    for name in ("top_p", "min_p"):
+        assert (gdn.sample_tokens(logits[3:6], u[3:6], **{name: math.nan})[0] == -1).all()
+
+
+@pytest.mark.parametrize("filters", [dict(), dict(top_k=20), dict(top_p=0.9), dict(top_k=2000, top_p=0.99)], ids=str)
+def test_random_numbers_at_their_ends(filters):
+    """0, the largest below 1, what lies outside and no number."""
+    logits, _, _ = inputs(6, 9000, f32, 8)
+    logits[:] = logits[0]
+    u = torch.tensor([0.0, 1 - 2.0 ** -24, 1.0, 7.0, -3.0, math.nan]).cuda()
+    meant = torch.tensor([0.0, 1 - 2.0 ** -24, 1 - 2.0 ** -24, 1 - 2.0 ** -24, 0.0, 0.0])
+    verify(gdn.sample_tokens(logits, u, **filters), logits, meant, **filters)
+
+
+def test_shares_are_what_is_drawn():
+    """Many draws of one row: every token as often as its share says.  A count of n draws of share p is off by more than
+    six of its standard deviations once in 10^9."""
+    logits, _, gen = inputs(1, 40, f32, 9)
+    n = 20000
+    u = ((torch.arange(n) + torch.rand(n, generator=gen)) / n).float().clamp(max=1 - 2.0 ** -24).cuda()
+    tokens, logprobs = gdn.sample_tokens(logits.expand(n, -1), u)
+    p = torch.softmax(logits[0].double().cpu(), 0)
+    count = torch.bincount(tokens.cpu().long(), minlength=40).double()
+    assert ((count - n * p).abs() <= 6 * (n * p * (1 - p)).sqrt() + 2).all()
+    assert torch.allclose(logprobs.cpu().double(), torch.log(p)[tokens.cpu().long()], atol=1e-5)
+
+
+def test_side_stream_and_graph():
+    logits, u, _ = inputs(9, 30000, bf16, 10)
+    kinds = dict(temperature=0.9, top_k=300, top_p=0.95)
+    want = gdn.sample_tokens(logits, u, **kinds)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = gdn.sample_tokens(logits, u, **kinds)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    kept = logits.clone()
+    with torch.cuda.graph(graph):
+        got = gdn.sample_tokens(logits, u, **kinds)
+    logits.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    verify(got, logits, u, **{**kinds})
+    logits.copy_(kept)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_any(seed):
+    """Rows, sizes, spreads and filters at random."""
+    gen = torch.Generator().manual_seed(100 + seed)
+    pick = lambda lo, hi: int(torch.randint(lo, hi, (1,), generator=gen))  # noqa: E731
+    for _ in range(4):
+        B, N = pick(1, 40), pick(1, 30000)
+        dtype = bf16 if pick(0, 2) else f32
+        logits = ((0.1 + 5 * torch.rand(1, generator=gen)) * torch.randn(B, N, generator=gen)).to(dtype)
+        u = torch.rand(B, generator=gen)
+        heat = 0.2 + 2 * torch.rand(B, generator=gen)
+        k = torch.randint(0, 2 * N, (B,), generator=gen).to(torch.int32) if pick(0, 2) else 0
+        p = 0.2 + 0.9 * torch.rand(B, generator=gen) if pick(0, 2) else 1.0
+        m = 0.3 * torch.rand(B, generator=gen) ** 3 if pick(0, 2) else 0.0
+        on = lambda v: v.cuda() if isinstance(v, torch.Tensor) else v  # noqa: E731
+        verify(gdn.sample_tokens(logits.cuda(), u.cuda(), heat.cuda(), on(k), on(p), on(m)), logits, u, heat, k, p, m)
