@@ -1,9 +1,12 @@
-"""Generating from a small model of gated delta rule layers: prefill, beam search, drafted trees.
+"""Generating from a small model of gated delta rule layers, or of linear attention: prefill, sampling, beam search,
+drafted trees.
 
 The model is random (there is nothing to learn here); what it shows is how the calls fit together.  One pool of
 states per layer, a slot per hypothesis:
 
-    prefill      chunk_gated_delta_rule leaves a state per prompt
+    prefill      chunk_gated_delta_rule (chunk_linear_attention) leaves a state per prompt
+    sampling     sample_tokens draws the next token of every row, recurrent_gated_delta_rule
+                 (recurrent_linear_attention) moves the row's state by it
     beam search  recurrent_gated_delta_rule moves every beam by a token, beam_search_step selects,
                  reorder_states lets the states follow the selection
     drafts       tree_gated_delta_rule answers a tree of drafted tokens without touching the states,
@@ -54,16 +57,62 @@ class Model:
         x = torch.nn.functional.rms_norm(x.float(), x.shape[-1:]).to(x.dtype)
         return x @ self.head.t()
 
+    def through(self, *inputs):
+        """(o, final state) of a layer's whole text."""
+        return gdn.chunk_gated_delta_rule(*inputs, output_final_state=True)
+
+    def step(self, state, *inputs):
+        """o of a token or a few behind the states, which are moved."""
+        return gdn.recurrent_gated_delta_rule(*inputs, state)
+
     def prefill(self, tokens):
         """(logits of all tokens, a state per prompt and layer [B, Hv, K, V])."""
         states = []
 
         def mix(layer, *inputs):
-            o, state = gdn.chunk_gated_delta_rule(*inputs, output_final_state=True)
+            o, state = self.through(*inputs)
             states.append(state)
             return o
 
         return self.forward(tokens, mix), states
+
+    def further(self, tokens, states):
+        """Logits [B, T, vocab] of tokens [B, T] behind the states, which are moved."""
+        return self.forward(tokens, lambda layer, *inputs: self.step(states[layer], *inputs))
+
+
+class LinearModel(Model):
+    """The same with linear attention: head i of n forgets by 1 - 2^(-1 - 8 i / n) a token."""
+
+    def inputs(self, layer, x):
+        q, k, v, _, _ = super().inputs(layer, x)
+        heads = torch.arange(self.Hv, device="cuda", dtype=torch.float64)
+        return q, k, v, torch.log1p(-torch.exp2(-1 - 8 * heads / self.Hv)).float()
+
+    def through(self, *inputs):
+        return gdn.chunk_linear_attention(*inputs, output_final_state=True)
+
+    def step(self, state, *inputs):
+        return gdn.recurrent_linear_attention(*inputs, state)
+
+
+@torch.no_grad()
+def generate(model, prompt, steps=8, copies=1, seed=0, **filters):
+    """`copies` drawn continuations of every prompt [B, T]: (tokens [B, copies, steps], the logarithms of their shares,
+    the same).  filters: what sample_tokens takes, temperature, top_k, top_p, min_p, mask."""
+    B = prompt.shape[0]
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    logits, states = model.prefill(prompt)
+    states = [s.repeat_interleave(copies, 0) for s in states]  # slot b * copies + i
+    logits = logits[:, -1].repeat_interleave(copies, 0)
+    tokens, shares = [], []
+    for step in range(steps):
+        if step:
+            logits = model.further(tokens[-1].unsqueeze(1), states)[:, -1]
+        token, share = gdn.sample_tokens(logits, torch.rand(B * copies, device="cuda", generator=gen), **filters)
+        tokens.append(token)
+        shares.append(share)
+    return torch.stack(tokens, 1).view(B, copies, steps), torch.stack(shares, 1).view(B, copies, steps)
 
 
 @torch.no_grad()
@@ -85,8 +134,7 @@ def beam_search(model, prompt, beams=4, steps=8, end=None):
         chosen = torch.cat([chosen.gather(1, at.unsqueeze(-1).expand(-1, -1, step)), tokens.unsqueeze(-1)], dim=-1)
         finished = finished.gather(1, at) | (tokens == (-2 if end is None else end))
         if step + 1 < steps:  # finished beams run along: what they would say is not looked at
-            logits = model.forward(tokens.clamp(min=0).view(B * beams, 1),
-                                   lambda layer, *x: gdn.recurrent_gated_delta_rule(*x, states[layer])).view(B, beams, -1)
+            logits = model.further(tokens.clamp(min=0).view(B * beams, 1), states).view(B, beams, -1)
     return chosen, scores
 
 
@@ -122,6 +170,9 @@ def main():
     tokens, scores = beam_search(model, prompt, beams=4, steps=6)
     for b in range(3):
         print("prompt", b, "best:", tokens[b, 0].tolist(), "score %.3f" % scores[b, 0].item())
+    for kind in (model, LinearModel()):
+        tokens, shares = generate(kind, prompt, steps=6, temperature=0.8, top_k=50, top_p=0.95)
+        print(type(kind).__name__, "draws:", tokens[0, 0].tolist(), "logarithm of its share %.3f" % shares[0, 0].sum().item())
     # drafts for every row: the right next tokens in one branch, wrong ones beside it
     greedy, _ = beam_search(model, prompt, beams=1, steps=3)
     logits, states = model.prefill(prompt)
