@@ -78,6 +78,24 @@ __device__ __forceinline__ void tmem_ld_fragments(uint32_t ta, uint32_t (&a)[16]
         : "memory");
 }
 #undef GDN_R8
+// Two stores of 16 lanes x 32 columns, waited: thread t gives, of every four columns, t % 4 of lane t / 4 and of lane t / 4 + 8
+#define GDN_S8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+__device__ __forceinline__ void tmem_st_fragments(uint32_t ta, const uint32_t (&a)[16], uint32_t tb, const uint32_t (&b)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};\n\t"
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%33], {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::GDN_S8(a, 0), GDN_S8(a, 8), GDN_S8(b, 0), GDN_S8(b, 8), "r"(ta), "r"(tb)
+        : "memory");
+}
+#undef GDN_S8
+// Four 8 x 8 matrices of 16-bit values; lane l gives row l % 8 of matrix l / 8.  Loaded with rows and columns exchanged, and
+// stored as they are
+__device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t (&x)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void store_rows(uint32_t addr, const uint32_t (&x)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+}
 // Four 8 x 8 matrices of bf16 fragments, stored with rows and columns exchanged; lane l gives row l % 8 of matrix l / 8
 __device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -536,47 +554,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             }
         }
     } else if (warp >= W_W0) {
-        // w c: column y of c
-        const int quarter = warp & 3, y = 32 * quarter + lane;
+        // w c: columns 32 quarter .. of c, as matrix fragments: a lane has, of eight tokens and each of four times eight columns,
+        // tokens 2 (lane % 4) and the next one of column lane / 4, which is how 16 lanes of TMEM take 128 bits each
+        const int quarter = warp & 3, row = lane & 7;
         const uint32_t t_w = tmem + ((uint32_t)(32 * quarter) << 16) + TM_WH;
-        const uint32_t c_at = sb + C_OFF + (uint32_t)(y >> 6) * BOX + (uint32_t)(y & 7) * 2;
-        uint32_t piece[8];  // where the column lies in rows 0 .. 7 (mod 8)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) piece[i] = (uint32_t)(i * 128) + ((uint32_t)(((y & 63) >> 3) ^ i) << 4);
+        const uint32_t c_at = sb + C_OFF + (uint32_t)(quarter >> 1) * BOX + (uint32_t)(row * 128 + ((((quarter & 1) * 4 + (lane >> 3)) ^ row) << 4));
+        const uint32_t w3_at = sb + SM_W3 + (uint32_t)((32 * quarter + lane) * 128);
 #pragma unroll 1
         for (int j = 0; 32 * quarter < r.dc && j < updates; ++j) {
             if (!wait_for(bar(FULL0 + j % kStages), (j / kStages) & 1, abort_flag)) break;
-            const uint32_t c = c_at + (uint32_t)(j % kStages) * STAGE, w3 = sb + SM_W3 + (j & 1) * 2 * BOX;
-            const float *up = tab.up[j + 1 < nck ? 0 : 1];
-            uint32_t hi[32], lo[32];
+            const uint32_t c = c_at + (uint32_t)(j % kStages) * STAGE, w3 = w3_at + (j & 1) * 2 * BOX;
+            const uint64_t *up = reinterpret_cast<const uint64_t *>(tab.up[j + 1 < nck ? 0 : 1]) + (lane & 3);
+            uint32_t hi[2][16], lo[2][16];  // of columns 0 .. 15 and 16 .. 31
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // 16 tokens
-                float w[16];
-                uint32_t rest[8];
-                lds16f(up + 16 * q, w);
+            for (int m = 0; m < 8; ++m) {  // eight tokens
+                uint32_t x[4], rest[4];
+                load_transposed(c + m * 1024, x);
+                const uint64_t w = up[4 * m];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint16_t v0, v1;
-                    const int t = 16 * q + 2 * i;
-                    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v0) : "r"(c + (t >> 3) * 1024 + piece[t & 7]));
-                    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v1) : "r"(c + (t >> 3) * 1024 + piece[(t + 1) & 7]));
-                    uint64_t x = mul2(pair_of(__uint_as_float((uint32_t)v0 << 16), __uint_as_float((uint32_t)v1 << 16)), pair_of(w[2 * i], w[2 * i + 1]));
-                    hi[8 * q + i] = take_bf16(x);
-                    if (THIRD) lo[8 * q + i] = take_bf16(x), rest[i] = last_bf16(x);
-                    else lo[8 * q + i] = last_bf16(x);
+                for (int n = 0; n < 4; ++n) {
+                    uint64_t v = mul2(pair_of(__uint_as_float(x[n] << 16), __uint_as_float(x[n] & 0xFFFF0000u)), w);
+                    uint32_t &h = hi[n >> 1][2 * m + (n & 1)], &l = lo[n >> 1][2 * m + (n & 1)];
+                    h = take_bf16(v);
+                    if (THIRD) l = take_bf16(v), rest[n] = last_bf16(v);
+                    else l = last_bf16(v);
                 }
-                if (THIRD) {  // into the buffer whose reader, U(j - 2), is done: it was waited for before the last W was stored
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        st_shared_v4(sw128_addr(w3, y, 2 * q + k), rest[4 * k], rest[4 * k + 1], rest[4 * k + 2], rest[4 * k + 3]);
-                }
+                // into the buffer whose reader, U(j - 2), is done: it was waited for before the last W was stored
+                if (THIRD) store_rows(w3 + ((uint32_t)(m ^ row) << 4), rest);
             }
             if (THIRD) fence_proxy_async_smem();
             if (j > 0 && !wait_for(bar(UDONE), (j - 1) & 1, abort_flag)) break;
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                tmem_st16x2(t_w + 16 * k, reinterpret_cast<uint32_t(&)[16]>(hi[16 * k]), t_w + (TM_WL - TM_WH) + 16 * k, reinterpret_cast<uint32_t(&)[16]>(lo[16 * k]));
+            tmem_st_fragments(t_w, hi[0], t_w + (TM_WL - TM_WH), lo[0]);
+            tmem_st_fragments(t_w + (16u << 16), hi[1], t_w + (16u << 16) + (TM_WL - TM_WH), lo[1]);
             tc_fence_before();
             mbar_arrive_warp(bar(WREADY));
         }
