@@ -32,11 +32,18 @@ gdn_status problem_ok(const gdn_linear_problem *p) {
 // Into how many segments sequences are cut.  A head of a sequence keeps one SM busy; where these are fewer than the SMs,
 // each is cut so that they fill them.  Every token's part in the state is then taken twice, and there are two launches more.
 // Measured on the tensor cores, us: 2.2 a chunk and 6 for whole ones, 1.5 + 2.2 a chunk of a segment and 16 for cut ones.
+// On the CUDA cores a head is a CTA for every 64 columns of V, of which an SM holds two where K is 64, and one where it is
+// 128; a chunk takes 9 us (64 x 64) to 15 (128 x 128), its part in the state some 0.6 of that, the launches and the join as
+// much as a chunk.  (2 x 1000 tokens, 8 heads: 64 x 64 146 us whole and 35 cut, 128 x 128 236 and 90; 1 x 200: 35 and 29, 56
+// and 31; near the border 4 x 300 of 24 heads, 64 x 64, gain 22 % forward and lose 18 % backward.)
 int segments(const gdn_linear_problem *p) {
-    const int64_t chains = p->n_seqs * p->Hv, chunks = (p->T + C - 1) / C;
-    if (chains == 0 || chains > kSMs / 2) return 1;
-    const int64_t n = std::min(kSMs / chains, chunks), each = n ? (chunks + n - 1) / n : 0;
-    return n > 1 && 3.7 * each + 16 < 2.2 * chunks + 6 ? (int)((chunks + each - 1) / each) : 1;
+    const bool f32 = p->io_dtype == GDN_F32;
+    const int64_t chains = p->n_seqs * p->Hv, chunks = (p->T + C - 1) / C, room = f32 ? kSMs * 8192 / (p->K * p->V) : kSMs;
+    if (chains == 0 || chains > room / 2) return 1;
+    const int64_t n = std::min(room / chains, chunks), each = n ? (chunks + n - 1) / n : 0;
+    if (n <= 1) return 1;
+    const bool cut = f32 ? 1.6 * each + 1 < chunks : 3.7 * each + 16 < 2.2 * chunks + 6;
+    return cut ? (int)((chunks + each - 1) / each) : 1;
 }
 
 struct Layout {
