@@ -404,3 +404,32 @@ def test_misaligned_rows_in_c():
     ref = reference(x, backward=True)
     for name, got in zip(("o", "ht", "dq", "dk", "dv", "dh0"), [o, ht] + out):
         verify(name, got, ref[name], bf16)
+
+
+@pytest.mark.parametrize("case", [(2, 1000, 4, 8, 64, 64), (1, 200, 4, 8, 128, 128), (1, 193, 2, 4, 128, 64), (1, 260, 1, 2, 64, 128)], ids=str)
+def test_fp32_in_segments(case):
+    x = make(*case, f32, seed=19)
+    leaves = [x[n].requires_grad_() for n in ("q", "k", "v", "h0")]
+    o, ht = call(x)
+    grads = torch.autograd.grad([o, ht], leaves, [x["do"], x["dht"]])
+    with torch.no_grad():
+        ref = reference(x, backward=True)
+    for name, got in zip(("o", "ht", "dq", "dk", "dv", "dh0"), (o, ht) + grads):
+        verify(name, got, ref[name], f32)
+
+
+@pytest.mark.parametrize("dtype", [bf16, f32])
+def test_sequences_that_are_one(dtype):
+    """Offsets that name the same tokens twice, of sequences that would each be cut: more segments than there can be."""
+    T = 6000
+    x = make(1, T, 2, 32 if dtype == bf16 else 8, 64, 64, dtype, seed=20, h0=False)
+    cu = torch.tensor([0, T, 0, T, 0], device="cuda")
+    o, ht = gdn.chunk_linear_attention(x["q"], x["k"], x["v"], x["g"], output_final_state=True, cu_seqlens=cu)
+    one, state = gdn.chunk_linear_attention(x["q"], x["k"], x["v"], x["g"], output_final_state=True)
+    # two answers, each off by its tolerance and its rounding
+    tol, half = (FP32_TOL, 2.0 ** -24) if dtype == f32 else (BF16_TOL, 2.0 ** -8)
+    a, b = o.double(), one.double()
+    assert ((a - b).abs() <= 2 * (tol * b.square().mean().sqrt() + half * torch.maximum(a.abs(), b.abs()))).all()
+    for n in (0, 2):
+        check("ht", ht[n], state[0], f32, f32, tol=2 * FP32_TOL)
+    assert (ht[1] == 0).all() and (ht[3] == 0).all()
