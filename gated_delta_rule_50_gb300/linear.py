@@ -14,6 +14,9 @@ those of ``chunk_gated_delta_rule``, so that both kinds of layers share a model'
     cu_seqlens [N+1]               B = 1: the sequences' offsets, read on the GPU alone.  A sequence whose offsets fall or leave the
                                    T tokens counts as empty; rows outside every sequence are 0 in all outputs
 
+A NaN or an infinity in a token reaches the outputs of its sequence's chunk of 64 tokens and of what comes behind it, and no
+other sequence.
+
 The calls go through the extension module (``csrc/binding.cpp``), synchronise nothing and read nothing back, so that they can be
 captured in a CUDA graph.
 """
