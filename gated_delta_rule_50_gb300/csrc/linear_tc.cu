@@ -62,14 +62,16 @@ struct Tables {
 };
 constexpr uint32_t SM_BAR = SM_TAB + (uint32_t)sizeof(Tables);
 enum {
-    FULL0 = 0, EMPTY0 = FULL0 + kStages, TAIL = EMPTY0 + kStages, PDONE, PREAD, PREADY0, PREADY1, WREADY, UDONE, XREADY, IDONE, ODONE, FINAL, BARRIERS
+    FULL0 = 0, EMPTY0 = FULL0 + kStages, TAIL = EMPTY0 + kStages, PDONE, PREAD, PREADY0, PREADY1, WREADY0, WREADY1, UDONE0, UDONE1, XREADY, IDONE, ODONE, FINAL, BARRIERS
 };
 constexpr uint32_t SM_MISC = SM_BAR + 8 * 32;
 constexpr uint32_t SMEM_BYTES = SM_MISC + 64 + 1024;
 static_assert(BARRIERS <= 32 && SMEM_BYTES <= 232448, "shared memory");
 
 // TMEM columns
-constexpr uint32_t TM_XH = 0, TM_XL = 64, TM_U = 128, TM_P = 256, TM_I = 320, TM_O = 384, TM_WH = 448, TM_WL = 480;
+constexpr uint32_t TM_XH = 0, TM_XL = 64, TM_U = 128, TM_P = 256, TM_I = 320, TM_O = 384, TM_W = 448, TM_WL = 32;
+// Where only the state is wanted, P, I, O and X are not there, and U and W have second buffers in their place
+constexpr uint32_t TM_U1 = 256, TM_W1 = 0;
 
 constexpr uint32_t ID_N64 = idesc_bf16(128, 64, 0, 0), ID_N64_AMN = idesc_bf16(128, 64, 1, 0);
 
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
     if (threadIdx.x == 0) {
         // of 64 columns only half of these warps have any
         const uint32_t x = r.dc == 128 ? kMainWarps : kMainWarps / 2, w = x + (r.dc == 128 ? kWWarps : kWWarps / 2);
-        const uint32_t counts[BARRIERS] = {1, 1, 1, 1, 1, 1, 1, 1, 2, 2, 2, w, 1, x, 1, 1, 1};
+        const uint32_t counts[BARRIERS] = {1, 1, 1, 1, 1, 1, 1, 1, 2, 2, 2, w, w, 1, 1, x, 1, 1, 1};
         for (int i = 0; i < BARRIERS; ++i) mbar_init(bar(i), counts[i]);
         misc[1] = 0;
         fence_mbar_init();
@@ -262,6 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
     const float *init = live && r.init ? r.init + unit * words : nullptr;
     float *fin = live && r.fin ? r.fin + unit * words : nullptr, *seg = r.seg + ((int64_t)slot * r.Hv + h) * words;
     constexpr bool outs = OUT != NO_OUT, F32OUT = OUT == F32_OUT;
+    // The buffer of U(j) and w c(j), how often it has been used before, and the chunk that takes it next
+    auto buffer = [](int j) { return outs ? 0 : j & 1; };
+    auto turn = [](int j) { return outs ? j : j >> 1; };
+    constexpr int kNext = outs ? 1 : 2;
     if (r.mode == LIN_SEG) {  // the last segment feeds no other
         live = live && c1 < span.chunks && c0 < c1;
         init = nullptr, fin = seg, fin_t = false;
@@ -366,14 +372,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             for (int j = 0; ok && j < nck; ++j) {
                 const uint32_t ph = j & 1, at = stage(j);
                 if (j < updates) {
-                    if (!(ok = wait(WREADY, ph))) break;
+                    if (!(ok = wait(WREADY0 + buffer(j), turn(j) & 1))) break;
                     tc_fence_after();
                     constexpr uint32_t ID_U = idesc_bf16(128, DA, 0, 1);
-                    const uint32_t b = desc(at + B_OFF, KB);
-                    products_ta<ID_U, false, 128>(tm + TM_U, tm + TM_WH, b);
-                    products_ta<ID_U, true, 128>(tm + TM_U, tm + TM_WL, b);
-                    if (THIRD) products<ID_U, true, 2, 128>(tm + TM_U, desc(sb + SM_W3 + ph * 2 * BOX, 16), b);
-                    mma_commit(bar(UDONE));
+                    const uint32_t b = desc(at + B_OFF, KB), u = tm + (buffer(j) ? TM_U1 : TM_U), w = tm + (buffer(j) ? TM_W1 : TM_W);
+                    products_ta<ID_U, false, 128>(u, w, b);
+                    products_ta<ID_U, true, 128>(u, w + TM_WL, b);
+                    if (THIRD) products<ID_U, true, 2, 128>(u, desc(sb + SM_W3 + ph * 2 * BOX, 16), b);
+                    mma_commit(bar(UDONE0 + buffer(j)));
                 }
                 if (j + 1 < nck) {
                     if (!(ok = full(j + 1)) || (outs && !(ok = wait(PREAD, ph)))) break;
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
         auto wait = [&](int id, int use) { return wait_for(bar(id), use & 1, abort_flag); };
         if (32 * quarter < r.dc) {
             constexpr int HALF = DA / 2;
-            const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16), t_x = trow + TM_XH + HALF / 2 * hh, t_u = trow + TM_U + HALF * hh,
+            const uint32_t trow = tmem + ((uint32_t)(32 * quarter) << 16), t_x = trow + TM_XH + HALF / 2 * hh, t_u = trow + HALF * hh,
                            t_io = trow + TM_I + 32 * hh;
             unsigned char *staged = sm + SM_OUT + 2048 * (warp - W_MAIN0);
             uint64_t X[HALF / 2];
@@ -422,17 +428,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             }
             // X l^n as X + (l^n - 1) X: nothing is lost where l is all but 1; any chunk but the last has C tokens
             const float l1_full = expm1f(g * (float)C), l1_last = nck > 0 ? expm1f(g * (float)tokens(nck - 1)) : 0.f;
-            // X takes U (and says that it is read), and goes to TMEM as hi and lo
-            auto advance = [&](bool update, float l1, bool say, bool store) {
+            // X takes U(i), if i is not -1 (and says that the buffer is free), and goes to TMEM as hi and lo
+            auto advance = [&](int i, float l1, bool store) {
+                const bool update = i >= 0;
                 const uint64_t l2 = pair_of(l1, l1);
+                const uint32_t from = t_u + (buffer(i) ? TM_U1 : TM_U);
 #pragma unroll
                 for (int q = 0; q < HALF / 32; ++q) {
                     if (update) {
                         uint32_t u[32];
-                        tmem_ld32(t_u + 32 * q, u);
-                        if (q + 1 == HALF / 32 && say) {
+                        tmem_ld32(from + 32 * q, u);
+                        if (q + 1 == HALF / 32 && i + kNext < updates) {
                             tc_fence_before();
-                            mbar_arrive_warp(bar(WREADY));
+                            mbar_arrive_warp(bar(WREADY0 + buffer(i + kNext)));
                         }
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -525,12 +533,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
 #pragma unroll 1
             for (int j = 0; j < nck; ++j) {
                 if (j > 0) {  // I(j - 1) ends after U(j - 1)
-                    if (!(ok = wait(outs ? IDONE : UDONE, j - 1))) break;
+                    if (!(ok = outs ? wait(IDONE, j - 1) : wait(UDONE0 + buffer(j - 1), turn(j - 1)))) break;
                     tc_fence_after();
-                } else if (updates > 0) {
-                    mbar_arrive_warp(bar(WREADY));
+                } else {
+                    for (int i = 0; i < kNext && i < updates; ++i) mbar_arrive_warp(bar(WREADY0 + buffer(i)));
                 }
-                advance(j > 0, l1_full, j < updates, outs);
+                advance(j - 1, l1_full, outs);
                 if (!outs) continue;
                 if (j > 0) {
                     if (!(ok = wait(ODONE, j - 1))) break;
@@ -541,9 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
                     mbar_arrive_warp(bar(XREADY));
                 }
             }
-            if (ok && nck > 0 && updates == nck && (ok = wait(UDONE, nck - 1))) {
+            if (ok && nck > 0 && updates == nck && (ok = wait(UDONE0 + buffer(nck - 1), turn(nck - 1)))) {
                 tc_fence_after();
-                advance(true, l1_last, false, false);
+                advance(nck - 1, l1_last, false);
             }
             if (ok && nck > 0 && outs && wait(ODONE, nck - 1)) {
                 tc_fence_after();
@@ -566,12 +574,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
         // w c: columns 32 quarter .. of c, as matrix fragments: a lane has, of eight tokens and each of four times eight columns,
         // tokens 2 (lane % 4) and the next one of column lane / 4, which is how 16 lanes of TMEM take 128 bits each
         const int quarter = warp & 3, row = lane & 7;
-        const uint32_t t_w = tmem + ((uint32_t)(32 * quarter) << 16) + TM_WH;
+        const uint32_t t_w = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t c_at = sb + C_OFF + (uint32_t)(quarter >> 1) * BOX + (uint32_t)(row * 128 + ((((quarter & 1) * 4 + (lane >> 3)) ^ row) << 4));
         const uint32_t w3_at = sb + SM_W3 + (uint32_t)((32 * quarter + lane) * 128);
 #pragma unroll 1
         for (int j = 0; 32 * quarter < r.dc && j < updates; ++j) {
             if (!wait_for(bar(FULL0 + j % kStages), (j / kStages) & 1, abort_flag)) break;
+            // the buffer's last reader is U(j - 1), or U(j - 2)
+            auto readable = [&] { return j < kNext || wait_for(bar(UDONE0 + buffer(j)), turn(j - kNext) & 1, abort_flag); };
+            if (!outs && !readable()) break;
             const uint32_t c = c_at + (uint32_t)(j % kStages) * STAGE, w3 = w3_at + (j & 1) * 2 * BOX;
             const uint64_t *up = reinterpret_cast<const uint64_t *>(tab.up[j + 1 < nck ? 0 : 1]) + (lane & 3);
             uint32_t hi[2][16], lo[2][16];  // of columns 0 .. 15 and 16 .. 31
@@ -592,12 +603,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
                 if (THIRD) store_rows(w3 + ((uint32_t)(m ^ row) << 4), rest);
             }
             if (THIRD) fence_proxy_async_smem();
-            if (j > 0 && !wait_for(bar(UDONE), (j - 1) & 1, abort_flag)) break;
+            if (outs && !readable()) break;
             tc_fence_after();
-            tmem_st_fragments(t_w, hi[0], t_w + (TM_WL - TM_WH), lo[0]);
-            tmem_st_fragments(t_w + (16u << 16), hi[1], t_w + (16u << 16) + (TM_WL - TM_WH), lo[1]);
+            const uint32_t to = t_w + (buffer(j) ? TM_W1 : TM_W);
+            tmem_st_fragments(to, hi[0], to + TM_WL, lo[0]);
+            tmem_st_fragments(to + (16u << 16), hi[1], to + (16u << 16) + TM_WL, lo[1]);
             tc_fence_before();
-            mbar_arrive_warp(bar(WREADY));
+            mbar_arrive_warp(bar(WREADY0 + buffer(j)));
         }
     } else {
         // P~: row y of the chunk, 32 columns that its own row cuts off and, for one of the two warps, 32 before them
