@@ -77,7 +77,7 @@ template <typename IO, int D, bool VEC> struct Rows {
     }
 };
 
-template <typename IO, int DA, bool VEC> __global__ void __launch_bounds__(kThreads) k_linear(const __grid_constant__ LinearRun r) {
+template <typename IO, int DA, bool VEC> __global__ void __launch_bounds__(kThreads, DA == 64 ? 2 : 0) k_linear(const __grid_constant__ LinearRun r) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem<DA> &s = *reinterpret_cast<Smem<DA> *>(smem_raw);
     wait_for_previous();
@@ -124,6 +124,7 @@ template <typename IO, int DA, bool VEC> __global__ void __launch_bounds__(kThre
         rb.load(b + tok * r.sb.token, r.sb.token, n, r.reverse);
         rc.load(c + tok * r.sc.token, r.sc.token, n, r.reverse);
     };
+    LinearDecay whole(g * N);
     if (from < to) fetch(from);
     for (int at = from; at < to; at += N) {
         const int n = min(N, to - at);
@@ -226,14 +227,14 @@ template <typename IO, int DA, bool VEC> __global__ void __launch_bounds__(kThre
                 }
             }
         }
-        const float l1 = expm1f(g * n);  // X l^n as X + l1 X: nothing is lost where l is all but 1
+        const float f = n == N ? whole.next() : LinearDecay(g * n).f;
 #pragma unroll
         for (int y = 0; y < ROWS; ++y) {
             float4 &x = *reinterpret_cast<float4 *>(&s.x[x0 + y][y0]);
             float v[4];
             halves(u[y][0], v[0], v[1]), halves(u[y][1], v[2], v[3]);
-            x.x += fmaf(l1, x.x, v[0]), x.y += fmaf(l1, x.y, v[1]);
-            x.z += fmaf(l1, x.z, v[2]), x.w += fmaf(l1, x.w, v[3]);
+            x.x = fmaf(f, x.x, v[0]), x.y = fmaf(f, x.y, v[1]);
+            x.z = fmaf(f, x.z, v[2]), x.w = fmaf(f, x.w, v[3]);
         }
     }
     __syncthreads();
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ LinearRun 
     if (span.segs < 2) return;
     const int64_t unit = (int64_t)seq * r.Hv + h;
     const float g = r.g ? r.g[h] : 0.f;
-    const float l1 = expm1f(g * (float)(span.per_seg * C));
+    const LinearDecay first(g * (float)(span.per_seg * C));
     const int64_t next = (int64_t)r.Hv * words;  // of the next segment
     for (int i = (blockIdx.y * 256 + threadIdx.x) * 4; i < words; i += gridDim.y * 1024) {
         const int x = i / r.dc, y = i % r.dc;
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ LinearRun 
             if (r.transposed) X = make_float4(init[y * r.da + x], init[(y + 1) * r.da + x], init[(y + 2) * r.da + x], init[(y + 3) * r.da + x]);
             else X = *reinterpret_cast<const float4 *>(init + i);
         }
+        LinearDecay decay = first;
         float *seg = r.seg + ((int64_t)span.slot * r.Hv + h) * words + i;
         for (int p0 = 0; p0 + 1 < span.segs; p0 += AHEAD) {  // all but the last are full
             float4 add[AHEAD];
@@ -296,8 +298,9 @@ __global__ void __launch_bounds__(256) k_join(const __grid_constant__ LinearRun 
             for (int p = 0; p < AHEAD; ++p) {
                 if (p0 + p + 1 >= span.segs) break;
                 if (p0 + p > 0) *reinterpret_cast<float4 *>(seg + (p0 + p) * next) = X;
-                X.x += fmaf(l1, X.x, add[p].x), X.y += fmaf(l1, X.y, add[p].y);
-                X.z += fmaf(l1, X.z, add[p].z), X.w += fmaf(l1, X.w, add[p].w);
+                const float f = decay.next();
+                X.x = fmaf(f, X.x, add[p].x), X.y = fmaf(f, X.y, add[p].y);
+                X.z = fmaf(f, X.z, add[p].z), X.w = fmaf(f, X.w, add[p].w);
             }
         }
         *reinterpret_cast<float4 *>(seg + (span.segs - 1) * next) = X;

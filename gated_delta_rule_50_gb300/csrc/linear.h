@@ -97,6 +97,28 @@ __device__ __forceinline__ LinearSpan linear_place(const LinearRun &r, int slot,
     return x;
 }
 
+// What a state is moved on by, again and again, over n tokens: X <- f X + U with f = l^n, at = g n.  One product and one sum:
+// X + (l^n - 1) X would leave, where l^n is small, what X was rounded by, which may be more than all of U.  Where l is all but
+// 1, f rounded would be off by up to 2^-25 every time, and always to the same side: 1e-5 after 300 chunks.  So each f is one
+// of the two fp32 numbers around l^n, and `owed`, which is what the ones before it left out, says which: their product stays
+// within 2^-23 of what it should be, however many there are.
+struct LinearDecay {
+    float f, left, owed;  // l^n = f + left
+    __device__ __forceinline__ explicit LinearDecay(float at) {
+        const float less = expm1f(at);
+        const bool near = fabsf(less) < 0.5f;  // else states are soon gone, or grow: f as it is
+        f = near ? 1.f + less : expf(at);
+        left = near ? less - (f - 1.f) : 0.f;
+        owed = 0.f;
+    }
+    __device__ __forceinline__ float next() {
+        owed += left;
+        const float now = f + owed;
+        owed -= now - f;
+        return now;
+    }
+};
+
 // The tensor cores' kernel: bf16, rows on 16-byte boundaries.  What it does not take, the CUDA cores' does
 bool linear_tc_supported(const LinearRun &r, gdn_dtype io);
 cudaError_t launch_linear_tc(const LinearRun &r, cudaStream_t st);

@@ -155,11 +155,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
@@ -426,12 +421,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
                 }
                 X[i] = pair_of(v0, v1);
             }
-            // X l^n as X + (l^n - 1) X: nothing is lost where l is all but 1; any chunk but the last has C tokens
-            const float l1_full = expm1f(g * (float)C), l1_last = nck > 0 ? expm1f(g * (float)tokens(nck - 1)) : 0.f;
+            LinearDecay whole(g * (float)C);  // of any chunk but the last
             // X takes U(i), if i is not -1 (and says that the buffer is free), and goes to TMEM as hi and lo
-            auto advance = [&](int i, float l1, bool store) {
+            auto advance = [&](int i, float f, bool store) {
                 const bool update = i >= 0;
-                const uint64_t l2 = pair_of(l1, l1);
+                const uint64_t f2 = pair_of(f, f);
                 const uint32_t from = t_u + (buffer(i) ? TM_U1 : TM_U);
 #pragma unroll
                 for (int q = 0; q < HALF / 32; ++q) {
@@ -444,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
                         }
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            X[16 * q + i] = add2(X[16 * q + i], fma2(l2, X[16 * q + i], pair_of(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))));
+                            X[16 * q + i] = fma2(f2, X[16 * q + i], pair_of(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])));
                     }
                     if (store) {
                         uint32_t xh[16], xl[16];
@@ -532,13 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             bool ok = true;
 #pragma unroll 1
             for (int j = 0; j < nck; ++j) {
+                const float f = j > 0 ? whole.next() : 0.f;
                 if (j > 0) {  // I(j - 1) ends after U(j - 1)
                     if (!(ok = outs ? wait(IDONE, j - 1) : wait(UDONE0 + buffer(j - 1), turn(j - 1)))) break;
                     tc_fence_after();
                 } else {
                     for (int i = 0; i < kNext && i < updates; ++i) mbar_arrive_warp(bar(WREADY0 + buffer(i)));
                 }
-                advance(j - 1, l1_full, outs);
+                advance(j - 1, f, outs);
                 if (!outs) continue;
                 if (j > 0) {
                     if (!(ok = wait(ODONE, j - 1))) break;
@@ -551,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             }
             if (ok && nck > 0 && updates == nck && (ok = wait(UDONE0 + buffer(nck - 1), turn(nck - 1)))) {
                 tc_fence_after();
-                advance(nck - 1, l1_last, false);
+                advance(nck - 1, LinearDecay(g * (float)tokens(nck - 1)).f, false);
             }
             if (ok && nck > 0 && outs && wait(ODONE, nck - 1)) {
                 tc_fence_after();
