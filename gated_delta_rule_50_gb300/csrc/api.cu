@@ -16,7 +16,7 @@ using namespace gdn;
 
 namespace {
 
-// Test aid of gdn_debug_set_wait: the forward chain's wait limit (0: the default) and dropped load.
+// Test aid of gdn_debug_set_wait: the forward chain's wait limit (0: the default) and the dropped load.
 std::atomic<long long> g_dbg_wait_ns{0};
 std::atomic<int> g_dbg_drop_chunk{-1};
 constexpr unsigned long long kDefaultWaitNs = 1000000000ull;
@@ -299,6 +299,8 @@ gdn_status bwd_saved_impl(Plan pl, const void *q, const void *k, const void *v, 
                           float *dh0, void *workspace, cudaStream_t st);
 
 }  // namespace
+
+int gdn::debug_drop_chunk() { return g_dbg_drop_chunk.load(); }
 
 extern "C" {
 

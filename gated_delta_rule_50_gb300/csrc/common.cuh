@@ -40,6 +40,8 @@ struct Plan {
     int drop_load_chunk;
 };
 
+int debug_drop_chunk();  // what gdn_debug_set_wait asked for: a chunk whose load is skipped (-1: none)
+
 struct SeqRange { int tok0, tok1, c0, c1; };  // token span and global chunk span
 
 __host__ __device__ inline SeqRange seq_range(const Plan &p, int s) {

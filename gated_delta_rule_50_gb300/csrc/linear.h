@@ -41,6 +41,7 @@ struct LinearRun {
     // Segments have numbers, their slots, 0 .. slots - 1 at most.
     int n_seg, seg_chunks, slots, mode;
     float *seg;         // [slots][Hv][da][dc]
+    int drop_chunk;     // test aid (gdn_debug_set_wait): a chunk that the tensor cores' kernel does not load, -1: none
 };
 
 // A sequence's first token (of its row of the batch), its tokens and chunks (offsets that fall or leave the T tokens: none),

@@ -75,6 +75,7 @@ Layout layout(const gdn_linear_problem *p, bool backward) {
 
 cudaError_t run(LinearRun r, const gdn_linear_problem *p, const Layout &l, unsigned char *ws, cudaStream_t st) {
     r.cu = p->cu_seqlens, r.B = (int)p->B, r.T = (int)p->T, r.Hv = (int)p->Hv, r.n_seqs = (int)p->n_seqs;
+    r.drop_chunk = debug_drop_chunk();
     r.n_seg = l.n_seg, r.seg_chunks = l.seg_chunks, r.slots = l.slots, r.seg = reinterpret_cast<float *>(ws + l.seg);
     auto launch = [&](int mode) {
         r.mode = mode;

@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
             if (j >= kStages && !wait_for(bar(EMPTY0 + st), (j / kStages - 1) & 1, abort_flag)) break;
             tail = tokens(j) < C;
             const uint32_t to = tail ? bar(TAIL) : bar(FULL0 + st), at = stage(j);
-            if (lane == 0) {
+            if (lane == 0 && j != r.drop_chunk) {
                 const int tok = token0(j);
                 mbar_arrive_expect_tx(to, bytes);
                 for (uint32_t x = 0; x < boxes_a; ++x) {
@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_linear_tc(const __grid_constant
         // never leave with copies in flight
         if (lane == 0) {
             for (int j = max(0, issued - kStages); j < issued; ++j) {
+                if (j == r.drop_chunk) continue;
                 if (j == nck - 1 && tail) mbar_drain(bar(TAIL), 0);
                 else mbar_drain(bar(FULL0 + j % kStages), (j / kStages) & 1);
             }

@@ -23,9 +23,12 @@
  *    on different streams with different workspaces are safe.
  *  - Arguments are validated on the host before anything is enqueued; a bad
  *    argument returns a status and enqueues nothing.  A failed launch returns
- *    GDN_ERR_CUDA.  Kernels that wait on an mbarrier give up after a bounded
- *    number of polls and record GDN_ERR_TIMEOUT in the workspace's error word;
- *    gdn_workspace_error() reads it back.
+ *    GDN_ERR_CUDA.  Kernels that wait on an mbarrier give up after a limit.
+ *    Those of gdn_fwd and gdn_bwd and their variants then record
+ *    GDN_ERR_TIMEOUT in the workspace's error word, which
+ *    gdn_workspace_error() reads back.  The decoding calls and linear attention
+ *    have no such word: what the wait concerns is NaN in their outputs and
+ *    states, and the status of the call and of later ones stays GDN_OK.
  *  - Shapes (B = batch, T = tokens per sequence, Hq = query/key heads,
  *    Hv = value heads, N = number of sequences):
  *        q, k            [B, T, Hq, K]   io dtype
@@ -500,8 +503,11 @@ gdn_status gdn_linear_bwd(const gdn_linear_problem *p, const void *q, const void
  * that load then expires: the kernel records GDN_ERR_TIMEOUT in the workspace
  * error word (read by gdn_workspace_error), waits for its own copies and
  * tensor-core operations in flight, frees its tensor memory and returns, and
- * the outputs of that call are incomplete.  Later calls on the same stream
- * run normally.  gdn_debug_set_wait(0, -1) restores the defaults.
+ * the outputs of that call are incomplete.  Linear attention's tensor-core
+ * kernel skips the load of that chunk in every sequence, or segment of one,
+ * that it takes; its limit stays a second, and its outputs and states are NaN
+ * where there was such a chunk.  Later calls on the same stream run normally.
+ * gdn_debug_set_wait(0, -1) restores the defaults.
  */
 void gdn_debug_set_wait(int64_t wait_ns, int32_t drop_load_chunk);
 
