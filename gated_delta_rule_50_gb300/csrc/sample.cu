@@ -37,7 +37,10 @@ constexpr int kMaxCluster = 8;
 constexpr int kOctave = 8, kBins = 44 * kOctave;  // w = 0 from t = -43 on
 constexpr int kSub = kThreads;
 constexpr int kList = 1024;
-constexpr int kSlice = 1 << 17;  // elements of a CTA, at most: then sums of a bin's 15-bit parts stay within 32 bits
+constexpr int kSlice = 1 << 17;  // elements of a CTA for which the next cluster size is taken
+// A slice has a few more where the longest row begins off a 16-byte boundary: a bin's sum of 14-bit parts, and of what w has
+// from bit 28 on, 2^14 at most, stays within 32 bits all the same
+static_assert((int64_t)kMaxCluster * kSlice >= GDN_SAMPLE_VOCAB_MAX && ((int64_t)(kSlice + 32) << 14) <= INT64_C(1) << 32, "sums of parts");
 constexpr int kCache = 96 << 10; // bytes of shared memory for the slice; larger ones are read again in every pass
 static_assert(kBins <= kThreads, "a thread per bin");
 constexpr int kShift = 42;
@@ -77,7 +80,7 @@ __device__ __forceinline__ uint64_t shfl_up64(uint64_t x, int d) { return __shfl
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int d) { return __shfl_xor_sync(~0u, (unsigned long long)x, d); }
 
 struct Shared {
-    uint32_t part[3][kSub];  // sums of w by bins, in three parts of 15 bits
+    uint32_t part[3][kSub];  // sums of w by bins, in parts: bits 0 .. 13, 14 .. 27, 28 ..
     uint32_t count[kSub];
     uint64_t total[kSub];    // of either, as whole numbers
     uint64_t key[kList], w[kList];
@@ -261,7 +264,7 @@ template <typename IO> struct Sampler {
     __device__ __forceinline__ void close_bins(bool by_count) {
         __syncthreads();
         const int i = threadIdx.x;
-        s.total[i] = by_count ? s.count[i] : ((uint64_t)s.part[2][i] << 30) + ((uint64_t)s.part[1][i] << 15) + s.part[0][i];
+        s.total[i] = by_count ? s.count[i] : ((uint64_t)s.part[2][i] << 28) + ((uint64_t)s.part[1][i] << 14) + s.part[0][i];
     }
     // Where in the bins (over the cluster; a thread for each) the running sum reaches `need`, of w or of tokens: at_bin
     // (kThreads: nowhere), what lies before it and in it, and how many tokens that are at most.  Bins of t only, where w was
@@ -296,9 +299,9 @@ template <typename IO> struct Sampler {
         __syncthreads();
     }
     __device__ __forceinline__ void add(int bin, uint64_t w) {
-        atomicAdd(&s.part[0][bin], (uint32_t)w & 0x7FFFu);
-        atomicAdd(&s.part[1][bin], (uint32_t)(w >> 15) & 0x7FFFu);
-        if (w >> 30) atomicAdd(&s.part[2][bin], (uint32_t)(w >> 30));
+        atomicAdd(&s.part[0][bin], (uint32_t)w & 0x3FFFu);
+        atomicAdd(&s.part[1][bin], (uint32_t)(w >> 14) & 0x3FFFu);
+        if (w >> 28) atomicAdd(&s.part[2][bin], (uint32_t)(w >> 28));
     }
     // Into the first CTA's list
     __device__ __forceinline__ void collect(uint64_t key) {
