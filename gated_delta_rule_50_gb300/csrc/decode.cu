@@ -3,7 +3,8 @@
 // Per row and value head, with a = e^g:  d = beta (v - a S^T k),  S' = a S + k d^T,  o = scale S'^T q.
 // Both products are taken from the state before the update, o = scale (a S^T q + (q.k) d), so one pass over
 // the state's registers serves k and q and a second one updates it.  Linear attention (DELTA false) is the same without the
-// correction, d = v, and with one a per head.
+// correction, d = v, and with one a per head, which every token meets, so that what a loses by its
+// rounding to fp32 would add up (3 % of a decay of 1e-6 a token): see advance().
 //
 // A warp holds a [K][32] tile of the state in registers: lane = (r, c) with c = 0..7 has the four columns
 // 4c .. 4c+3 of the rows 16 i + 4 r + j (K values of 32 bits per lane, K/4 accesses of 16 bytes, each a full
@@ -11,7 +12,7 @@
 // the four r lanes of a column group meet through shuffles.
 //
 // For one token the states' way through memory bounds the step (each is read and written once): 64 rows of 32 heads,
-// 128 x 128, bf16, take 45 us, 6.0 TB/s (linear attention 44, 6.2); one row 3.0 us, where reads, sums and writes wait for
+// 128 x 128, bf16, take 45 us, 6.0 TB/s (linear attention 43.5, 6.2); one row 3.0 us, where reads, sums and writes wait for
 // each other.  More tokens
 // on the same states take 53 us (3) and 74 us (6), where memory would take 41 and 42: each costs three multiply-adds per
 // element of the state and two reads of k, with seven or eight warps on an SM.  Two kernels share the arithmetic: k_recurrent, a warp per CTA and 32 columns, and k_recurrent_flow for
@@ -67,7 +68,7 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
 // Up to kTok tokens for COLS threads, one state column each
 template <int K, int COLS, typename IO> struct Stage {
     alignas(16) IO k[kTok<IO>][K], q[kTok<IO>][K], v[kTok<IO>][COLS];
-    float a[kTok<IO>], b[kTok<IO>];
+    float a[kTok<IO>], b[kTok<IO>];  // with the delta rule: e^g, beta
     int tok[kTok<IO>];
 };
 __device__ __forceinline__ float4 load4(const float *x) { return *reinterpret_cast<const float4 *>(x); }
@@ -75,6 +76,34 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *x) {
     const uint2 u = *reinterpret_cast<const uint2 *>(x);
     return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
                        __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void halves(uint64_t p, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Linear attention's a - 1, or a where that is below 1/2
+__device__ __forceinline__ float rest_of(float g) {
+    const float less = expm1f(g);
+    return less >= -0.5f ? less : expf(g);
 }
 
 // The threads of one head (tid = 0 .. COLS - 1, columns col0 + tid) and, for more than a warp, their barrier
@@ -86,6 +115,7 @@ template <int K, int COLS, typename IO, bool DELTA> struct Head {
     const IO *q, *k, *v;
     const float *g, *beta;
     IO *o;  // row out_row of this head, this thread's column
+    float log_a;  // of all tokens, without the delta rule
     int n, tid, bar;
     bool rows16;  // rows of q, k and v begin on 16-byte boundaries
 
@@ -95,8 +125,12 @@ template <int K, int COLS, typename IO, bool DELTA> struct Head {
         q = static_cast<const IO *>(a.q) + u.b * a.sq.batch + hq * a.sq.head;
         k = static_cast<const IO *>(a.k) + u.b * a.sk.batch + hq * a.sk.head;
         v = static_cast<const IO *>(a.v) + u.b * a.sv.batch + h * a.sv.head + col0 + tid;
-        g = a.g ? a.g + u.b * a.sg.batch + h * a.sg.head : nullptr;
-        beta = DELTA ? a.beta + u.b * a.sb.batch + h * a.sb.head : nullptr;
+        if constexpr (DELTA) {
+            g = a.g + u.b * a.sg.batch + h * a.sg.head;
+            beta = a.beta + u.b * a.sb.batch + h * a.sb.head;
+        } else {
+            log_a = a.g ? a.g[h * a.sg.head] : 0.f;
+        }
         o = a.o ? static_cast<IO *>(a.o) + (u.out_row * a.Hv + h) * a.V + col0 : nullptr;
     }
     __device__ __forceinline__ void sync() const {
@@ -146,15 +180,14 @@ template <int K, int COLS, typename IO, bool DELTA> struct Head {
 #pragma unroll 4
             for (int t = 0; t < m; ++t) s.v[t][tid] = v[token(t) * a.sv.token];
         }
-        if (tid < m) {
-            s.a[tid] = DELTA || g ? expf(g[token(tid) * a.sg.token]) : 1.f;
-            if constexpr (DELTA) s.b[tid] = beta[token(tid) * a.sb.token];
+        if (DELTA && tid < m) {
+            s.a[tid] = expf(g[token(tid) * a.sg.token]), s.b[tid] = beta[token(tid) * a.sb.token];
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         return m;
     }
-    // m staged tokens, the first of them the t0-th of the row
-    __device__ __forceinline__ void advance(float4 (&S)[NR], int t0, int m) const {
+    // m staged tokens, the first of them the t0-th of the row; without the delta rule, the decay as run() has it
+    __device__ __forceinline__ void advance(float4 (&S)[NR], int t0, int m, float one_a, float rest) const {
         const int lane = tid & 31, c = lane & 7, r = lane >> 3;
         const int col = (tid & ~31) + 4 * c + r;  // the column whose sums this lane gets
 #pragma unroll 1
@@ -186,7 +219,7 @@ template <int K, int COLS, typename IO, bool DELTA> struct Head {
                     }
                 }
             }
-            const float al = s.a[t];
+            const float al = DELTA ? s.a[t] : one_a;
             float d = to_f<IO>(s.v[t][col]);
             if constexpr (DELTA) d = s.b[t] * (d - al * reduce_columns(ks, r));
             if (o) {
@@ -197,27 +230,53 @@ template <int K, int COLS, typename IO, bool DELTA> struct Head {
             float dj[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) dj[j] = __shfl_sync(~0u, d, c + 8 * j);
+            if constexpr (DELTA) {
 #pragma unroll
-            for (int i = 0; i < K / 16; ++i) {
-                const float4 kk = load4(s.k[t] + 16 * i + 4 * r);
-                const float kj[4] = {kk.x, kk.y, kk.z, kk.w};
+                for (int i = 0; i < K / 16; ++i) {
+                    const float4 kk = load4(s.k[t] + 16 * i + 4 * r);
+                    const float kj[4] = {kk.x, kk.y, kk.z, kk.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float4 &x = S[4 * i + j];
-                    x.x = fmaf(kj[j], dj[0], al * x.x);
-                    x.y = fmaf(kj[j], dj[1], al * x.y);
-                    x.z = fmaf(kj[j], dj[2], al * x.z);
-                    x.w = fmaf(kj[j], dj[3], al * x.w);
+                    for (int j = 0; j < 4; ++j) {
+                        float4 &x = S[4 * i + j];
+                        x.x = fmaf(kj[j], dj[0], al * x.x);
+                        x.y = fmaf(kj[j], dj[1], al * x.y);
+                        x.z = fmaf(kj[j], dj[2], al * x.z);
+                        x.w = fmaf(kj[j], dj[3], al * x.w);
+                    }
                 }
+                continue;
             }
+            const uint64_t d01 = pair_of(dj[0], dj[1]), d23 = pair_of(dj[2], dj[3]), f2 = pair_of(rest, rest);
+            auto update = [&](auto one) {
+#pragma unroll
+                for (int i = 0; i < K / 16; ++i) {
+                    const float4 kk = load4(s.k[t] + 16 * i + 4 * r);
+                    const float kj[4] = {kk.x, kk.y, kk.z, kk.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float4 &x = S[4 * i + j];
+                        const uint64_t k2 = pair_of(kj[j], kj[j]);
+                        halves(one(pair_of(x.x, x.y), k2, d01), x.x, x.y);
+                        halves(one(pair_of(x.z, x.w), k2, d23), x.z, x.w);
+                    }
+                }
+            };
+            // a below 1/2: a S as it is.  Above, (a - 1) S + S in one rounding, unbiased where S moves by many of its steps; a
+            // decay of less than 2^-10 is summed with k d first, for S + (a - 1) S alone is S again where (a - 1) S is less than
+            // half a step of S.  That costs three operations for two: 96 lists of 6 tokens, 64 heads
+            // 204 us instead of 188
+            if (rest == al) update([&](uint64_t x, uint64_t k, uint64_t d) { return fma2(k, d, mul2(f2, x)); });
+            else if (rest == 0.f || fabsf(rest) >= 0x1p-10f) update([&](uint64_t x, uint64_t k, uint64_t d) { return fma2(k, d, fma2(f2, x, x)); });
+            else update([&](uint64_t x, uint64_t k, uint64_t d) { return add2(x, fma2(k, d, mul2(f2, x))); });
         }
     }
     // The row from its first m tokens, which all threads see in the stage, to its end; whether the new state is to be
     // kept
     __device__ __forceinline__ bool run(float4 (&S)[NR], int m, bool more, bool bad) const {
         int t0 = 0;
+        const float one_a = DELTA ? 0.f : expf(log_a), rest = DELTA ? 0.f : rest_of(log_a);
         for (;;) {
-            advance(S, t0, m);
+            advance(S, t0, m, one_a, rest);
             t0 += m;
             if (!more || t0 >= u.len) break;
             sync();
@@ -335,9 +394,9 @@ __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_c
         }
         x.tok = at;
         x.g = x.beta = 0.f;
-        if (lane < x.m) {
-            if (DELTA || a.g) x.g = a.g[x.u.b * a.sg.batch + x.h * a.sg.head + x.tok * a.sg.token];
-            if constexpr (DELTA) x.beta = a.beta[x.u.b * a.sb.batch + x.h * a.sb.head + x.tok * a.sb.token];
+        if (DELTA && lane < x.m) {
+            x.g = a.g[x.u.b * a.sg.batch + x.h * a.sg.head + x.tok * a.sg.token];
+            x.beta = a.beta[x.u.b * a.sb.batch + x.h * a.sb.head + x.tok * a.sb.token];
         }
         return x;
     };
@@ -345,7 +404,7 @@ __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_c
         const int slot = i % F::slots, hq = x.h / a.G;
         const uint32_t at = smem_u32(sm) + slot * F::slot_bytes, bar_f = full + 8 * slot;
         const bool live = x.u.valid && x.u.slot >= 0 && x.u.slot < a.n_slots;
-        if (lane < x.m) info[slot].a[lane] = expf(x.g), info[slot].b[lane] = x.beta;
+        if (DELTA && lane < x.m) info[slot].a[lane] = expf(x.g), info[slot].b[lane] = x.beta;
         __syncwarp();
         if (lane == 0) {
             info[slot].m = x.m, info[slot].more = x.more, info[slot].bad = x.bad;
@@ -420,7 +479,7 @@ __global__ void __launch_bounds__(2 * kGroup, 1) k_recurrent_flow(const __grid_c
             }
             const IO *raw_v = reinterpret_cast<const IO *>(raw + 2 * AHEAD * ROW) + tid;
             for (int t = 0; t < m; ++t) s.v[t][tid] = raw_v[t * V];
-            if (tid < m) s.a[tid] = info[slot].a[tid], s.b[tid] = info[slot].b[tid];
+            if (DELTA && tid < m) s.a[tid] = info[slot].a[tid], s.b[tid] = info[slot].b[tid];
             alive = named_bar_and(bar, V, ok);
             if (alive && tid < 32 && next < heads) fetch(i + F::slots, ahead);
         }
