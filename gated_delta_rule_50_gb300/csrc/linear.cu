@@ -85,7 +85,8 @@ template <typename IO, int DA, bool VEC> __global__ void __launch_bounds__(kThre
     int seq, part;
     const LinearSpan span = linear_place(r, slot, seq, part);
     if (seq < 0) return;
-    const int from = part * span.per_seg * C, to = min(span.tokens, (part + 1) * span.per_seg * C);
+    const LinearPart range = linear_part(span.tokens, span.chunks, span.per_seg, part);
+    const int from = range.from, to = range.to;
     const int64_t unit = (int64_t)seq * r.Hv + h, words = (int64_t)DA * r.dc;
     const float *init = r.init ? r.init + unit * words : nullptr;
     float *fin = r.fin ? r.fin + unit * words : nullptr, *seg = r.seg + ((int64_t)slot * r.Hv + h) * words;

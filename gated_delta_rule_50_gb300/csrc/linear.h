@@ -62,6 +62,15 @@ __device__ __forceinline__ LinearSpan linear_span(const LinearRun &r, int s) {
     x.slot = s * r.n_seg, x.segs = x.per_seg ? (x.chunks + x.per_seg - 1) / x.per_seg : 1;
     return x;
 }
+// The tokens [from, to) of a sequence that its segment `part` takes: whole chunks, the last one's rest, none behind it.  By
+// chunks, for (part + 1) per_seg C passes 2^31 where a sequence nearly has as many tokens
+struct LinearPart {
+    int from, to;
+};
+__host__ __device__ inline LinearPart linear_part(int tokens, int chunks, int per_seg, int part) {
+    const int first = part * per_seg, c0 = first < chunks ? first : chunks, c1 = per_seg < chunks - c0 ? c0 + per_seg : chunks;
+    return {c0 < chunks ? c0 * C : tokens, c1 < chunks ? c1 * C : tokens};
+}
 // Packed sequences: lane s has the s-th one's, and their slots follow each other by the segments' lengths, the longest first,
 // so that a long one does not begin when the others are done.  A whole warp
 __device__ __forceinline__ bool linear_packed(const LinearRun &r) { return r.cu && r.n_seqs > 1 && r.n_seqs <= 32; }
