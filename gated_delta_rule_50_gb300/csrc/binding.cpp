@@ -170,6 +170,7 @@ struct Decode {
             shaped(beta, "beta", {p.B, p.T, p.Hv}, dev);
         } else if (g.defined()) {
             shaped(g, "g", {p.Hv}, dev);
+            if (c10::isComplexType(g.scalar_type())) type_error("g must hold real numbers");
         }
         if (v.scalar_type() != k.scalar_type() || (q.defined() && q.scalar_type() != k.scalar_type()))
             type_error("q, k and v must have one dtype");
