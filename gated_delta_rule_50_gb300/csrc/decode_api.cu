@@ -165,7 +165,7 @@ gdn_status gdn_sample(const gdn_sample_problem *p, const void *logits, const flo
                       float *logprobs, gdn_stream_t stream) {
     if (!p || p->B < 0 || p->vocab < 1) return GDN_ERR_INVALID_ARG;
     if (p->logits_dtype != GDN_F32 && p->logits_dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
-    if (p->vocab > GDN_SAMPLE_VOCAB_MAX || p->B > (1 << 20)) return GDN_ERR_UNSUPPORTED;
+    if (p->vocab > GDN_SAMPLE_VOCAB_MAX || p->B > GDN_SAMPLE_ROWS_MAX) return GDN_ERR_UNSUPPORTED;
     if (p->B == 0) return GDN_OK;
     if (!logits || !u || !tokens) return GDN_ERR_INVALID_ARG;
     if (!aligned(logits, p->logits_dtype == GDN_BF16 ? 2 : 4) || !aligned(u, 4) || !aligned(tokens, 4) ||

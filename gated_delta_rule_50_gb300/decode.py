@@ -129,9 +129,9 @@ def sample_tokens(logits: torch.Tensor, random: torch.Tensor, temperature: Union
                   min_p: Union[float, torch.Tensor, None] = None, mask: Optional[torch.Tensor] = None):
     """One token for each row, drawn with a given random number: (tokens int32 [B], logprobs fp32 [B]).
 
-    logits [B,vocab] (bf16 or fp32, the vocabulary contiguous); random [B] fp32 in [0, 1); temperature, top_k, top_p and
-    min_p are numbers or tensors [B], one for each row; mask bool, broadcastable to logits: False forbids a token,
-    whatever its logit holds.
+    logits [B,vocab] (bf16 or fp32, the vocabulary contiguous, B and vocab up to 2^20); random [B] fp32 in [0, 1);
+    temperature, top_k, top_p and min_p are numbers or tensors [B], one for each row; mask bool, broadcastable to logits:
+    False forbids a token, whatever its logit holds.
 
     Of the allowed tokens, best first and equal ones by the lower token, the ``top_k`` first are kept (0 or below: all);
     of these, with shares softmax(logits / temperature), the fewest whose shares sum to ``top_p`` at least (1 or above:

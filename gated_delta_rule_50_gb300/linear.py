@@ -15,7 +15,8 @@ those of ``chunk_gated_delta_rule``, so that both kinds of layers share a model'
                                    T tokens counts as empty; rows outside every sequence are 0 in all outputs
 
 A NaN or an infinity in a token reaches the outputs of its sequence's chunk of 64 tokens and of what comes behind it, and no
-other sequence.
+other sequence.  The gradients of k, v and the initial state run from the last token to the first: there it reaches the chunk,
+counted from the sequence's end, and what comes before it.
 
 The calls go through the extension module (``csrc/binding.cpp``), synchronise nothing and read nothing back, so that they can be
 captured in a CUDA graph.

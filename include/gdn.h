@@ -432,9 +432,11 @@ gdn_status gdn_linear_recurrent(const gdn_decode_problem *p, const void *q, cons
  * Parameters are given for each row (fp32 or int32 [B] on the device) or, with
  * a NULL pointer, once for all rows.  Shares are whole numbers of 2^-42 of the
  * best one's: smaller ones are never drawn, and no sum depends on an order.
+ *   Up to GDN_SAMPLE_ROWS_MAX rows of up to GDN_SAMPLE_VOCAB_MAX tokens; more
+ * are GDN_ERR_UNSUPPORTED.
  */
 typedef struct {
-    int64_t B, vocab;                       /* vocab <= GDN_SAMPLE_VOCAB_MAX                     */
+    int64_t B, vocab;
     int64_t logits_row, mask_row;           /* strides in elements and bytes; mask_row 0: shared */
     gdn_dtype logits_dtype;
     const float *temperatures, *top_ps, *min_ps;
@@ -443,6 +445,7 @@ typedef struct {
     int32_t top_k;
 } gdn_sample_problem;
 #define GDN_SAMPLE_VOCAB_MAX (1 << 20)
+#define GDN_SAMPLE_ROWS_MAX (1 << 20)
 
 /* u [B] fp32, mask bytes (nullable) -> tokens int32 [B], logprobs fp32 [B] (nullable). */
 gdn_status gdn_sample(const gdn_sample_problem *p, const void *logits, const float *u, const uint8_t *mask,
@@ -466,11 +469,14 @@ gdn_status gdn_sample(const gdn_sample_problem *p, const void *logits, const flo
  * Neither call synchronises or allocates; both can be captured in a graph.
  * Waits of the kernels are bounded (a second); where one ran out, the outputs
  * and the states that it concerns are NaN.
- * The sequences are split over the GPU where they are few, and joined exactly.
+ * The sequences are split over the GPU where they are few, and joined without
+ * approximation, in fp32.
  * bf16 whose pointers and strides are multiples of 16 bytes above 0: the tensor
  * cores' kernels; the rest and fp32: the CUDA cores'.  A token that is not
  * finite reaches those of its own chunk before it, and all that follow it in its
- * sequence, none of another sequence.
+ * sequence, none of another sequence.  The gradients of k, v and h0 run from the
+ * last token to the first: there it reaches those of its own chunk, counted
+ * from the sequence's end, and all that are before it; dq is as o.
  */
 typedef struct {
     int64_t B, T, Hq, Hv, K, V;    /* K, V in {64, 128}; Hv % Hq == 0; Hv <= 16383; B T < 2^31  */
