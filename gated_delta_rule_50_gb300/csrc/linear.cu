@@ -5,8 +5,9 @@
 // tokens with the state [da][64] in shared memory: P = (A B^T) under the decays, O = P C + l^(j + e) A X,
 // X <- l^n X + (w B)^T C.  All in fp32, two at a time; the next block's rows come under a block's work.  Reads of shared
 // memory bound it: 16 products for every two 16-byte reads of a thread's 4 x 4 tile, with eight warps on an SM (two times
-// eight at 64 x 64).  A block takes 9 us at 64 x 64 and 15 at 128 x 128, 0.23 and 0.25 TFLOP/s an SM of 0.49; 4 x 1024
-// tokens of 16 heads, 128 x 128, 241 us; 2 x 1000 of 8 heads, 64 x 64, 35 us (in segments of one block).
+// eight at 64 x 64).  A block takes 9 us at 64 x 64 and 14 at 128 x 128, 0.23 and 0.26 TFLOP/s an SM of 0.49; 4 x 1024
+// tokens of 16 heads, 128 x 128, 227 us; 2 x 1000 of 8 heads, 64 x 64, 34 us (in segments of one block).  Two CTAs an SM are
+// asked for at 64: with 160 registers, which the compiler takes otherwise, one fits, and those 34 us are 42.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -33,7 +33,7 @@ gdn_status problem_ok(const gdn_linear_problem *p) {
 // each is cut so that they fill them.  Every token's part in the state is then taken twice, and there are two launches more.
 // Measured on the tensor cores, us: 2.2 a chunk and 6 for whole ones, 1.5 + 2.2 a chunk of a segment and 16 for cut ones.
 // On the CUDA cores a head is a CTA for every 64 columns of V, of which an SM holds two where K is 64, and one where it is
-// 128; a chunk takes 9 us (64 x 64) to 15 (128 x 128), its part in the state some 0.6 of that, the launches and the join as
+// 128; a chunk takes 9 us (64 x 64) to 14 (128 x 128), its part in the state some 0.6 of that, the launches and the join as
 // much as a chunk.  (2 x 1000 tokens, 8 heads: 64 x 64 146 us whole and 35 cut, 128 x 128 236 and 90; 1 x 200: 35 and 29, 56
 // and 31; near the border 4 x 300 of 24 heads, 64 x 64, gain 22 % forward and lose 18 % backward.)
 int segments(const gdn_linear_problem *p) {
@@ -58,7 +58,10 @@ Layout layout(const gdn_linear_problem *p, bool backward) {
     l.slots = (int)(p->n_seqs * l.n_seg);
     // Packed sequences may be of any lengths, which are not known here.  Where one that had all the tokens would take much
     // longer than these shared evenly, what is longer than half of an SM's share is cut.  (13 sequences, one with two
-    // fifths of 10007 tokens, 32 heads: 175 us as they are; where none is cut, this costs two launches, some 10 us.)
+    // fifths of 10007 tokens, 32 heads: 175 us as they are and 158 cut; where none is cut, this costs two launches, some 10 us.)
+    // Up to 32 sequences, for the table has a lane for each, and up to four heads an SM.  What that costs beyond, one
+    // sequence of 8192 tokens among others of 100, the sequences' number times heads: 19 x 32 181 us and 20 x 32 250, 32 x 8
+    // 97 and 33 x 8 229.
     const int64_t chains = p->n_seqs * p->Hv, chunks = (p->T + C - 1) / C;
     if (p->cu_seqlens && l.n_seg == 1 && p->n_seqs > 1 && p->n_seqs <= 32 && chains <= 4 * kSMs) {
         const int64_t even = (chunks * p->Hv + kSMs - 1) / kSMs;

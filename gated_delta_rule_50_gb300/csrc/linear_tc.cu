@@ -24,12 +24,13 @@
 //     U(j), P(j + 1), I(j), O(j)
 // and the others follow them: w c while I(j - 1) and O(j - 1) run, U, X and out from I(j - 1)'s end on, P~(j + 1) until O(j + 1).
 //
-// 4 sequences of 4096 tokens, 32 heads of 128 x 128 on 16 of q and k, with their final states: 126 us (112 without them),
-// 3.3 TB/s; 2.0 us a chunk, 1.4 where only the state is wanted.  What bounds it is the products in their order: without any
-// conversion and without out 100 us are left, of which the 40 products of a chunk take 2600 to 2900 of 3000 cycles at the
-// rates that they have alone (w c with b across rows 89 cycles, the others 46 to 77, where 32 would be full rate); the tensor
-// pipe counts 49 % as active.  The conversions read and write the shared memory from which the operands come, and slow them
-// down to 3800 cycles a chunk.  Chunks of 64: half of P's rows and of P~ are not used, at 128 it would be as much of O.
+// 4 sequences of 4096 tokens, 32 heads of 128 x 128 on 16 of q and k, with their final states: 123 us (112 without them),
+// 3.3 TB/s; 1.9 us a chunk, 1.4 where only the state is wanted.  What bounds it is the products in their order: without any
+// conversion and without out 100 us are left, of which the 44 products of a chunk (40 without a third part of w c) take 2600 to
+// 2900 of 3000 cycles at the rates that they have alone (w c with b across rows 89 cycles, the others 46 to 77, where 32 would be full rate); the tensor
+// pipe counts 50 % as active.  The conversions read and write the shared memory from which the operands come, and slow them
+// down to 3800 cycles a chunk.  Chunks of 64: half of P's rows and of P~ are not used, at 128 it would be as much of O; and
+// three stages of 128 tokens are 288 KB, where two of 64 already cost a third of the speed.
 // Two stages instead of three: 241 -> 330 us (2 x 8192 tokens, 64 heads).  28 warps instead of 16, products issued by two
 // warps, out and I in one accumulator: within 3 % of this.
 #include <cuda.h>
